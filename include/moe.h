@@ -325,6 +325,167 @@ int moe_router_fwd(const moe_desc* d, const float* logits, int32_t* topk_idx, fl
 int moe_router_bwd(const moe_desc* d, const int32_t* topk_idx, const float* topk_w,
                    const float* dtopk_w, float* dlogits, void* stream);
 
+/* Load-balancing loss of the router, its z-loss and the per-expert counts (what
+ * trains the router to spread the tokens that the layer then sorts: Prime Mega
+ * MoE news item, "Why is MoE training communication-bound?").  With V the
+ * tokens t whose valid[t] is not 0 (all T of them when `valid` is NULL), n = |V|,
+ * p_t = softmax(logits_t) and lse_t = log sum_e exp(logits_te):
+ *   counts[e]  = #{(t,k) : t in V, topk_idx[t,k] = e}, and counts[E] = n;
+ *   mean_p[e]  = (1/n) sum_{t in V} p_te;
+ *   losses[0]  = E sum_e f_e mean_p[e] with f_e = counts[e] / (n K) (1 for equal
+ *                shares, whatever K), losses[1] = (1/n) sum_{t in V} lse_t^2.
+ * With n = 0 mean_p and losses are 0.  Ids outside [0, E) are not counted; logits and
+ * ids of tokens outside V are not read.  A token of V with a NaN, a +inf or
+ * only -inf logits makes mean_p and losses NaN, as the definition does (one
+ * -inf is an expert of probability 0).
+ * Reads only T, E, K of `d`: T >= 0, 1 <= K <= E, T*K < 2^31 (else MOE_EINVAL),
+ * E <= 1024 (else MOE_EUNSUPPORTED).  logits: device float32 [T, E];
+ * topk_idx: device int32 [T, K] (moe_router_fwd's); valid: device uint8 [T] or
+ * NULL; counts: device int32 [E+1]; mean_p: device float32 [E]; losses: device
+ * float32 [2]; all 4-byte aligned (MOE_EALIGN), `valid` of any alignment.
+ * scratch: device, 16-byte aligned, scratch_bytes >= moe_balance_scratch_bytes(d)
+ * (MOE_ESCRATCH), used only during the call.  With T = 0 logits, topk_idx may
+ * be NULL; counts, mean_p and losses are written (zeros).  The sums have a
+ * fixed order: the same inputs give the same bits.  Asynchronous on `stream`;
+ * allocates nothing. */
+size_t moe_balance_scratch_bytes(const moe_desc* d);
+int moe_balance_fwd(const moe_desc* d, const float* logits, const int32_t* topk_idx,
+                    const uint8_t* valid, int32_t* counts, float* mean_p, float* losses,
+                    void* scratch, size_t scratch_bytes, void* stream);
+
+/* Gradient of dlosses[0] * losses[0] + dlosses[1] * losses[1] with respect to
+ * the logits (counts do not depend on them): for t in V
+ *   dlogits[t,j] = p_tj (dlosses[0] (E/n) (f_j - sum_e f_e p_te)
+ *                        + dlosses[1] (2/n) lse_t),
+ * and 0 for the other tokens.  With topk_idx, topk_w and dtopk_w (all three, or
+ * all NULL: else MOE_EINVAL) moe_router_bwd's gradient is added to every token,
+ * so that the router's whole backward is one pass; this needs K <= 64
+ * (MOE_EUNSUPPORTED).  counts: moe_balance_fwd's [E+1] (a job of several ranks
+ * may sum them over the ranks in between: f and n are taken from it, n from
+ * counts[E]); dlosses: device float32 [2]; dlogits: device float32 [T, E], every
+ * entry written, not `logits` itself.  Other requirements as moe_balance_fwd.  With T = 0 it returns
+ * MOE_OK and touches nothing. */
+int moe_balance_bwd(const moe_desc* d, const float* logits, const uint8_t* valid,
+                    const int32_t* counts, const float* dlosses, const int32_t* topk_idx,
+                    const float* topk_w, const float* dtopk_w, float* dlogits, void* stream);
+
+/* Element types and scale layouts of the block-scaled calls below. */
+enum moe_type { MOE_TYPE_F32 = 0, MOE_TYPE_BF16 = 1, MOE_TYPE_E4M3 = 2 };
+enum moe_scale { MOE_SCALE_TILE = 0, MOE_SCALE_BLOCK = 1 };
+
+/* Dense e4m3 operands with one fp32 scale for each block of 128: the layer's
+ * blockwise FP8 recipe (Prime Mega MoE news item, "How does the fused kernel
+ * work?") for the linear layers beside the experts.  A matrix [R, C] is stored
+ * as codes [R, ld] (ld >= C, a multiple of 16) and
+ *   MOE_SCALE_TILE   a scale for each 1 x 128 run of a row: [ceil(C/128), R]
+ *                    (one row of scales per step of 128 columns);
+ *   MOE_SCALE_BLOCK  a scale for each 128 x 128 block: [ceil(R/128), ceil(C/128)].
+ * Its last runs and blocks may be partial.  scale = amax / 448 (fp32 division; 1
+ * where that is 0), code = e4m3(x / scale) of the fp32 quotient, to nearest even,
+ * saturating at 448; the value is code * scale.  A NaN keeps its code NaN, and
+ * an infinity makes its run or block NaN. */
+typedef struct moe_block_quant_desc {
+  int32_t rows, cols;
+  int32_t in_type;     /* MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  int32_t scale;       /* enum moe_scale */
+  int64_t ld_in;       /* elements between rows of x, >= cols */
+  int64_t ld_codes;    /* bytes between rows of codes, >= cols, % 16 == 0 */
+  int64_t ld_codes_t;  /* bytes between rows of codes_t, >= rows, % 16 == 0 */
+} moe_block_quant_desc;
+
+/* Quantises x [rows, cols] in one pass into either orientation or both:
+ *   codes [rows, ld_codes] with scales as above, and
+ *   codes_t [cols, ld_codes_t], the transpose: with MOE_SCALE_TILE its own tiles
+ *   run along the rows of x (the operand of a product contracted over them, a
+ *   weight gradient's), with scales_t [ceil(rows/128), cols]; with
+ *   MOE_SCALE_BLOCK the same codes, with scales_t [ceil(cols/128), ceil(rows/128)].
+ * A pair (codes, scales) or (codes_t, scales_t) is left out by passing both as
+ * NULL; one of a pair alone, or neither pair, is MOE_EINVAL, as are negative
+ * sizes, types other than those above and row strides that are too small.
+ * The bytes of a row of codes from its last column to the next multiple of 16
+ * are written 0; those behind them are left as they were.  codes and codes_t
+ * 16-byte aligned, their strides multiples of 16, scales 4-byte, x aligned to its element
+ * (MOE_EALIGN).  A stride of 2^22 or more, or scales or tiles past 2^31 bytes or
+ * launches, are MOE_EUNSUPPORTED.  An empty matrix is MOE_OK and touches
+ * nothing.  Asynchronous on `stream`; allocates nothing. */
+int moe_block_quant(const moe_block_quant_desc* q, const void* x, uint8_t* codes, float* scales,
+                    uint8_t* codes_t, float* scales_t, void* stream);
+
+/* Add the product to C instead of overwriting it (c_type MOE_TYPE_F32 only). */
+#define MOE_MM_ACCUMULATE 0x1
+
+typedef struct moe_block_mm_desc {
+  int32_t M, N, K;
+  int32_t a_type;      /* MOE_TYPE_E4M3 codes, or F32 / BF16: quantised by the call */
+  int32_t b_scale;     /* enum moe_scale of b; a has MOE_SCALE_TILE */
+  int32_t c_type;      /* MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  int32_t flags;       /* MOE_MM_* */
+  int64_t lda, ldb;    /* elements between rows; of codes % 16 == 0 */
+  int64_t ldc;
+} moe_block_mm_desc;
+
+/* C [M, N] (+)= A B^T for A [M, K] and B [N, K] as above, both with the
+ * contraction along their rows: the forward product y = x W^T (b: W's codes),
+ * its input gradient dx = dy W (b: W's codes_t) and its weight gradient
+ * dW = dy^T x (a, b: the codes_t of dy and x, b_scale MOE_SCALE_TILE, K tokens).
+ * A run of 128 products is summed by the matrix core, multiplied by both scales
+ * and added over the runs in fp32; C is rounded once.  With c_type F32 the products are
+ * exact and every sum is fp32's; with BF16 the run's sums are the e4m3 matrix
+ * instruction's, which drops what lies 13 bits below the largest of eight
+ * products (about 1.5e-5 of a result, against bf16's own 2e-3).  With a_type F32 or BF16
+ * `a` holds the values, a_scales is NULL and the call quantises them as
+ * moe_block_quant would, with the same result.  Codes behind column K are not
+ * used.  Padding of C's rows (ldc > N) is left as it was.
+ * K = 0 gives C = 0 (or C as it was, with MOE_MM_ACCUMULATE); M = 0 or N = 0 is
+ * MOE_OK and touches nothing.  a, b (codes) 16-byte aligned; values, C and
+ * scales aligned to their element (MOE_EALIGN); scratch 16-byte aligned, of
+ * moe_block_mm_scratch_bytes(m) (MOE_ESCRATCH; 0 bytes: it may be NULL), used only
+ * during the call.  MOE_EINVAL for null pointers, negative sizes, bad types or
+ * flags and strides that are too small; MOE_EUNSUPPORTED for strides of 2^22 or more
+ * (lda, ldb) or scales past 2^31 bytes; moe_block_mm_scratch_bytes is then 0.
+ * The order of the sums depends on the sizes alone: the same inputs give
+ * the same bits.  Asynchronous on `stream`; allocates nothing. */
+size_t moe_block_mm_scratch_bytes(const moe_block_mm_desc* m);
+int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scales,
+                 const uint8_t* b, const float* b_scales, void* c, void* scratch,
+                 size_t scratch_bytes, void* stream);
+
+/* One gradient of a list: n elements at src (device, aligned to its element),
+ * and where moe_grad_clip writes them, dst (src itself, or memory that no src
+ * and no other dst of the list overlaps).  moe_grad_norm does not use dst. */
+typedef struct moe_grad {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t type; /* MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  int32_t reserved; /* 0 */
+} moe_grad;
+
+/* Global L2 norm of a list of gradients, what follows moe_bwd in a training
+ * step (its dw1 and dw2, the router's gradient, ...):
+ *   norm[0] = sqrt(sum over the list of x^2), squares and sums in 64 bits, rounded
+ * to fp32 (inf past its range; NaN with any NaN; 0 for an empty list).
+ * `g` is a host array of `count` entries, read during the call only.  norm:
+ * device float32 [1].  scratch: device, 16-byte aligned, of
+ * moe_grad_scratch_bytes(count) (MOE_ESCRATCH), used only during the call.
+ * MOE_EINVAL for null pointers, count < 0, n < 0, a bad type or reserved != 0
+ * (MOE_EUNSUPPORTED for n >= 2^34); an entry with n = 0 may have null pointers.  The order of the sum depends on the
+ * list's lengths, types and alignments alone.  Asynchronous on `stream`; allocates
+ * no device memory. */
+size_t moe_grad_scratch_bytes(int32_t count);
+int moe_grad_norm(const moe_grad* g, int32_t count, float* norm, void* scratch,
+                  size_t scratch_bytes, void* stream);
+
+/* dst = src * c for every entry of the list, with c = 1 where norm[0] <= max_norm
+ * and max_norm / norm[0] elsewhere (a NaN norm makes everything NaN, an infinite
+ * one 0, or NaN where src is not finite); the product is fp32, rounded once.
+ * norm is read on the GPU when the call runs (moe_grad_norm's, or that of
+ * several ranks together).  max_norm >= 0 and finite (MOE_EINVAL).  Where dst is src
+ * and c is 1 nothing is written.  Overlapping memory as described at moe_grad is
+ * MOE_EINVAL.  Other requirements as moe_grad_norm. */
+int moe_grad_clip(const moe_grad* g, int32_t count, const float* norm, float max_norm,
+                  void* stream);
+
 /* Synchronizes `stream`, returns the latched device error (MOE_OK, MOE_EINDEX
  * or MOE_ETIMEOUT) of `scratch` and clears it.  Error reporting of this
  * library (the pages define no error interface): the descriptor and scratch

@@ -27,17 +27,38 @@ MOE_NOALLOC_SCRATCH_BYTES = 256 << 20
  MOE_VIEW_DXPERM, MOE_VIEW_WPERM, MOE_VIEW_Q_ROWS, MOE_VIEW_Q_ROWS_SCALE, MOE_VIEW_Q_TOK_A,
  MOE_VIEW_Q_TOK_A_SCALE, MOE_VIEW_Q_TOK_B, MOE_VIEW_Q_TOK_B_SCALE, MOE_VIEW_QUEUE) = range(15)
 
+MOE_TYPE_F32, MOE_TYPE_BF16, MOE_TYPE_E4M3 = range(3)
+MOE_SCALE_TILE, MOE_SCALE_BLOCK = range(2)
+MOE_MM_ACCUMULATE = 0x1
+
 # Exported symbols, in the order include/moe.h declares them.
 EXPORTS = (
     "moe_scratch_bytes", "moe_wprep_bytes", "moe_prepare_weights", "moe_route",
     "moe_routing_view", "moe_scratch_view", "moe_fwd", "moe_bwd", "moe_fwd_noalloc", "moe_router_fwd",
-    "moe_router_bwd", "moe_check", "moe_strerror", "moe_abi_version", "moe_profile_enable", "moe_profile_collect",
+    "moe_router_bwd", "moe_balance_scratch_bytes", "moe_balance_fwd", "moe_balance_bwd", "moe_block_quant",
+    "moe_block_mm_scratch_bytes", "moe_block_mm", "moe_grad_scratch_bytes", "moe_grad_norm", "moe_grad_clip",
+    "moe_check", "moe_strerror", "moe_abi_version", "moe_profile_enable", "moe_profile_collect",
     "moe_profile_get", "moe_profile_reset",
 )
 
 
 class moe_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "F", "E", "K", "mode", "flags")]
+
+
+class moe_block_quant_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "cols", "in_type", "scale")] + \
+               [(n, ctypes.c_int64) for n in ("ld_in", "ld_codes", "ld_codes_t")]
+
+
+class moe_block_mm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "a_type", "b_scale", "c_type", "flags")] + \
+               [(n, ctypes.c_int64) for n in ("lda", "ldb", "ldc")]
+
+
+class moe_grad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -70,6 +91,15 @@ def lib() -> ctypes.CDLL:
             "moe_fwd_noalloc": (_i32, [_dp] + [_vp] * 8),
             "moe_router_fwd": (_i32, [_dp, _vp, _vp, _vp, _vp]),
             "moe_router_bwd": (_i32, [_dp, _vp, _vp, _vp, _vp, _vp]),
+            "moe_balance_scratch_bytes": (_sz, [_dp]),
+            "moe_balance_fwd": (_i32, [_dp] + [_vp] * 7 + [_sz, _vp]),
+            "moe_balance_bwd": (_i32, [_dp] + [_vp] * 9),
+            "moe_block_quant": (_i32, [ctypes.POINTER(moe_block_quant_desc)] + [_vp] * 6),
+            "moe_block_mm_scratch_bytes": (_sz, [ctypes.POINTER(moe_block_mm_desc)]),
+            "moe_block_mm": (_i32, [ctypes.POINTER(moe_block_mm_desc)] + [_vp] * 6 + [_sz, _vp]),
+            "moe_grad_scratch_bytes": (_sz, [_i32]),
+            "moe_grad_norm": (_i32, [ctypes.POINTER(moe_grad), _i32, _vp, _vp, _sz, _vp]),
+            "moe_grad_clip": (_i32, [ctypes.POINTER(moe_grad), _i32, _vp, ctypes.c_float, _vp]),
             "moe_check": (_i32, [_dp, _vp, _sz, _vp]),
             "moe_strerror": (ctypes.c_char_p, [_i32]),
             "moe_abi_version": (_i32, []),
@@ -146,6 +176,157 @@ def moe_router_fwd(desc, logits, topk_idx, topk_w, stream=None) -> int:
 def moe_router_bwd(desc, topk_idx, topk_w, dtopk_w, dlogits, stream=None) -> int:
     return lib().moe_router_bwd(ctypes.byref(desc), _p(topk_idx), _p(topk_w), _p(dtopk_w),
                                 _p(dlogits), _stream(stream))
+
+
+def _fits(*tensors) -> bool:
+    """Whether each (tensor, element types, count) is what a call reads or writes: a contiguous GPU
+    tensor of one of those types with that many elements, or, as (tensor, types, rows, columns, row
+    stride), so many rows of its own stride; all of them on the current device, whose stream the call
+    takes.  None and raw addresses are the C side's to check."""
+    dev = None
+    for t, types, n, *row in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev or t.dtype not in types:
+            return False
+        if row:
+            if t.dim() != 2 or t.size(0) < n or t.size(1) < row[0]:
+                return False
+            if (n > 1 and t.stride(0) != row[1]) or (row[0] > 1 and t.stride(1) != 1):
+                return False
+        elif t.numel() < n or not t.is_contiguous():
+            return False
+    return True
+
+
+def _types() -> tuple:
+    """(fp32, int32, masks, codes, values by moe_type)"""
+    global _type_sets
+    if _type_sets is None:
+        import torch
+        _type_sets = ((torch.float32,), (torch.int32,), (torch.uint8, torch.bool),
+                      (torch.uint8, torch.float8_e4m3fn),
+                      {MOE_TYPE_F32: (torch.float32,), MOE_TYPE_BF16: (torch.bfloat16,)})
+    return _type_sets
+
+
+_type_sets = None
+
+
+def moe_balance_scratch_bytes(desc: moe_desc) -> int:
+    return lib().moe_balance_scratch_bytes(ctypes.byref(desc))
+
+
+def moe_balance_fwd(desc, logits, topk_idx, valid, counts, mean_p, losses, scratch, stream=None) -> int:
+    T, E, K = desc.T, desc.E, desc.K
+    f32, i32, mask, _, _ = _types()
+    if not _fits((logits, f32, T * E), (topk_idx, i32, T * K), (valid, mask, T), (counts, i32, E + 1),
+                 (mean_p, f32, E), (losses, f32, 2)):
+        return MOE_EINVAL
+    return lib().moe_balance_fwd(ctypes.byref(desc), _p(logits), _p(topk_idx), _p(valid), _p(counts),
+                                 _p(mean_p), _p(losses), _p(scratch),
+                                 0 if scratch is None else _nbytes(scratch), _stream(stream))
+
+
+def moe_balance_bwd(desc, logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, dlogits,
+                    stream=None) -> int:
+    T, E, K = desc.T, desc.E, desc.K
+    f32, i32, mask, _, _ = _types()
+    if not _fits((logits, f32, T * E), (valid, mask, T), (counts, i32, E + 1), (dlosses, f32, 2),
+                 (topk_idx, i32, T * K), (topk_w, f32, T * K), (dtopk_w, f32, T * K), (dlogits, f32, T * E)):
+        return MOE_EINVAL
+    return lib().moe_balance_bwd(ctypes.byref(desc), _p(logits), _p(valid), _p(counts), _p(dlosses),
+                                 _p(topk_idx), _p(topk_w), _p(dtopk_w), _p(dlogits), _stream(stream))
+
+
+def _code_ld(n: int) -> int:
+    return (n + 15) // 16 * 16
+
+
+def make_block_quant_desc(rows, cols, in_type=MOE_TYPE_BF16, scale=MOE_SCALE_TILE, ld_in=None,
+                          ld_codes=None, ld_codes_t=None) -> moe_block_quant_desc:
+    """Row strides default to the columns; those of codes to their next multiple of 16."""
+    return moe_block_quant_desc(rows, cols, in_type, scale, cols if ld_in is None else ld_in,
+                                _code_ld(cols) if ld_codes is None else ld_codes,
+                                _code_ld(rows) if ld_codes_t is None else ld_codes_t)
+
+
+def moe_block_quant(desc, x, codes, scales, codes_t=None, scales_t=None, stream=None) -> int:
+    R, C = desc.rows, desc.cols
+    rb, cb = (R + 127) // 128, (C + 127) // 128
+    block = desc.scale == MOE_SCALE_BLOCK
+    f32, _, _, code, io = _types()
+    if not _fits((x, io.get(desc.in_type, ()), R, C, desc.ld_in), (codes, code, R, _code_ld(C), desc.ld_codes),
+                 (codes_t, code, C, _code_ld(R), desc.ld_codes_t), (scales, f32, cb * (rb if block else R)),
+                 (scales_t, f32, rb * (cb if block else C))):
+        return MOE_EINVAL
+    return lib().moe_block_quant(ctypes.byref(desc), _p(x), _p(codes), _p(scales), _p(codes_t),
+                                 _p(scales_t), _stream(stream))
+
+
+def make_block_mm_desc(M, N, K, a_type=MOE_TYPE_E4M3, b_scale=MOE_SCALE_BLOCK, c_type=MOE_TYPE_BF16,
+                       flags=0, lda=None, ldb=None, ldc=None) -> moe_block_mm_desc:
+    """Row strides as in make_block_quant_desc."""
+    if lda is None:
+        lda = _code_ld(K) if a_type == MOE_TYPE_E4M3 else K
+    return moe_block_mm_desc(M, N, K, a_type, b_scale, c_type, flags, lda,
+                             _code_ld(K) if ldb is None else ldb, N if ldc is None else ldc)
+
+
+def moe_block_mm_scratch_bytes(desc: moe_block_mm_desc) -> int:
+    return lib().moe_block_mm_scratch_bytes(ctypes.byref(desc))
+
+
+def moe_block_mm(desc, a, a_scales, b, b_scales, c, scratch=None, stream=None) -> int:
+    M, N, K = desc.M, desc.N, desc.K
+    steps, own = (K + 127) // 128, desc.a_type == MOE_TYPE_E4M3
+    f32, _, _, code, io = _types()
+    if not _fits((a, code if own else io.get(desc.a_type, ()), M, _code_ld(K) if own else K, desc.lda),
+                 (a_scales, f32, steps * M), (b, code, N, _code_ld(K), desc.ldb),
+                 (b_scales, f32, steps * (N if desc.b_scale == MOE_SCALE_TILE else (N + 127) // 128)),
+                 (c, io.get(desc.c_type, ()), M, N, desc.ldc)):
+        return MOE_EINVAL
+    return lib().moe_block_mm(ctypes.byref(desc), _p(a), _p(a_scales), _p(b), _p(b_scales), _p(c),
+                              _p(scratch), 0 if scratch is None else _nbytes(scratch), _stream(stream))
+
+
+def make_grad_list(src, dst=None):
+    """The moe_grad array of contiguous GPU tensors (float32 or bfloat16) and of where their clipped
+    values go (default: in place).  It holds addresses: keep the tensors alive, and make it anew when
+    they move."""
+    import torch
+    types = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
+    src = list(src)
+    dst = src if dst is None else list(dst)
+    if len(dst) != len(src):
+        raise ValueError("as many destinations as gradients")
+    for s, d in zip(src, dst):
+        if s.dtype not in types or d.dtype != s.dtype or d.numel() != s.numel():
+            raise ValueError("gradients are float32 or bfloat16, their destinations alike")
+        if not (s.is_cuda and d.device == s.device == src[0].device and s.is_contiguous() and d.is_contiguous()):
+            raise ValueError("gradients and destinations are contiguous tensors on one GPU")
+    return (moe_grad * len(src))(*[moe_grad(s.data_ptr(), d.data_ptr(), s.numel(), types[s.dtype], 0)
+                                   for s, d in zip(src, dst)])
+
+
+def moe_grad_scratch_bytes(count: int) -> int:
+    return lib().moe_grad_scratch_bytes(count)
+
+
+def moe_grad_norm(grads, norm, scratch, stream=None) -> int:
+    if not _fits((norm, _types()[0], 1)):
+        return MOE_EINVAL
+    return lib().moe_grad_norm(grads, len(grads), _p(norm), _p(scratch),
+                               0 if scratch is None else _nbytes(scratch), _stream(stream))
+
+
+def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> int:
+    if not _fits((norm, _types()[0], 1)):
+        return MOE_EINVAL
+    return lib().moe_grad_clip(grads, len(grads), _p(norm), max_norm, _stream(stream))
 
 
 def moe_routing_view(desc, scratch) -> tuple:

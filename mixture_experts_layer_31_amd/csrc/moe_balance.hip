@@ -1,0 +1,440 @@
+// Load-balancing loss, z-loss and per-expert counts of the router, and their
+// gradient into the logits (moe_balance_fwd, moe_balance_bwd in moe.h).
+//
+// With p = softmax(z), f_e = counts_e / (n K) and P_e the mean of p_te over the n
+// kept tokens, loss0 = E sum_e f_e P_e has d loss0 / d z_tj =
+// (E / n) p_tj (f_j - sum_e f_e p_te), and loss1 = mean lse_t^2 has
+// d loss1 / d z_tj = (2 / n) lse_t p_tj.
+//
+// Both passes read each logit once into registers.  LPT lanes share a token (16 up
+// to 256 experts, so a wave holds four tokens and a row reduction is four DPP
+// moves; 64 above), each with VPL logits of it in runs of four.  The forward
+// adds p to per-lane sums over the block's tokens, joined at the end over the
+// wave's tokens and the block's waves in a fixed order, and counts the block's ids
+// with LDS atomics (integers: their order does not show); a second launch adds the
+// blocks' partial sums, in 64 bits.  Sums over one block's tokens are fp32: at most
+// a few dozen p <= 1 a lane.  A partial sum in global atomics would be one launch
+// fewer and another result with each run.
+#include <type_traits>
+
+#include "moe_args.h"
+#include "moe_fp8_codec.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBalThreads = 1024;  // forward: 16 waves join their sums in LDS
+constexpr int kBalBwdThreads = 256;
+constexpr int kBalMaxBlocks = 256;
+constexpr int kMaxExperts = 1024;
+
+struct BalScratch {
+  float* p;      // [blocks][E] sums of p
+  int32_t* c;    // [blocks][E] counts
+  float* z;      // [blocks] sums of lse^2
+  int32_t* n;    // [blocks] kept tokens
+  size_t bytes;
+};
+
+int bal_blocks(int T) {
+  const long long b = ceil_div(T, 64);
+  return b < 1 ? 1 : b > kBalMaxBlocks ? kBalMaxBlocks : int(b);
+}
+
+BalScratch bal_scratch(const moe_desc& d, char* base) {
+  const size_t G = bal_blocks(d.T), E = d.E;
+  BalScratch s;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { char* r = base + o; o = align256(o + bytes); return r; };
+  s.p = reinterpret_cast<float*>(take(G * E * 4));
+  s.c = reinterpret_cast<int32_t*>(take(G * E * 4));
+  s.z = reinterpret_cast<float*>(take(G * 4));
+  s.n = reinterpret_cast<int32_t*>(take(G * 4));
+  s.bytes = o;
+  return s;
+}
+
+// Sum over aligned groups of LPT lanes, in every lane.
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+  v += __int_as_float(dpp_swap1(__float_as_int(v)));
+  v += __int_as_float(dpp_swap2(__float_as_int(v)));
+  v += __int_as_float(dpp_mirror8(__float_as_int(v)));
+  v += __int_as_float(dpp_mirror16(__float_as_int(v)));
+  if constexpr (LPT == 64) {
+    v += __shfl_xor(v, 16, 64);
+    v += __shfl_xor(v, 32, 64);
+  }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float group_max(float v) {
+  v = max16(v);
+  if constexpr (LPT == 64) {
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    v = fmaxf(v, __shfl_xor(v, 32, 64));
+  }
+  return v;
+}
+
+// Expert of a lane's i-th value: runs of four, the group's lanes side by side.
+template <int LPT>
+__device__ __forceinline__ int expert_of(int l, int i) { return 4 * (l + LPT * (i >> 2)) + (i & 3); }
+
+// A token's logits (-inf past E); VEC: E % 4 == 0 and 16-byte rows.
+template <int LPT, int VPL, bool VEC>
+__device__ __forceinline__ void load_row(const float* row, int E, int l, float (&z)[VPL]) {
+#pragma unroll
+  for (int q = 0; q < VPL / 4; ++q) {
+    const int e = expert_of<LPT>(l, 4 * q);
+    if constexpr (VEC) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e < E) v = *reinterpret_cast<const float4*>(row + e);
+      z[4 * q] = v.x; z[4 * q + 1] = v.y; z[4 * q + 2] = v.z; z[4 * q + 3] = v.w;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) z[4 * q + r] = e + r < E ? row[e + r] : -INFINITY;
+    }
+  }
+}
+
+// Softmax of the row in place; returns its log-sum-exp.
+template <int LPT, int VPL>
+__device__ __forceinline__ float softmax_row(float (&z)[VPL], int E, int l) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) m = fmaxf(m, z[i]);
+  m = group_max<LPT>(m);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    // the padding stays out also where m is not finite
+    z[i] = expert_of<LPT>(l, i) < E ? expf(z[i] - m) : 0.f;
+    s += z[i];
+  }
+  s = group_sum<LPT>(s);
+  const float r = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) z[i] *= r;
+  return m + logf(s);
+}
+
+template <int LPT, int VPL, bool VEC>
+__global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const uint8_t* __restrict__ valid, int T, int E, int K, BalScratch out) {
+  constexpr int GROUPS = kBalThreads / LPT, WAVES = kBalThreads / 64, COLS = LPT * VPL;
+  __shared__ int32_t hist[COLS];
+  __shared__ float red[WAVES][COLS];
+  __shared__ float zred[WAVES];
+  __shared__ int32_t nred[WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = tid & (LPT - 1);
+  // token numbers in 64 bits: a step past the last of 2^31 - 1 tokens must not wrap
+  const int64_t chunk = (int64_t(T) + gridDim.x - 1) / gridDim.x;
+  const int64_t t0 = min(int64_t(T), blockIdx.x * chunk), t1 = min(int64_t(T), t0 + chunk);
+  const int pairs = int(t1 - t0) * K;
+  for (int e = tid; e < COLS; e += kBalThreads) hist[e] = 0;
+  __syncthreads();
+  // ids, one (token, slot) pair a thread
+  for (int64_t i = tid; i < pairs; i += kBalThreads) {
+    if (valid == nullptr || valid[t0 + int(i) / K]) {
+      const int e = topk_idx[size_t(t0) * K + i];
+      if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+    }
+  }
+  float acc[VPL], zsum = 0.f;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  for (int64_t t = t0 + tid / LPT; t < t1; t += GROUPS) {
+    if (valid != nullptr && !valid[t]) continue;
+    float p[VPL];
+    load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, p);
+    const float lse = softmax_row<LPT>(p, E, l);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) acc[i] += p[i];
+    zsum = __builtin_fmaf(lse, lse, zsum);
+    n += 1;
+  }
+  if constexpr (LPT == 16) {  // the wave's four tokens
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      acc[i] += __shfl_xor(acc[i], 16, 64);
+      acc[i] += __shfl_xor(acc[i], 32, 64);
+    }
+    zsum += __shfl_xor(zsum, 16, 64);
+    zsum += __shfl_xor(zsum, 32, 64);
+    n += __shfl_xor(n, 16, 64);
+    n += __shfl_xor(n, 32, 64);
+  }
+  if (lane < LPT) {
+#pragma unroll
+    for (int q = 0; q < VPL / 4; ++q)
+      *reinterpret_cast<float4*>(&red[wv][expert_of<LPT>(l, 4 * q)]) =
+          make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+  }
+  if (lane == 0) {
+    zred[wv] = zsum;
+    nred[wv] = n;
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kBalThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) s += red[w][e];
+    out.p[size_t(blockIdx.x) * E + e] = s;
+    out.c[size_t(blockIdx.x) * E + e] = hist[e];
+  }
+  if (tid == 0) {
+    float s = 0.f;
+    int c = 0;
+    for (int w = 0; w < WAVES; ++w) {
+      s += zred[w];
+      c += nred[w];
+    }
+    out.z[blockIdx.x] = s;
+    out.n[blockIdx.x] = c;
+  }
+}
+
+// One block: the partial sums of the forward's blocks, and the losses.
+__global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(
+    BalScratch in, int blocks, int E, int K, int32_t* __restrict__ counts,
+    float* __restrict__ mean_p, float* __restrict__ losses) {
+  __shared__ double ps[kBalThreads];
+  __shared__ int32_t cs[kBalThreads];
+  __shared__ int32_t n_all;
+  const int tid = threadIdx.x;
+  if (tid < 64) {
+    double z = 0.;
+    int n = 0;
+    for (int b = tid; b < blocks; b += 64) {
+      z += in.z[b];
+      n += in.n[b];
+    }
+    for (int o = 32; o >= 1; o >>= 1) {
+      z += __shfl_xor(z, o, 64);
+      n += __shfl_xor(n, o, 64);
+    }
+    if (tid == 0) {
+      n_all = n;
+      counts[E] = n;
+      losses[1] = n > 0 ? float(z / n) : 0.f;
+    }
+  }
+  // `cols` threads side by side, `rows` of them in each column
+  const int cols = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : E <= 512 ? 512 : 1024;
+  const int rows = kBalThreads / cols, e = tid & (cols - 1), r = tid / cols;
+  double p = 0.;
+  int c = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int b = r; b < blocks; b += rows) {
+      p += in.p[size_t(b) * E + e];
+      c += in.c[size_t(b) * E + e];
+    }
+  }
+  ps[tid] = p;
+  cs[tid] = c;
+  __syncthreads();
+  const int n = n_all;
+  double dot = 0.;
+  if (r == 0 && e < E) {
+    for (int k = 1; k < rows; ++k) {
+      p += ps[k * cols + e];
+      c += cs[k * cols + e];
+    }
+    const double mp = n > 0 ? p / n : 0.;
+    counts[e] = c;
+    mean_p[e] = float(mp);
+    dot = n > 0 ? mp * (double(c) / (double(n) * K)) : 0.;
+  }
+  __syncthreads();
+  ps[tid] = dot;
+  __syncthreads();
+  for (int o = kBalThreads / 2; o >= 1; o >>= 1) {
+    if (tid < o) ps[tid] += ps[tid + o];
+    __syncthreads();
+  }
+  if (tid == 0) losses[0] = float(E * ps[0]);
+}
+
+template <int LPT, int VPL, bool VEC, bool ROUTER>
+__global__ void __launch_bounds__(kBalBwdThreads) balance_bwd_kernel(
+    const float* __restrict__ logits, const uint8_t* __restrict__ valid,
+    const int32_t* __restrict__ counts, const float* __restrict__ dlosses,
+    const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
+    const float* __restrict__ dtopk_w, int T, int E, int K, float* __restrict__ dlogits) {
+  constexpr int GROUPS = kBalBwdThreads / LPT;
+  __shared__ int32_t s_j[ROUTER ? GROUPS : 1][64];
+  __shared__ float s_w[ROUTER ? GROUPS : 1][64], s_dw[ROUTER ? GROUPS : 1][64];
+  const int tid = threadIdx.x, l = tid & (LPT - 1), g = tid / LPT;
+  const int n = counts[E];
+  const float per = n > 0 ? 1.f / float(n) : 0.f;
+  const float a = dlosses[0] * (float(E) * per), b = dlosses[1] * (2.f * per);
+  float f[VPL];  // the lane's experts' shares
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = expert_of<LPT>(l, i);
+    f[i] = e < E ? float(counts[e]) * (per / float(K)) : 0.f;
+  }
+  for (int64_t t = int64_t(blockIdx.x) * GROUPS + g; t < T; t += int64_t(gridDim.x) * GROUPS) {
+    const bool keep = valid == nullptr || valid[t];
+    float p[VPL];
+    if (keep) {
+      load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, p);
+      const float lse = softmax_row<LPT>(p, E, l);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s = __builtin_fmaf(f[i], p[i], s);
+      s = group_sum<LPT>(s);
+      const float zl = b * lse;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) p[i] *= __builtin_fmaf(a, f[i] - s, zl);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) p[i] = 0.f;
+    }
+    if constexpr (ROUTER) {
+      // w_k (dw_k - sum w dw) on the selected experts, slots in order; the group's
+      // lanes are in one wave, whose LDS accesses stay in order
+      for (int k = l; k < K; k += LPT) {
+        s_j[g][k] = topk_idx[size_t(t) * K + k];
+        s_w[g][k] = topk_w[size_t(t) * K + k];
+        s_dw[g][k] = dtopk_w[size_t(t) * K + k];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      float c = 0.f;
+      for (int k = 0; k < K; ++k) c += s_w[g][k] * s_dw[g][k];
+      for (int k = 0; k < K; ++k) {
+        const int j = s_j[g][k];
+        const float v = s_w[g][k] * (s_dw[g][k] - c);
+        // j = 4 (l + LPT q) + r is value 4 q + r of lane l
+        const bool mine = j >= 0 && j < E && ((j >> 2) & (LPT - 1)) == l;
+        const int at = mine ? 4 * ((j >> 2) / LPT) + (j & 3) : -1;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) p[i] += at == i ? v : 0.f;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    float* out = dlogits + size_t(t) * E;
+#pragma unroll
+    for (int q = 0; q < VPL / 4; ++q) {
+      const int e = expert_of<LPT>(l, 4 * q);
+      if constexpr (VEC) {
+        if (e < E)
+          *reinterpret_cast<float4*>(out + e) =
+              make_float4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (e + r < E) out[e + r] = p[4 * q + r];
+      }
+    }
+  }
+}
+
+template <class F>
+int with_shape(int E, bool vec, F&& f) {
+  auto go = [&](auto lpt, auto vpl) {
+    return vec ? f(lpt, vpl, std::true_type{}) : f(lpt, vpl, std::false_type{});
+  };
+  using std::integral_constant;
+  if (E <= 64) return go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (E <= 128) return go(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+  if (E <= 256) return go(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+  if (E <= 512) return go(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  return go(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+}
+
+int check_balance_desc(const moe_desc* d) {
+  if (d == nullptr) return MOE_EINVAL;
+  if (d->T < 0 || d->E <= 0 || d->K <= 0 || d->K > d->E) return MOE_EINVAL;
+  if ((long long)d->T * d->K >= (1LL << 31)) return MOE_EINVAL;
+  return d->E > kMaxExperts ? MOE_EUNSUPPORTED : MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_balance_scratch_bytes(const moe_desc* d) {
+  return check_balance_desc(d) == MOE_OK ? bal_scratch(*d, nullptr).bytes : 0;
+}
+
+int moe_balance_fwd(const moe_desc* d, const float* logits, const int32_t* topk_idx,
+                    const uint8_t* valid, int32_t* counts, float* mean_p, float* losses,
+                    void* scratch, size_t scratch_bytes, void* stream) {
+  const int rc = check_balance_desc(d);
+  if (rc) return rc;
+  if (counts == nullptr || mean_p == nullptr || losses == nullptr || scratch == nullptr ||
+      (d->T > 0 && (logits == nullptr || topk_idx == nullptr)))
+    return MOE_EINVAL;
+  if (!aligned_to(logits, 4) || !aligned_to(topk_idx, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(mean_p, 4) || !aligned_to(losses, 4) || !aligned_to(scratch, 16))
+    return MOE_EALIGN;
+  const BalScratch sc = bal_scratch(*d, static_cast<char*>(scratch));
+  if (scratch_bytes < sc.bytes) return MOE_ESCRATCH;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int blocks = bal_blocks(d->T);
+  const bool vec = d->E % 4 == 0 && aligned_to(logits, 16);
+  prof_begin("balance_fwd", s);
+  with_shape(d->E, vec, [&](auto lpt, auto vpl, auto v) {
+    balance_fwd_kernel<decltype(lpt)::value, decltype(vpl)::value, decltype(v)::value>
+        <<<unsigned(blocks), kBalThreads, 0, s>>>(logits, topk_idx, valid, d->T, d->E, d->K, sc);
+    return 0;
+  });
+  prof_end(s);
+  if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+  prof_begin("balance_finish", s);
+  balance_finish_kernel<<<1, kBalThreads, 0, s>>>(sc, blocks, d->E, d->K, counts, mean_p, losses);
+  prof_end(s);
+  return launched();
+}
+
+int moe_balance_bwd(const moe_desc* d, const float* logits, const uint8_t* valid,
+                    const int32_t* counts, const float* dlosses, const int32_t* topk_idx,
+                    const float* topk_w, const float* dtopk_w, float* dlogits, void* stream) {
+  const int rc = check_balance_desc(d);
+  if (rc) return rc;
+  const bool router = topk_idx != nullptr;
+  if ((topk_w != nullptr) != router || (dtopk_w != nullptr) != router) {
+    if (d->T > 0) return MOE_EINVAL;
+  }
+  if (router && d->K > 64) return MOE_EUNSUPPORTED;
+  if (d->T == 0) return MOE_OK;
+  if (logits == nullptr || counts == nullptr || dlosses == nullptr || dlogits == nullptr ||
+      static_cast<const void*>(dlogits) == logits)
+    return MOE_EINVAL;
+  if (!aligned_to(logits, 4) || !aligned_to(counts, 4) || !aligned_to(dlosses, 4) ||
+      !aligned_to(topk_idx, 4) || !aligned_to(topk_w, 4) || !aligned_to(dtopk_w, 4) ||
+      !aligned_to(dlogits, 4))
+    return MOE_EALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool vec = d->E % 4 == 0 && aligned_to(logits, 16) && aligned_to(dlogits, 16);
+  prof_begin("balance_bwd", s);
+  with_shape(d->E, vec, [&](auto lpt, auto vpl, auto v) {
+    constexpr int LPT = decltype(lpt)::value, VPL = decltype(vpl)::value;
+    constexpr bool VEC = decltype(v)::value;
+    const long long want = ceil_div(d->T, kBalBwdThreads / LPT);
+    const unsigned grid = unsigned(want < 4096 ? want : 4096);
+    if (router)
+      balance_bwd_kernel<LPT, VPL, VEC, true><<<grid, kBalBwdThreads, 0, s>>>(
+          logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, d->T, d->E, d->K, dlogits);
+    else
+      balance_bwd_kernel<LPT, VPL, VEC, false><<<grid, kBalBwdThreads, 0, s>>>(
+          logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, d->T, d->E, d->K, dlogits);
+    return 0;
+  });
+  prof_end(s);
+  return launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,226 @@
+"""Balance loss, counts and their gradient on the GPU (through the C ABI) against the float64 oracle.
+
+Tolerances, u = 2^-24 (fp32, half a step).  With R the largest |z - max z| of a token:
+* a probability: z - max rounds by R u, expf is within 2 ulp (4 u), the sum of its row adds
+  VPL + 6 <= E / 16 + 70 roundings at most, the reciprocal and the product 3 u: relative error
+  d = (R + E / 16 + 77) u;
+* mean_p: positive terms, fp32 over a block's tokens (its lanes' tokens, the wave's and the
+  waves' joins: at most T / 64 + 24 roundings), then 64 bits and one rounding:
+  d + (T / 64 + 25) u relative; losses[0] alike, with one more rounding;
+* lse: max + log(s): e = d + 4 u (|log s| + |lse|) absolute; losses[1] = mean lse^2 within
+  mean(2 |lse| e + e^2) + (T / 64 + 25) u mean(lse^2);
+* dlogits: p (a (f - s) + b lse), a = dl0 E / n, b = 2 dl1 / n (4 u each): within
+  p ((|a| (f + s) + |b lse|) (2 d + 12 u) + |b| e); the router's part w (dw - c) within
+  (K + 4) u w (|dw| + sum w |dw|) and one rounding of the sum;
+* 2^-126 absolute, where a result may be subnormal.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_31_amd as moe
+from oracle import balance_oracle as bo
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+TINY = 2.0 ** -126
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    moe.lib()
+
+
+def _dev(a, off=0):
+    """On the GPU, its first element off * 4 bytes past a 16-byte line."""
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    flat = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+    flat[off:].copy_(t.reshape(-1))
+    return flat[off:].view(t.shape)
+
+
+def _call(z, idx, valid, dl, router=None, off=0):
+    T, E = z.shape
+    K = idx.shape[1]
+    d = moe.make_desc(T, 0, 0, E, K)
+    zt, it = _dev(z.astype(np.float32), off), _dev(idx.astype(np.int32))
+    vt = None if valid is None else _dev(valid)
+    counts = torch.full((E + 1,), -7, dtype=torch.int32, device="cuda")
+    mp, losses = torch.full((E,), np.nan, device="cuda"), torch.full((2,), np.nan, device="cuda")
+    scratch = torch.full((moe.moe_balance_scratch_bytes(d),), 0xA5, dtype=torch.uint8, device="cuda")
+    assert moe.moe_balance_fwd(d, zt, it, vt, counts, mp, losses, scratch) == moe.MOE_OK
+    dz = _dev(np.full((T, E), np.nan, np.float32), off)
+    part = (None, None, None) if router is None else (it, *[_dev(r) for r in router])
+    assert moe.moe_balance_bwd(d, zt, vt, counts, _dev(np.float32(dl)), *part, dz) == moe.MOE_OK
+    torch.cuda.synchronize()
+    return [t.cpu().numpy() for t in (counts, mp, losses, dz)]
+
+
+def _check(z, idx, valid, dl=(0.7, -0.3), router=None, off=0, name=""):
+    T, E = z.shape
+    K = idx.shape[1]
+    print(f"[case] balance {name} T={T} E={E} K={K} masked={valid is not None} router={router is not None}",
+          flush=True)
+    z, dl = z.astype(np.float32), np.float32(dl).astype(np.float64)
+    counts, mp, losses, dz = _call(z, idx, valid, dl, router, off)
+    f = bo.forward(z, idx, valid)
+    assert np.array_equal(counts, f["counts"])
+    n, keep = len(f["keep"]), f["keep"]
+    p, lse = f["p"], f["lse"]
+    sums = (T / 64 + 25) * U
+    if n:
+        zk = z[keep].astype(np.float64)
+        R = np.where(np.isfinite(zk), zk.max(axis=1, keepdims=True) - zk, 0).max()
+        d = (R + E / 16 + 77) * U
+        e = d + 4 * U * (np.abs(lse - zk.max(axis=1)) + np.abs(lse))
+        assert np.all(np.abs(mp - f["mean_p"]) <= (d + sums) * f["mean_p"] + TINY)
+        assert abs(losses[0] - f["losses"][0]) <= (d + sums + 2 * U) * f["losses"][0]
+        assert abs(losses[1] - f["losses"][1]) <= (2 * np.abs(lse) * e + e * e).mean() + sums * f["losses"][1] + TINY
+    else:
+        assert not mp.any() and not losses.any()
+    ref, bound = bo.backward(z, idx, valid, dl, f), np.zeros((T, E))
+    if n:
+        a, b = abs(dl[0]) * E / n, abs(dl[1]) * 2 / n
+        share = f["counts"][:E] / (n * K)
+        s = (p * share).sum(axis=1, keepdims=True)
+        bound[keep] = p * ((a * (share + s) + b * np.abs(lse)[:, None]) * (2 * d + 12 * U) + b * e[:, None]) + TINY
+    if router is not None:
+        w, dw = [r.astype(np.float64) for r in router]
+        part = bo.router_part(idx, w, dw, E)
+        size = np.zeros((T, E))
+        t, k = np.nonzero((idx >= 0) & (idx < E))
+        each = w * (np.abs(dw) + (w * np.abs(dw)).sum(axis=1, keepdims=True))
+        np.add.at(size, (t, idx[t, k]), each[t, k])
+        ref = ref + part
+        bound += (K + 4) * U * size + U * np.abs(ref) + TINY
+    err = np.abs(dz - ref)
+    assert np.all(err <= bound), (name, float((err - bound).max()))
+
+
+def _inputs(seed, T, E, K, spread=1.0):
+    rng = np.random.default_rng(seed)
+    z = (rng.standard_normal((T, E)) * spread).astype(np.float32)
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :K]
+    w = rng.random((T, K)).astype(np.float32)
+    w /= w.sum(axis=1, keepdims=True)
+    return z, idx, (w, rng.standard_normal((T, K)).astype(np.float32)), rng
+
+
+@pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 8, 2), (1, 128, 8), (3, 5, 5), (64, 8, 2), (65, 64, 3),
+                                   (257, 65, 4), (700, 100, 6), (333, 128, 8), (129, 256, 8), (50, 257, 2),
+                                   (200, 512, 64), (41, 513, 3), (37, 1000, 7), (66, 1024, 64), (16411, 12, 2)])
+def test_shapes(T, E, K):
+    z, idx, router, rng = _inputs(T * 7 + E, T, E, K)
+    _check(z, idx, None, router=router, name="plain")
+    _check(z, idx, rng.random(T) < 0.6, name="masked", off=1)
+
+
+def test_every_slot_of_many_experts():
+    z, idx, _, _ = _inputs(5, 20, 200, 200)
+    _check(z, idx, None, name="K=E")  # the loss's gradient has no limit of 64 slots
+
+
+def test_masks():
+    T, E, K = 130, 12, 3
+    z, idx, router, rng = _inputs(6, T, E, K)
+    _check(z, idx, np.zeros(T, bool), router=router, name="nothing kept")
+    one = np.zeros(T, bool)
+    one[-1] = True
+    _check(z, idx, one, router=router, name="the last token")
+    # what a dropped token holds does not matter
+    valid = rng.random(T) < 0.5
+    bad = z.copy()
+    bad[~valid] = np.array([np.nan, np.inf, -np.inf] * 4, np.float32)
+    ids = idx.copy()
+    ids[~valid] = 1 << 30
+    a, b = _call(z, idx, valid, (1, 1)), _call(bad, ids, valid, (1, 1))
+    for x, y in zip(a, b):
+        assert np.array_equal(x, y)
+    assert not b[3][~valid].any()
+    # any byte but 0 keeps a token
+    _check(z, idx, valid.astype(np.uint8) * 2, name="bytes")
+
+
+def test_ids_out_of_range_and_twice():
+    T, E, K = 90, 10, 4
+    z, idx, router, rng = _inputs(7, T, E, K)
+    idx = idx.copy()
+    idx[::3, 1], idx[1::3, 2] = -1, E
+    _check(z, idx, None, router=router, name="out of range")
+    idx[:] = idx[:, :1]
+    _check(z, idx, None, router=router, name="one id in every slot")
+
+
+def test_extreme_logits():
+    T, E, K = 70, 16, 2
+    z, idx, router, rng = _inputs(8, T, E, K, spread=30.0)
+    z[:, :5] = -np.inf  # dead experts
+    idx = np.argsort(-z, axis=1, kind="stable")[:, :K]
+    _check(z, idx, None, router=router, name="dead experts")
+    _check(np.full_like(z, 5), idx, None, router=router, name="equal")
+    # the definition's NaN, in its own row only
+    z[3] = -np.inf
+    counts, mp, losses, dz = _call(z, idx, None, (1, 1))
+    assert np.isnan(mp).all() and np.isnan(losses).all() and counts[E] == T
+    assert np.isnan(dz[3]).all() and np.isfinite(np.delete(dz, 3, axis=0)).all()
+
+
+def test_no_tokens():
+    d = moe.make_desc(0, 0, 0, 8, 2)
+    counts = torch.full((9,), 5, dtype=torch.int32, device="cuda")
+    mp, losses = torch.ones(8, device="cuda"), torch.ones(2, device="cuda")
+    scratch = torch.empty(moe.moe_balance_scratch_bytes(d), dtype=torch.uint8, device="cuda")
+    assert moe.moe_balance_fwd(d, None, None, None, counts, mp, losses, scratch) == moe.MOE_OK
+    torch.cuda.synchronize()
+    assert not counts.any() and not mp.any() and not losses.any()
+
+
+def test_same_bits_and_graph_replays():
+    T, E, K = 5000, 128, 8
+    z, idx, (w, dw), _ = _inputs(9, T, E, K)
+    ref = _call(z, idx, None, (1e-2, 1e-3), (w, dw))
+    for x, y in zip(ref, _call(z, idx, None, (1e-2, 1e-3), (w, dw))):
+        assert np.array_equal(x, y)
+    d = moe.make_desc(T, 0, 0, E, K)
+    ins = [_dev(z), _dev(idx.astype(np.int32)), _dev(w), _dev(dw), _dev(np.float32([1e-2, 1e-3]))]
+    counts = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    mp, losses, dz = (torch.empty(n, device="cuda") for n in (E, 2, T * E))
+    scratch = torch.empty(moe.moe_balance_scratch_bytes(d), dtype=torch.uint8, device="cuda")
+
+    def step():
+        moe.check(moe.moe_balance_fwd(d, ins[0], ins[1], None, counts, mp, losses, scratch))
+        moe.check(moe.moe_balance_bwd(d, ins[0], None, counts, ins[4], ins[1], ins[2], ins[3], dz))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # another stream than the tensors' own
+        step()
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        for t in (counts, mp, losses, dz, scratch):
+            t.fill_(1)
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(ref, (counts, mp, losses, dz)):
+            assert np.array_equal(x.reshape(-1), y.cpu().numpy())
+        step()  # the program's own eager calls between the replays
+        torch.cuda.synchronize()
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    d = moe.make_desc(4, 0, 0, 8, 2)
+    z = torch.zeros(4, 8, device="cuda")
+    idx = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    out = [torch.zeros(9, dtype=torch.int32, device="cuda"), torch.zeros(8, device="cuda"),
+           torch.zeros(2, device="cuda"), torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")]
+    assert moe.moe_balance_fwd(d, z, idx, None, *out) == moe.MOE_OK
+    for bad in (z.cpu(), z.double(), z[:3], torch.zeros(8, 4, device="cuda").t()):
+        assert moe.moe_balance_fwd(d, bad, idx, None, *out) == moe.MOE_EINVAL
+    assert moe.moe_balance_fwd(d, z, idx.long(), None, *out) == moe.MOE_EINVAL
