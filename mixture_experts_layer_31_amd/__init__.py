@@ -126,9 +126,9 @@ def _p(t):
 
 
 def _stream(stream):
-    if stream is None:
+    if stream is None:  # the raw handle: building a torch Stream object takes 3 us a call
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -40,6 +40,12 @@ def compile_flags() -> list:
     ]
 
 
+# Flags of one file.  moe_block.hip: matrix instructions write vector registers, where each run's
+# sums are scaled and added next; in the accumulator registers that the compiler otherwise takes
+# when they fit, every one of them costs a move first, as much vector work as the scaling itself.
+FILE_FLAGS = {"moe_block.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
+
 def sources() -> list:
     return sorted(glob.glob(os.path.join(HERE, "csrc", "*.hip")))
 
@@ -51,7 +57,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
 
     def one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-        cmd = [cc, *compile_flags(), "-c", src, "-o", obj]
+        cmd = [cc, *compile_flags(), *FILE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)

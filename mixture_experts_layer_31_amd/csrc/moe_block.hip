@@ -68,39 +68,19 @@ struct QuantArgs {
   float* sc;
   uint8_t* qt;   // [cols, ldt] or null
   float* sct;
-  bool vec;      // 16-byte loads of eight (four) elements are aligned
 };
 
-// Eight consecutive elements of row r from column c (0 where there is none).
 template <class T>
-__device__ __forceinline__ void load8(const QuantArgs& p, int64_t r, int c, float (&v)[8]) {
+__device__ __forceinline__ void as_floats(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  if (r >= p.rows || c >= p.cols) return;
-  const T* x = static_cast<const T*>(p.x) + r * p.ldx + c;
-  if (p.vec && c + 8 <= p.cols) {
+  for (int j = 0; j < 4; ++j) {
     if constexpr (sizeof(T) == 2) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 w = reinterpret_cast<const float4*>(x)[i];
-        v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
-      }
+      f[j] = __uint_as_float(w[j]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < p.cols) {
-        if constexpr (sizeof(T) == 2) v[i] = bf2f(x[i]);
-        else v[i] = x[i];
-      }
   }
 }
 
@@ -129,8 +109,28 @@ __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
   const int rw = wv * 4 + (lane >> 4);
   T* tile = reinterpret_cast<T*>(smem);
   float v[8][8];
+  {
+    constexpr int N = 16 / sizeof(T), NP = 8 / N;  // pieces of eight elements
+    const T* x = static_cast<const T*>(p.x);
+    RowPiece<T> raw[8][NP];
+    const bool wide = p.cols >= N, edge = c0 + 128 > p.cols;
 #pragma unroll
-  for (int it = 0; it < 8; ++it) load8<T>(p, r0 + it * 16 + rw, c0 + 8 * l16, v[it]);
+    for (int it = 0; it < 8; ++it) {
+      const int64_t r = r0 + it * 16 + rw;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (wide) raw[it][i].load(x + r * p.ldx, c0 + 8 * l16 + i * N, p.cols, r < p.rows, x);
+        else raw[it][i].load_short(x + r * p.ldx, c0 + 8 * l16 + i * N, p.cols, r < p.rows);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 8; ++it)
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (wide) raw[it][i].mend(edge);
+        as_floats<T>(raw[it][i].v, v[it] + i * N);
+      }
+  }
   float amax = 0.f;
   if constexpr (BLOCK) {
 #pragma unroll
@@ -209,10 +209,61 @@ __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
   }
 }
 
+// Rows alone, in tiles: IT rows a thread and no LDS.
+template <class T, int IT>
+__global__ void __launch_bounds__(256) block_quant_rows_kernel(QuantArgs p) {
+  constexpr int N = 16 / sizeof(T), NP = 8 / N;
+  const int rt = blockIdx.x / p.ctiles, ct = blockIdx.x - rt * p.ctiles;
+  const int lane = threadIdx.x & 63, l16 = lane & 15;
+  const int64_t r0 = int64_t(rt) * (16 * IT) + (threadIdx.x >> 6) * 4 + (lane >> 4);
+  const int c = ct * 128 + 8 * l16;
+  const T* x = static_cast<const T*>(p.x);
+  RowPiece<T> raw[IT][NP];
+  const bool wide = p.cols >= N, edge = ct * 128 + 128 > p.cols;
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int64_t r = r0 + it * 16;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (wide) raw[it][i].load(x + r * p.ldx, c + i * N, p.cols, r < p.rows, x);
+      else raw[it][i].load_short(x + r * p.ldx, c + i * N, p.cols, r < p.rows);
+    }
+  }
+  const int cols16 = (p.cols + 15) & ~15;
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int64_t r = r0 + it * 16;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if (wide) raw[it][i].mend(edge);
+      as_floats<T>(raw[it][i].v, v + i * N);
+    }
+    const Quant qz(max16(amax8(v)));
+    const uint2 w = make_uint2(qz.codes(v[0], v[1], v[2], v[3]), qz.codes(v[4], v[5], v[6], v[7]));
+    if (r < p.rows && c < cols16) {
+      *reinterpret_cast<uint2*>(p.q + r * p.ldq + c) = w;
+      if (l16 == 0) p.sc[int64_t(ct) * p.rows + r] = qz.scale;
+    }
+  }
+}
+
+template <class T>
+void launch_quant_rows(const QuantArgs& a, hipStream_t s) {
+  // as many rows a thread as still leave a few workgroups a CU
+  const long long slabs = ceil_div(a.rows, 16) * a.ctiles;
+  if (slabs >= 16384) block_quant_rows_kernel<T, 8><<<unsigned(ceil_div(a.rows, 128) * a.ctiles), 256, 0, s>>>(a);
+  else if (slabs >= 4096) block_quant_rows_kernel<T, 2><<<unsigned(ceil_div(a.rows, 32) * a.ctiles), 256, 0, s>>>(a);
+  else block_quant_rows_kernel<T, 1><<<unsigned(slabs), 256, 0, s>>>(a);
+}
+
 int launch_block_quant(const QuantArgs& a, int in_type, bool block, hipStream_t s) {
   const unsigned grid = unsigned(ceil_div(a.rows, 128) * a.ctiles);
   prof_begin("block_quant", s);
-  if (in_type == MOE_TYPE_BF16) {
+  if (a.qt == nullptr && !block) {
+    if (in_type == MOE_TYPE_BF16) launch_quant_rows<uint16_t>(a, s);
+    else launch_quant_rows<float>(a, s);
+  } else if (in_type == MOE_TYPE_BF16) {
     if (block) block_quant_kernel<uint16_t, true><<<grid, 256, 0, s>>>(a);
     else block_quant_kernel<uint16_t, false><<<grid, 256, 0, s>>>(a);
   } else {
@@ -223,14 +274,13 @@ int launch_block_quant(const QuantArgs& a, int in_type, bool block, hipStream_t 
   return launched();
 }
 
-QuantArgs quant_args(const void* x, int in_type, int rows, int cols, int64_t ldx) {
+QuantArgs quant_args(const void* x, int rows, int cols, int64_t ldx) {
   QuantArgs a{};
   a.x = x;
   a.ldx = ldx;
   a.rows = rows;
   a.cols = cols;
   a.ctiles = int(ceil_div(cols, 128));
-  a.vec = aligned_to(x, 16) && ldx * int64_t(type_bytes(in_type)) % 16 == 0;
   return a;
 }
 
@@ -240,22 +290,14 @@ QuantArgs quant_args(const void* x, int in_type, int rows, int cols, int64_t ldx
 struct MmArgs {
   int M, N, K, ntm, ntn, ksteps;
   const uint8_t* A;
-  const float* SA;  // [ksteps][M]
+  const float* SA;  // [ksteps][ldsa]
+  int ldsa;
   const uint8_t* B;
   const float* SB;  // TILE: [ksteps][N]; BLOCK: [ceil(N/128)][ksteps]
   int64_t lda, ldb, ldc;
   void* C;
-  bool add, vec;    // add: C += ; vec: 16-byte accesses of C's rows are aligned
+  bool add;         // C +=
 };
-
-// fp8 fragment (32 bytes: two 16-byte chunks of a 128-byte row) of sub-step kk: the
-// same bytes of a run for A and B, so their order within the run does not matter.
-__device__ __forceinline__ i32x8 frag_q(const char* tile, int row, int kk, int lane) {
-  const int h = lane >> 5, c0 = 4 * kk + h, c1 = 4 * kk + 2 + h;
-  const i32x4 a = *reinterpret_cast<const i32x4*>(tile + row * 128 + ((c0 ^ swz_k(row)) << 4));
-  const i32x4 b = *reinterpret_cast<const i32x4*>(tile + row * 128 + ((c1 ^ swz_k(row)) << 4));
-  return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-}
 
 // Eight of the fragment's codes as bf16 (exact), the eighth part s of its 32.
 __device__ __forceinline__ bf16x8 widen(const i32x8& f, int s) {
@@ -269,10 +311,6 @@ __device__ __forceinline__ bf16x8 widen(const i32x8& f, int s) {
   return r;
 }
 
-__device__ __forceinline__ f32x16 mfma_q(i32x8 b, i32x8 a, f32x16 c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, c, 0, 0, 0, 127, 0, 127);
-}
-
 // One 4-byte entry a lane into LDS at lds + 4 * lane.
 __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
   asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, 0 offen lds"
@@ -281,176 +319,709 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
                : "memory", "m0");
 }
 
-// One BM x BN tile of C a workgroup, 128-element steps in two LDS stages.
-template <class TL, bool B_TILE, bool OUT_F32>
-__global__ void __launch_bounds__(TL::THREADS, 1) block_mm_kernel(MmArgs p) {
-  constexpr int BM = TL::BM, BN = TL::BN, WM = TL::WM, WN = TL::WN, WAVES = TL::WAVES;
-  constexpr int WMT = TL::WMT, WNT = TL::WNT;
-  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-  constexpr int STAGE = A_BYTES + B_BYTES + (BM + BN) * 4;
-  constexpr int ES = OUT_F32 ? 4 : 2, BAND = TL::WGM * 32 * BN * ES;
-  constexpr int LDS = 2 * STAGE > BAND ? 2 * STAGE : BAND;
-  static_assert(BM % 64 == 0 && BN % 64 == 0, "scale loads of 64 entries");
-  __shared__ __attribute__((aligned(1024))) char smem[LDS];
+// Large products, bf16 results: 256 x 256 tiles, eight waves of 128 x 64.
+template <bool B_TILE>
+__global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
+  constexpr int BM = 256, BN = 256, WAVES = 8, MB = 8, NB = 4;
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES + 2048;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
   const int l = xcd_remap(blockIdx.x, gridDim.x);
-  const int mt = l % p.ntm, nt = l / p.ntm;
-  const int lane = threadIdx.x & 63;
+  int mt, nt;
+  wgrad_mn(l, p.ntm, p.ntn, mt, nt);
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / TL::WGN, wn = wave % TL::WGN;
+  const int wm = wave >> 2, wn = wave & 3;
   const int m0 = mt * BM, n0 = nt * BN;
   const int mrows = min(BM, p.M - m0), nrows = min(BN, p.N - n0);
   const int kbytes = (p.K + 15) & ~15;
-
   KStager<BM, WAVES, 128> sa;
   sa.init(make_rsrc(p.A + int64_t(m0) * p.lda, uint32_t((mrows - 1) * p.lda + kbytes)),
           [&](int r) { return r < mrows ? int(r * p.lda) : -1; }, wave, lane);
   KStager<BN, WAVES, 128> sb;
   sb.init(make_rsrc(p.B + int64_t(n0) * p.ldb, uint32_t((nrows - 1) * p.ldb + kbytes)),
           [&](int r) { return r < nrows ? int(r * p.ldb) : -1; }, wave, lane);
-  // scales of a step: wave w < BM / 64 loads A's entries 64 w .., the next BN / 64 waves B's
-  constexpr int QA = BM / 64, QB = BN / 64, QW = (QA + QB + WAVES - 1) / WAVES;
   const uint32_t base = lds_addr(smem);
-  const i32x4 ra = make_rsrc(p.SA, uint32_t(p.ksteps) * p.M * 4u);
   const int nblocks = (p.N + 127) / 128;
-  const i32x4 rb = make_rsrc(p.SB, uint32_t(p.ksteps) * uint32_t(B_TILE ? p.N : nblocks) * 4u);
-  auto issue = [&](int s, int kt) {
+  const bool sis_a = wave < 4;
+  const i32x4 rs = sis_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
+                         : make_rsrc(p.SB, uint32_t(p.ksteps) * uint32_t(B_TILE ? p.N : nblocks) * 4u);
+  const int sr = (wave & 3) * 64 + lane;
+  const int sstep = sis_a ? p.ldsa * 4 : B_TILE ? p.N * 4 : 4;
+  const int soff = sr >= (sis_a ? mrows : nrows) ? int(0x80000000u)
+                   : sis_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ksteps * 4;
+  // Loads of step kt into stage s, the q-th of nine; past the last step they miss every
+  // buffer (no traffic).
+  constexpr int NL = decltype(sa)::NI + decltype(sb)::NI + 1;
+  auto issue1 = [&](int s, int kt, int q) __attribute__((always_inline)) {
     const uint32_t st = base + s * STAGE;
-    sa.issue(st, wave, kt);
-    sb.issue(st + A_BYTES, wave, kt);
+    const bool there = kt < p.ksteps;
+    constexpr int NA = decltype(sa)::NI, NBI = decltype(sb)::NI;
+    const int kb = there ? kt * 128 : 0x40000000;
+    if (q < NA) dma16(sa.rsrc, st + uint32_t(wave * NA + q) * 1024u, sa.vb[q] + kb);
+    else if (q < NA + NBI)
+      dma16(sb.rsrc, st + A_BYTES + uint32_t(wave * NBI + q - NA) * 1024u, sb.vb[q - NA] + kb);
+    else dma4(rs, st + A_BYTES + B_BYTES + wave * 256, there ? soff + kt * sstep : int(0x80000000u));
+  };
+  auto issue = [&](int s, int kt) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < QW; ++u) {
-      const int q = wave + u * WAVES;
-      const uint32_t dst = st + A_BYTES + B_BYTES + q * 256;
-      if (q < QA) {
-        const int r = q * 64 + lane;
-        dma4(ra, dst, r < mrows ? (kt * p.M + m0 + r) * 4 : int(0x80000000u));
-      } else if (q < QA + QB) {
-        const int r = (q - QA) * 64 + lane;
-        int off = int(0x80000000u);
-        if (r < nrows) off = B_TILE ? (kt * p.N + n0 + r) * 4 : ((n0 + r) / 128 * p.ksteps + kt) * 4;
-        dma4(rb, dst, off);
-      }
+    for (int q = 0; q < NL; ++q) issue1(s, kt, q);
+  };
+  f32x4 acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{};
+  // fragments of a stage: chunks g and g + 4 of the lane's row
+  const int sw = (l16 >> 1) & 7;
+  const char* f0 = smem + l16 * 128 + ((g ^ sw) << 4);
+  const char* f1 = smem + l16 * 128 + (((g + 4) ^ sw) << 4);
+  auto frag = [&](int at) __attribute__((always_inline)) {
+    const i32x4 x = *reinterpret_cast<const i32x4*>(f0 + at);
+    const i32x4 y = *reinterpret_cast<const i32x4*>(f1 + at);
+    return i32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+  const char* sap = smem + A_BYTES + B_BYTES + (wm * 128 + l16) * 4;
+  const char* sbp = smem + A_BYTES + B_BYTES + BM * 4 + (wn * 64 + (B_TILE ? 4 * g : 0)) * 4;
+  auto frag_a = [&](int st, int i) __attribute__((always_inline)) { return frag(st + (wm * 128 + i * 16) * 128); };
+  auto frag_b = [&](int st, int j) __attribute__((always_inline)) {
+    return frag(st + A_BYTES + (wn * 64 + j * 16) * 128);
+  };
+  auto scale_a = [&](int st, int i) __attribute__((always_inline)) {
+    return *reinterpret_cast<const float*>(sap + st + i * 64);
+  };
+  constexpr int NS = B_TILE ? NB : 1;
+  using SB_ = typename std::conditional<B_TILE, f32x4, float>::type;
+  auto scale_b = [&](int st, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<const SB_*>(sbp + st + j * 64);
+  };
+  i32x8 b[NB], a;
+  SB_ sbv[NS];
+  float sav;
+  auto open = [&](int st) __attribute__((always_inline)) {
+    a = frag_a(st, 0);
+    sav = scale_a(st, 0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) b[j] = frag_b(st, j);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) sbv[j] = scale_b(st, j);
+  };
+  auto mfma = [&](const i32x8& x, const i32x8& y) __attribute__((always_inline)) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{}, 0, 0, 0, 0, 0, 0);
+  };
+  auto promote = [&](int i, int j, const f32x4& part, float sr_) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float sc;
+      if constexpr (B_TILE) sc = sr_ * sbv[j][e]; else sc = sr_ * sbv[0];
+      acc[i][j][e] = __builtin_fmaf(part[e], sc, acc[i][j][e]);
     }
   };
-  f32x16 acc[WMT][WNT];
-  zero(acc);
-  if (p.ksteps > 0) issue(0, 0);
-  for (int kt = 0; kt < p.ksteps; ++kt) {
+  // One 16-row block of A against the step's four of B, the block after it on the way.
+  // Each product's run sums wait a whole block in P before they are promoted, between the
+  // next block's products: a wave that promotes right behind its own product stalls on it.
+  f32x4 P[NB];
+  float sp = 0.f;
+  auto row = [&](int st, int i, bool more) __attribute__((always_inline)) {
+    i32x8 an = a;
+    float sn = sav;
+    if (more) {
+      an = frag_a(st, i + 1);
+      sn = scale_a(st, i + 1);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const f32x4 q = mfma(b[j], a);
+      if (i > 0) promote(i - 1, j, P[j], sp);
+      P[j] = q;
+    }
+    sp = sav;
+    a = an;
+    sav = sn;
+    if (more) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, B_TILE ? 8 : 5, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto rest = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) promote(i, j, P[j], sp);
+  };
+  // the last step's codes behind column K become 0, once its stage has arrived
+  const bool tail = p.K % 128 != 0;
+  auto mend = [&](int st) __attribute__((always_inline)) {
+    const int kr = p.K % 128;
+    for (int r = threadIdx.x; r < BM + BN; r += 512) {
+      char* at = smem + st + r * 128;  // B's rows follow A's
+      const int w8 = swz_k(r & 255);
+      for (int c = kr >> 4; c < 8; ++c) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(at + ((c ^ w8) << 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int keep = kr - c * 16 - 4 * j;  // bytes of this word that exist
+          if (keep <= 0) w[j] = 0;
+          else if (keep < 4) w[j] &= (1u << (8 * keep)) - 1;
+        }
+      }
+    }
+    __syncthreads();
+  };
+  issue(0, 0);
+  wait_vmcnt<0>();
+  __builtin_amdgcn_s_barrier();
+  if (tail && p.ksteps == 1) mend(0);
+  open(0);
+  int kt = 0, st = 0;
+  const int straight = p.ksteps - 1 - (tail ? 1 : 0);  // steps whose successor needs no mending
+  for (; kt < straight; ++kt) {
+    const int sn = STAGE - st;
+#pragma unroll
+    for (int i = 0; i < MB - 3; ++i) {
+      // the next step's loads, spread: in one burst they hold up the fragment reads
+      // behind the barrier
+      if (i * 2 < NL) issue1(st ? 0 : 1, kt + 1, i * 2);
+      if (i * 2 + 1 < NL) issue1(st ? 0 : 1, kt + 1, i * 2 + 1);
+      row(st, i, true);
+    }
+    // with the last two blocks of A in registers the stage is read: the next one takes
+    // over, its fragments replacing those of B as the last products release them
+    const i32x8 a6 = frag_a(st, MB - 2), a7 = frag_a(st, MB - 1);
+    const float s6 = scale_a(st, MB - 2), s7 = scale_a(st, MB - 1);
+    row(st, MB - 3, false);
+    wait_lgkm0();
     wait_vmcnt<0>();
     __builtin_amdgcn_s_barrier();
-    if (kt + 1 < p.ksteps) issue((kt + 1) & 1, kt + 1);
-    char* ta = smem + (kt & 1) * STAGE;
-    char* tb = ta + A_BYTES;
-    const int kr = p.K - kt * 128;
-    if (kr < 128) {  // the last step: codes behind column K become 0
-      for (int r = threadIdx.x; r < BM + BN; r += TL::THREADS) {
-        char* row = ta + r * 128;  // B's rows follow A's
-        const int sw = swz_k(r < BM ? r : r - BM);
-        for (int c = kr >> 4; c < 8; ++c) {
-          uint32_t* w = reinterpret_cast<uint32_t*>(row + ((c ^ sw) << 4));
+    a = frag_a(sn, 0);
+    sav = scale_a(sn, 0);
+    f32x4 P6, P7;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int keep = kr - c * 16 - 4 * j;  // bytes of this word that exist
-            if (keep <= 0) w[j] = 0;
-            else if (keep < 4) w[j] &= (1u << (8 * keep)) - 1;
+    for (int j = 0; j < NB; ++j) {
+      const f32x4 q6 = mfma(b[j], a6), q7 = mfma(b[j], a7);
+      b[j] = frag_b(sn, j);
+      if (j == 0) {
+        rest(MB - 3);
+      } else {
+        promote(MB - 2, j - 1, P6, s6);
+        promote(MB - 1, j - 1, P7, s7);
+      }
+      P6 = q6;
+      P7 = q7;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    promote(MB - 2, NB - 1, P6, s6);
+    promote(MB - 1, NB - 1, P7, s7);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) sbv[j] = scale_b(sn, j);
+    st = sn;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (tail && p.ksteps > 1) {
+    issue(st ? 0 : 1, kt + 1);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) row(st, i, i + 1 < MB);
+    rest(MB - 1);
+    wait_lgkm0();
+    wait_vmcnt<0>();
+    __builtin_amdgcn_s_barrier();
+    st = STAGE - st;
+    mend(st);
+    open(st);
+  }
+#pragma unroll
+  for (int i = 0; i < MB; ++i) row(st, i, i + 1 < MB);
+  rest(MB - 1);
+  // Epilogue: the whole bf16 tile through LDS, whole rows out
+  __syncthreads();
+  BandTile<2> t{smem, BN};
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      *reinterpret_cast<uint2*>(t.at(wm * 128 + i * 16 + l16, wn * 64 + j * 16 + 4 * g)) =
+          pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+  __syncthreads();
+  uint16_t* c = static_cast<uint16_t*>(p.C) + int64_t(m0) * p.ldc + n0;
+#pragma unroll 4
+  for (int k = threadIdx.x; k < BM * 32; k += 512) {
+    const int row = k >> 5, ch = k & 31;
+    if (row >= mrows || ch * 8 >= nrows) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(smem + row * 512 + ((ch ^ (row & 31)) << 4));
+    uint16_t* dst = c + row * p.ldc + ch * 8;
+    if (ch * 8 + 8 <= nrows) {
+      store16(dst, v);
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (ch * 8 + e < nrows) dst[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
+  MmArgs p = a;
+  p.ntm = int(ceil_div(p.M, 256));
+  p.ntn = int(ceil_div(p.N, 256));
+  const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
+  prof_begin("block_mm_large", s);
+  if (b_tile) block_mm_large_kernel<true><<<grid, 512, 0, s>>>(p);
+  else block_mm_large_kernel<false><<<grid, 512, 0, s>>>(p);
+  prof_end(s);
+  return launched();
+}
+
+// Products of a medium size, and all but the smallest with fp32 results: BM x BN tiles of WGM x WGN
+// waves in 16 x 16 blocks, KG such groups a workgroup that share the runs of the contraction and
+// are joined at the end.  Where tiles or steps are few, a step's latency is what it costs: a
+// ring of four stages is filled four steps ahead, a step's fragments are read one step before
+// their products, and a product's sums are promoted one step behind it.
+template <int BM_, int BN_, int WGM_, int WGN_, int KG_>
+struct MidTile {
+  static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, KG = KG_;
+  static constexpr int WAVES = WGM * WGN, THREADS = 64 * WAVES * KG, MB = BM / WGM / 16, NB = BN / WGN / 16;
+};
+
+template <class TL, bool B_TILE, bool OUT_F32>
+__global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
+  constexpr int BM = TL::BM, BN = TL::BN, KG = TL::KG, WAVES = TL::WAVES, MB = TL::MB, NB = TL::NB;
+  constexpr int S = 4, A_BYTES = BM * 128, BYTES = (BM + BN) * 128, STAGE = BYTES + (BM + BN) * 4, RING = S * STAGE;
+  constexpr int LDR = BN + 4;  // join: rows apart in banks
+  static_assert(RING >= BM * LDR * 4, "the join fits a group's ring");
+  __shared__ __attribute__((aligned(1024))) char smem[KG * RING];
+  const int l = xcd_remap(blockIdx.x, gridDim.x);
+  int mt, nt;
+  wgrad_mn(l, p.ntm, p.ntn, mt, nt);
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = wv / WAVES, wave = wv % WAVES, wm = wave / TL::WGN, wn = wave % TL::WGN;
+  const int m0 = mt * BM, n0 = nt * BN;
+  const int mrows = min(BM, p.M - m0), nrows = min(BN, p.N - n0);
+  const int kbytes = (p.K + 15) & ~15;
+  char* ring = smem + kg * RING;
+  KStager<BM, WAVES, 128> sa;
+  sa.init(make_rsrc(p.A + int64_t(m0) * p.lda, uint32_t((mrows - 1) * p.lda + kbytes)),
+          [&](int r) { return r < mrows ? int(r * p.lda) : -1; }, wave, lane);
+  KStager<BN, WAVES, 128> sb;
+  sb.init(make_rsrc(p.B + int64_t(n0) * p.ldb, uint32_t((nrows - 1) * p.ldb + kbytes)),
+          [&](int r) { return r < nrows ? int(r * p.ldb) : -1; }, wave, lane);
+  constexpr int NA = decltype(sa)::NI, NBI = decltype(sb)::NI, NI = NA + NBI + 1;
+  const int nblocks = (p.N + 127) / 128;
+  // scales, 64 a load; with more waves than loads some come twice
+  constexpr int QA = BM / 64, QB = BN / 64;
+  static_assert(QA + QB <= WAVES, "a load of scales a wave");
+  const int sq = wave % (QA + QB);
+  const bool of_a = sq < QA;
+  const i32x4 rs = of_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
+                        : make_rsrc(p.SB, uint32_t(p.ksteps) * uint32_t(B_TILE ? p.N : nblocks) * 4u);
+  const int sr = (of_a ? sq : sq - QA) * 64 + lane;
+  const int sstep = of_a ? p.ldsa * 4 : B_TILE ? p.N * 4 : 4;
+  const int soff = sr >= (of_a ? mrows : nrows) ? int(0x80000000u)
+                   : of_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ksteps * 4;
+  const uint32_t base = lds_addr(ring);
+  // the group's i-th step is run i KG + kg; one past the last misses every buffer and loads zeros
+  auto issue = [&](int i) __attribute__((always_inline)) {
+    const uint32_t st = base + (i % S) * STAGE;
+    const int kt = i * KG + kg;
+    const bool there = kt < p.ksteps;
+    const int kb = there ? kt * 128 : 0x40000000;
+#pragma unroll
+    for (int j = 0; j < NA; ++j) dma16(sa.rsrc, st + uint32_t(wave * NA + j) * 1024u, sa.vb[j] + kb);
+#pragma unroll
+    for (int j = 0; j < NBI; ++j)
+      dma16(sb.rsrc, st + A_BYTES + uint32_t(wave * NBI + j) * 1024u, sb.vb[j] + kb);
+    dma4(rs, st + BYTES + sq * 256, there ? soff + kt * sstep : int(0x80000000u));
+  };
+  const int sw = (l16 >> 1) & 7;
+  const int f0 = l16 * 128 + ((g4 ^ sw) << 4), f1 = l16 * 128 + (((g4 + 4) ^ sw) << 4);
+  using SB_ = typename std::conditional<B_TILE, f32x4, float>::type;
+  struct Step {
+    i32x8 a[MB], b[NB];
+    float sa[MB];
+    SB_ sb[NB];
+  };
+  auto read = [&](int i, Step& x) __attribute__((always_inline)) {
+    const char* st = ring + (i % S) * STAGE;
+    const float* sc = reinterpret_cast<const float*>(st + BYTES);
+    auto frag = [&](const char* rows) __attribute__((always_inline)) {
+      const i32x4 u = *reinterpret_cast<const i32x4*>(rows + f0), v = *reinterpret_cast<const i32x4*>(rows + f1);
+      return i32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+    };
+#pragma unroll
+    for (int q = 0; q < MB; ++q) {
+      const int r = (wm * MB + q) * 16;
+      x.a[q] = frag(st + r * 128);
+      x.sa[q] = sc[r + l16];
+    }
+#pragma unroll
+    for (int q = 0; q < NB; ++q) {
+      const int r = (wn * NB + q) * 16;
+      x.b[q] = frag(st + A_BYTES + r * 128);
+      x.sb[q] = *reinterpret_cast<const SB_*>(sc + BM + r + (B_TILE ? 4 * g4 : 0));
+    }
+  };
+  f32x4 acc[MB][NB] = {}, P[MB][NB] = {};
+  float psa[MB] = {};
+  SB_ psb[NB] = {};
+  auto promote = [&](int i, int j) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float s;
+      if constexpr (B_TILE) s = psa[i] * psb[j][e]; else s = psa[i] * psb[j];
+      acc[i][j][e] = __builtin_fmaf(P[i][j][e], s, acc[i][j][e]);
+    }
+  };
+  auto promote_all = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) promote(i, j);
+  };
+  auto multiply = [&](const Step& x) __attribute__((always_inline)) {
+    if constexpr (OUT_F32) {
+      promote_all();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        bf16x8 wb[NB];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) wb[j] = widen(x.b[j], e);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          const bf16x8 wa = widen(x.a[i], e);
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            P[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, e ? P[i][j] : f32x4{}, 0, 0, 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          promote(i, j);
+          P[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.b[j], x.a[i], f32x4{}, 0, 0, 0, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) psa[i] = x.sa[i];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) psb[j] = x.sb[j];
+  };
+  const int n = (p.ksteps + KG - 1) / KG;  // steps a group
+  const bool tail = p.K % 128 != 0;
+  // stage i has arrived for every wave; the last run's codes behind column K become 0
+  auto arrive = [&](int i) __attribute__((always_inline)) {
+    wait_lgkm0();
+    wait_vmcnt<(S - 2) * NI>();
+    __builtin_amdgcn_s_barrier();
+    if (tail && i == n - 1) {
+      if (i * KG + kg == p.ksteps - 1) {
+        const int kr = p.K % 128;
+        for (int r = wave * 64 + lane; r < BM + BN; r += 64 * WAVES) {  // B's rows follow A's
+          char* at = ring + (i % S) * STAGE + r * 128;
+          const int w8 = swz_k(r < BM ? r : r - BM);
+          for (int c = kr >> 4; c < 8; ++c) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(at + ((c ^ w8) << 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int keep = kr - c * 16 - 4 * j;  // bytes of this word that exist
+              if (keep <= 0) w[j] = 0;
+              else if (keep < 4) w[j] &= (1u << (8 * keep)) - 1;
+            }
           }
         }
       }
-      __syncthreads();
+      wait_lgkm0();
+      __builtin_amdgcn_s_barrier();
     }
-    const float* sca = reinterpret_cast<const float*>(tb + B_BYTES);
-    const float* scb = sca + BM;
-    i32x8 b0[WNT], b1[WNT];
+  };
 #pragma unroll
-    for (int j = 0; j < WNT; ++j) {
-      const int n = wn * WN + j * 32 + (lane & 31);
-      b0[j] = frag_q(tb, n, 0, lane);
-      b1[j] = frag_q(tb, n, 1, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < WMT; ++i) {
-      const int r = wm * WM + i * 32 + (lane & 31);
-      const i32x8 a0 = frag_q(ta, r, 0, lane), a1 = frag_q(ta, r, 1, lane);
-      const float sr = sca[r];
-#pragma unroll
-      for (int j = 0; j < WNT; ++j) {
-        f32x16 part = {};
-        if constexpr (OUT_F32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b0[j], e), widen(a0, e), part, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            part = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(b1[j], e), widen(a1, e), part, 0, 0, 0);
-        } else {
-          part = mfma_q(b0[j], a0, part);
-          part = mfma_q(b1[j], a1, part);
-        }
-        const float* sn = scb + wn * WN + j * 32;
-        if constexpr (B_TILE) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[i][j][4 * g + e] = __builtin_fmaf(part[4 * g + e], sr * sn[acc_col(g, lane) + e],
-                                                    acc[i][j][4 * g + e]);
-        } else {
-          const float s = sr * sn[0];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(part[e], s, acc[i][j][e]);
-        }
-      }
-    }
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  // here S - 1 stages are on the way; `arrive` lets S - 2 of them be out
+  Step x0, x1;
+  arrive(0);
+  issue(S - 1);
+  read(0, x0);
+  // step i: the next stage arrives, the one just read takes the loads four steps on
+  auto step = [&](int i, const Step& cur, Step& nxt) __attribute__((always_inline)) {
+    arrive(i + 1);
+    issue(i + S);
+    read(i + 1, nxt);
+    multiply(cur);
+  };
+  int i = 0;
+  for (; i + 2 < n; i += 2) {
+    step(i, x0, x1);
+    step(i + 1, x1, x0);
   }
-  // Epilogue: bands of 32 rows a wave row through LDS, whole rows out
+  if (i + 1 < n) {
+    step(i, x0, x1);
+    multiply(x1);
+  } else {
+    multiply(x0);
+  }
+  promote_all();
+  wait_vmcnt<0>();  // loads that missed still write their zeros
   __syncthreads();
-  constexpr int VE = 16 / ES;  // elements of a 16-byte chunk
+  float* red = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int r = 0; r < MB; ++r)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      *reinterpret_cast<f32x4*>(red + ((wm * MB + r) * 16 + l16) * LDR + (wn * NB + j) * 16 + 4 * g4) = acc[r][j];
+  __syncthreads();
   using T = typename std::conditional<OUT_F32, float, uint16_t>::type;
+  constexpr int VE = 16 / sizeof(T);
   T* c = static_cast<T*>(p.C) + int64_t(m0) * p.ldc + n0;
 #pragma unroll
-  for (int i = 0; i < WMT; ++i) {
-    BandTile<ES> t{smem, BN};
-    const int rr = wm * 32 + (lane & 31);
+  for (int e = threadIdx.x; e < BM * BN / VE; e += TL::THREADS) {
+    const int row = e / (BN / VE), col = e % (BN / VE) * VE;
+    if (row >= mrows || col >= nrows) continue;
+    float v[VE];
 #pragma unroll
-    for (int j = 0; j < WNT; ++j)
+    for (int q = 0; q < VE; q += 4) {
+      f32x4 t = *reinterpret_cast<const f32x4*>(smem + (row * LDR + col + q) * 4);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x16& a = acc[i][j];
-        char* dst = t.at(rr, wn * WN + j * 32 + acc_col(g, lane));
-        if constexpr (OUT_F32)
-          *reinterpret_cast<float4*>(dst) = make_float4(a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]);
-        else
-          *reinterpret_cast<uint2*>(dst) = pack4(a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]);
-      }
-    __syncthreads();
-    constexpr int CH = BN / VE, SW = (CH < 32 ? CH : 32) - 1;
-    for (int k = threadIdx.x; k < TL::WGM * 32 * CH; k += TL::THREADS) {
-      const int b = k / CH, ch = k - b * CH;
-      const int row = (b >> 5) * WM + i * 32 + (b & 31), col = ch * VE;
-      if (row >= mrows || col >= nrows) continue;
-      uint4 v = *reinterpret_cast<const uint4*>(smem + b * CH * 16 + ((ch ^ (b & SW)) << 4));
-      T* dst = c + row * p.ldc + col;
-      if (p.vec && col + VE <= nrows) {
-        if constexpr (OUT_F32) {
-          if (p.add) {
-            const float4 o = *reinterpret_cast<const float4*>(dst);
-            v = make_uint4(__float_as_uint(__uint_as_float(v.x) + o.x), __float_as_uint(__uint_as_float(v.y) + o.y),
-                           __float_as_uint(__uint_as_float(v.z) + o.z), __float_as_uint(__uint_as_float(v.w) + o.w));
-          }
+      for (int k = 1; k < KG; ++k) t += *reinterpret_cast<const f32x4*>(smem + k * RING + (row * LDR + col + q) * 4);
+      v[q] = t[0]; v[q + 1] = t[1]; v[q + 2] = t[2]; v[q + 3] = t[3];
+    }
+    T* dst = c + row * p.ldc + col;
+    if (col + VE <= nrows) {
+      if constexpr (OUT_F32) {
+        if (p.add) {
+          float o[4];
+          as_floats<float>(load16(dst), o);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] += o[q];
         }
-        *reinterpret_cast<uint4*>(dst) = v;
+        store16(dst, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                __float_as_uint(v[3])));
       } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        store16(dst, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                pack_bf16x2(v[6], v[7])));
+      }
+    } else {
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-          if (col + e < nrows) {
-            if constexpr (OUT_F32) dst[e] = __uint_as_float(w[e]) + (p.add ? dst[e] : 0.f);
-            else dst[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
-          }
+      for (int q = 0; q < VE; ++q)
+        if (col + q < nrows) {
+          if constexpr (OUT_F32) dst[q] = p.add ? dst[q] + v[q] : v[q];
+          else dst[q] = uint16_t(pack_bf16x2(v[q], 0.f));
+        }
+    }
+  }
+}
+
+template <class TL>
+int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
+  MmArgs p = a;
+  p.ntm = int(ceil_div(p.M, TL::BM));
+  p.ntn = int(ceil_div(p.N, TL::BN));
+  const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
+  prof_begin("block_mm_mid", s);
+  if (b_tile) {
+    if (f32) block_mm_mid_kernel<TL, true, true><<<grid, TL::THREADS, 0, s>>>(p);
+    else block_mm_mid_kernel<TL, true, false><<<grid, TL::THREADS, 0, s>>>(p);
+  } else {
+    if (f32) block_mm_mid_kernel<TL, false, true><<<grid, TL::THREADS, 0, s>>>(p);
+    else block_mm_mid_kernel<TL, false, false><<<grid, TL::THREADS, 0, s>>>(p);
+  }
+  prof_end(s);
+  return launched();
+}
+
+// Small products: 16 x 16 tiles of C, `wk` waves on a tile, its runs split over them and their
+// sums joined in LDS in wave order.  B goes from memory to registers, a run ahead.  A as codes
+// does too; A as values is quantised by the workgroup into LDS first (16 rows, up to kDirectK
+// columns), while the first of B is on its way, so that the call is one launch.  Lane l of a
+// fragment holds row l & 15 and bytes 32 (l >> 4) .. + 31 of a run, for A and B alike; with B as
+// the first operand a lane's results are row l & 15 of C and columns 4 (l >> 4) .. + 3.
+// Every workgroup of a row of tiles quantises its A again, which costs less than a second launch
+// up to the size in use_direct.
+enum AKind { A_CODES = 0, A_BF16 = 1, A_F32 = 2 };
+constexpr int kDirectWaves = 16, kDirectK = 4096;
+
+struct DirectArgs {
+  MmArgs m;
+  const void* X;  // A as values
+  int64_t ldx;
+  int wk;         // waves a tile
+};
+
+// A quarter of a run of codes of a row on its way, from column k (k % 32 == 0).
+struct RunPart {
+  i32x4 c[2];
+  int left;  // codes that exist from k on
+  __device__ __forceinline__ void load(const uint8_t* row, int k, int K, bool ok) {
+    left = ok ? K - k : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c[i] = i32x4{};
+      if (left > 16 * i) c[i] = *reinterpret_cast<const i32x4*>(row + k + 16 * i);
+    }
+  }
+  __device__ __forceinline__ i32x8 codes() const {  // 0 behind column K
+    i32x8 r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int v = c[j >> 2][j & 3], keep = left - 4 * j;
+      r[j] = keep >= 4 ? v : keep <= 0 ? 0 : v & int((1u << (8 * keep)) - 1);
+    }
+    return r;
+  }
+};
+
+template <int AK, bool B_TILE, bool OUT_F32>
+__global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectArgs p) {
+  constexpr bool VALUES = AK != A_CODES;
+  constexpr int LDR = 20;           // join: rows apart in banks
+  constexpr int LDA = kDirectK + 16;  // staged codes: 16 rows on 64 banks
+  constexpr int STAGED = VALUES ? 16 * LDA + kDirectK / 128 * 64 : 0, JOIN = kDirectWaves * 16 * LDR * 4;
+  __shared__ __attribute__((aligned(16))) char smem[STAGED > JOIN ? STAGED : JOIN];
+  const MmArgs& q = p.m;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wt = wave / p.wk, kw = wave - wt * p.wk;  // tile of the workgroup, share of its runs
+  const int mt = blockIdx.x % q.ntm, nt = blockIdx.x / q.ntm * int((blockDim.x >> 6) / p.wk) + wt;
+  const int m = mt * 16 + l16, n = nt * 16 + l16, nc = nt * 16 + 4 * g;
+  const uint8_t* arow = q.A + int64_t(m) * q.lda;
+  const uint8_t* brow = q.B + int64_t(n) * q.ldb;
+  const int nb = min(nt * 16, q.N - 1) >> 7;
+  struct Run {
+    RunPart a, b;
+    float sa, sb[B_TILE ? 4 : 1];
+  };
+  auto load = [&](int kt, Run& r) __attribute__((always_inline)) {
+    const int k = kt * 128 + 32 * g;
+    const bool run = kt < q.ksteps;
+    if constexpr (!VALUES) {
+      r.a.load(arow, k, q.K, m < q.M && run);
+      r.sa = m < q.M && run ? q.SA[int64_t(kt) * q.ldsa + m] : 0.f;
+    }
+    r.b.load(brow, k, q.K, n < q.N && run);
+    if constexpr (B_TILE) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.sb[e] = nc + e < q.N && run ? q.SB[int64_t(kt) * q.N + nc + e] : 0.f;
+    } else {
+      r.sb[0] = q.SB[int64_t(nb) * q.ksteps + min(kt, q.ksteps - 1)];
+    }
+  };
+  Run cur;
+  load(kw, cur);
+  float* scales = reinterpret_cast<float*>(smem + 16 * LDA);  // [run][row]
+  if constexpr (VALUES) {
+    using T = typename std::conditional<AK == A_BF16, uint16_t, float>::type;
+    constexpr int N = 16 / sizeof(T), NP = 8 / N;
+    const T* x = static_cast<const T*>(p.X);
+    const int rows = min(16, q.M - mt * 16), groups = blockDim.x >> 4;
+    const bool wide = q.K >= N;
+    // sixteen lanes a run, in pairs of runs so that two loads are on their way
+    for (int u = threadIdx.x >> 4; u < rows * q.ksteps; u += 2 * groups) {
+      RowPiece<T> raw[2][NP];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int v = u + h * groups, r = v / q.ksteps, c = (v - r * q.ksteps) * 128 + 8 * l16;
+        const T* row = x + int64_t(mt * 16 + r) * p.ldx;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (wide) raw[h][i].load(row, c + i * N, q.K, r < rows, x);
+          else raw[h][i].load_short(row, c + i * N, q.K, r < rows);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int v = u + h * groups, r = v / q.ksteps, kt = v - r * q.ksteps;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          if (wide) raw[h][i].mend(q.K % 128 != 0);
+          as_floats<T>(raw[h][i].v, f + i * N);
+        }
+        const Quant qz(max16(amax8(f)));
+        const uint2 w = make_uint2(qz.codes(f[0], f[1], f[2], f[3]), qz.codes(f[4], f[5], f[6], f[7]));
+        if (r < rows) {
+          *reinterpret_cast<uint2*>(smem + r * LDA + kt * 128 + 8 * l16) = w;
+          if (l16 == 0) scales[kt * 16 + r] = qz.scale;
+        }
       }
     }
     __syncthreads();
   }
+  const int arl = VALUES ? min(l16, q.M - 1 - mt * 16) : 0;  // a row that is staged
+  f32x4 acc = {};
+  for (int kt = kw; kt < q.ksteps; kt += p.wk) {
+    Run next;
+    load(kt + p.wk, next);
+    i32x8 a;
+    float sa;
+    if constexpr (VALUES) {
+      const i32x4* s = reinterpret_cast<const i32x4*>(smem + arl * LDA + kt * 128 + 32 * g);
+      const i32x4 u = s[0], v = s[1];
+      a = i32x8{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+      sa = scales[kt * 16 + arl];
+    } else {
+      a = cur.a.codes();
+      sa = cur.sa;
+    }
+    const i32x8 b = cur.b.codes();
+    f32x4 part = {};
+    if constexpr (OUT_F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b, e), widen(a, e), part, 0, 0, 0);
+    } else {
+      part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, part, 0, 0, 0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], sa * cur.sb[B_TILE ? e : 0], acc[e]);
+    cur = next;
+  }
+  using O = typename std::conditional<OUT_F32, float, uint16_t>::type;
+  O* c = static_cast<O*>(q.C);
+  auto put = [&](int r, int col, float s) __attribute__((always_inline)) {
+    if (r >= q.M || col >= q.N) return;
+    O* dst = c + int64_t(r) * q.ldc + col;
+    if constexpr (OUT_F32) *dst = q.add ? *dst + s : s;
+    else *dst = uint16_t(pack_bf16x2(s, 0.f));
+  };
+  if (p.wk == 1) {  // a tile a wave: nothing to join
+#pragma unroll
+    for (int e = 0; e < 4; ++e) put(m, nc + e, acc[e]);
+    return;
+  }
+  if constexpr (VALUES) __syncthreads();  // the join overwrites the staged codes
+  float* red = reinterpret_cast<float*>(smem);
+  *reinterpret_cast<f32x4*>(red + (wave * 16 + l16) * LDR + 4 * g) = acc;
+  __syncthreads();
+  for (int e = kw * 64 + lane; e < 256; e += p.wk * 64) {
+    const int r = e >> 4, col = e & 15;
+    const float* t = red + (wt * p.wk * 16 + r) * LDR + col;
+    float s = t[0];
+    for (int w = 1; w < p.wk; ++w) s += t[w * 16 * LDR];
+    put(mt * 16 + r, nt * 16 + col, s);
+  }
+}
+
+template <int AK>
+int launch_direct(const DirectArgs& a, bool b_tile, bool f32, hipStream_t s) {
+  DirectArgs p = a;
+  // a power of two of waves on a tile's runs, up to one each; at least eight waves a workgroup, the
+  // rest of them on further tiles (a launch of thousands of single waves is slower than its work)
+  p.wk = 1;
+  while (p.wk < kDirectWaves && p.wk < p.m.ksteps) p.wk *= 2;
+  const int waves = p.wk > 8 ? p.wk : 8;
+  p.m.ntm = int(ceil_div(p.m.M, 16));
+  const unsigned grid = unsigned(p.m.ntm) * unsigned(ceil_div(ceil_div(p.m.N, 16), waves / p.wk));
+  prof_begin("block_direct", s);
+  if (b_tile) {
+    if (f32) block_direct_kernel<AK, true, true><<<grid, 64 * waves, 0, s>>>(p);
+    else block_direct_kernel<AK, true, false><<<grid, 64 * waves, 0, s>>>(p);
+  } else {
+    if (f32) block_direct_kernel<AK, false, true><<<grid, 64 * waves, 0, s>>>(p);
+    else block_direct_kernel<AK, false, false><<<grid, 64 * waves, 0, s>>>(p);
+  }
+  prof_end(s);
+  return launched();
 }
 
 // C = 0: a product over nothing.
@@ -460,22 +1031,76 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
   for (int j = threadIdx.x; j < N; j += 256) row[j] = T(0);
 }
 
-template <class TL>
-int launch_mm(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
-  MmArgs p = a;
-  p.ntm = int(ceil_div(p.M, TL::BM));
-  p.ntn = int(ceil_div(p.N, TL::BN));
-  const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
-  prof_begin("block_mm", s);
-  if (b_tile) {
-    if (f32) block_mm_kernel<TL, true, true><<<grid, TL::THREADS, 0, s>>>(p);
-    else block_mm_kernel<TL, true, false><<<grid, TL::THREADS, 0, s>>>(p);
-  } else {
-    if (f32) block_mm_kernel<TL, false, true><<<grid, TL::THREADS, 0, s>>>(p);
-    else block_mm_kernel<TL, false, false><<<grid, TL::THREADS, 0, s>>>(p);
+// Which kernel a product takes.  Measured on an MI355X (256 CUs, one workgroup of 256 x 256 or 128 x
+// 128, or two of 64 x 64, a CU), in us a round of workgroups with `steps` runs:
+//   256 x 256             5   + 1.72 steps  (4096 x 4096 x 4096 60.5, 16384 x 4096 x 4096 4 x 68)
+//   128 x 128             2.5 + 0.8  steps  (2048 x 2048 x 2048 16.0)
+//   64 x 64, two a CU     2   + 0.5  steps  (2048 x 2048 x 2048 19.6 in two rounds)
+//   64 x 64, two groups   3   + 0.28 steps  (256 x 4096 x 4096 11.1, 12.6 with one group)
+// The sizes' best is the least of these, and so for fp32 results, whose steps all take about 1.6
+// times as long (there is no 256 x 256 kernel for them).  Where a few rows past a multiple of 256
+// cost a further round, they go to a launch of 64 x 64 tiles.
+enum MmKind { MM_LARGE, MM_128, MM_64, MM_64X2 };
+struct MmPlan {
+  MmKind kind;
+  double us;
+  int peel;  // rows at the end that take a launch of their own
+};
+
+MmPlan mm_plan(long long M, long long N, int steps, bool f32) {
+  constexpr int kCus = 256;
+  const auto tiles = [&](long long m, int b) { return ceil_div(m, b) * ceil_div(N, b); };
+  const auto large = [&](long long m) { return ceil_div(tiles(m, 256), kCus) * (5 + 1.72 * steps); };
+  const auto small = [&](long long m) {
+    const long long t = tiles(m, 64);
+    return t <= kCus ? MmPlan{MM_64X2, 3 + 0.28 * steps, 0}
+                     : MmPlan{MM_64, ceil_div(t, 2 * kCus) * (2 + 0.5 * steps), 0};
+  };
+  MmPlan best = small(M);
+  const double mid = ceil_div(tiles(M, 128), kCus) * (2.5 + 0.8 * steps);
+  if (mid < best.us) best = {MM_128, mid, 0};
+  if (f32) return best;
+  if (large(M) < best.us) best = {MM_LARGE, large(M), 0};
+  const int rest = int(M % 256);
+  if (M > 256 && rest > 0 && rest <= 64) {
+    const double us = large(M - rest) + small(rest).us + 1.5;
+    if (us < best.us) best = {MM_LARGE, us, rest};
   }
-  prof_end(s);
-  return launched();
+  return best;
+}
+
+int launch_mm(const MmArgs& p, bool b_tile, bool f32, hipStream_t s) {
+  const MmPlan plan = mm_plan(p.M, p.N, p.ksteps, f32);
+  switch (plan.kind) {
+    case MM_64X2: return launch_mm_mid<MidTile<64, 64, 2, 2, 2>>(p, b_tile, f32, s);
+    case MM_64: return launch_mm_mid<MidTile<64, 64, 2, 2, 1>>(p, b_tile, f32, s);
+    case MM_128: return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
+    case MM_LARGE: break;
+  }
+  if (plan.peel == 0) return launch_mm_large(p, b_tile, s);
+  MmArgs head = p, rest = p;
+  head.M = p.M - plan.peel;
+  rest.M = plan.peel;
+  rest.A += int64_t(head.M) * p.lda;
+  rest.SA += head.M;
+  rest.C = static_cast<uint16_t*>(p.C) + int64_t(head.M) * p.ldc;
+  if (const int rc = launch_mm_large(head, b_tile, s)) return rc;
+  return launch_mm(rest, b_tile, f32, s);
+}
+
+// Whether the one-launch kernel takes the product: for values, up to the work of quantising A again
+// in every workgroup (in runs of 128 values: 64 x 1024 x 1024, 32768 runs, takes 5.8 us against 7.1
+// in two launches, 128 x 1024 x 1024, 65536, 7.9 against 7.2 and a launch's host time, 16 x 4096 x 4096, 131072,
+// 13.9 against 12.1); for codes, up to 4096 runs of tiles (128 x 1024 x 1024: 4.5 us against 4.9; 256 x
+// 1024 x 1024: 7.6 against 5.0), and with one row of tiles up to 16384 (16 x 4096 x 4096: 7.3 against 9.8).
+bool use_direct(long long M, long long N, long long K, bool values) {
+  const long long steps = ceil_div(K, 128), tm = ceil_div(M, 16), tn = ceil_div(N, 16);
+  if (!values) return tm * tn * steps <= (M <= 16 ? 16384 : 4096);
+  if (K > kDirectK) return false;
+  long long wk = 1;
+  while (wk < kDirectWaves && wk < steps) wk *= 2;
+  const long long groups = ceil_div(tn, wk > 8 ? 1 : 8 / wk);  // workgroups a row of tiles
+  return tm * groups * (M < 16 ? M : 16) * steps <= 65536;
 }
 
 // ---------------------------------------------------------------------------
@@ -540,7 +1165,7 @@ int moe_block_quant(const moe_block_quant_desc* q, const void* x, uint8_t* codes
       (codes_t && q->ld_codes_t >= kMaxStride) ||
       ceil_div(q->rows, 128) * ceil_div(q->cols, 128) >= (1LL << 31))
     return MOE_EUNSUPPORTED;
-  QuantArgs a = quant_args(x, q->in_type, q->rows, q->cols, q->ld_in);
+  QuantArgs a = quant_args(x, q->rows, q->cols, q->ld_in);
   a.q = codes;
   a.ldq = q->ld_codes;
   a.sc = scales;
@@ -590,6 +1215,7 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
   p.ksteps = int(ceil_div(m->K, 128));
   p.A = static_cast<const uint8_t*>(a);
   p.SA = a_scales;
+  p.ldsa = m->M;
   p.lda = m->lda;
   p.B = b;
   p.SB = b_scales;
@@ -597,12 +1223,18 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
   p.C = c;
   p.ldc = m->ldc;
   p.add = (m->flags & MOE_MM_ACCUMULATE) != 0;
-  p.vec = aligned_to(c, 16) && m->ldc * int64_t(type_bytes(m->c_type)) % 16 == 0;
+  const bool bt = m->b_scale == MOE_SCALE_TILE;
+  if (use_direct(m->M, m->N, m->K, quant)) {
+    const DirectArgs dp{p, a, m->lda, 0};
+    if (!quant) return launch_direct<A_CODES>(dp, bt, f32, s);
+    if (m->a_type == MOE_TYPE_BF16) return launch_direct<A_BF16>(dp, bt, f32, s);
+    return launch_direct<A_F32>(dp, bt, f32, s);
+  }
   if (quant) {
     char* sc = static_cast<char*>(scratch);
     size_t at;
     (void)mm_quant_bytes(*m, &at);
-    QuantArgs q = quant_args(a, m->a_type, m->M, m->K, m->lda);
+    QuantArgs q = quant_args(a, m->M, m->K, m->lda);
     q.q = reinterpret_cast<uint8_t*>(sc);
     q.ldq = code_ld(m->K);
     q.sc = reinterpret_cast<float*>(sc + at);
@@ -611,7 +1243,7 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
     p.lda = q.ldq;
     p.SA = q.sc;
   }
-  return launch_mm<Tile<128, 128, 2, 2, 2>>(p, m->b_scale == MOE_SCALE_TILE, f32, s);
+  return launch_mm(p, bt, f32, s);
 }
 
 }  // extern "C"

@@ -203,16 +203,23 @@ def test_product(M, N, K, b_scale):
     _check_mm(M, N, K, b_scale, F32, seed=M + N + K, ldc=N + 3, off=1)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 64, 4096), (7, 100, 700), (150, 300, 1500), (300, 260, 128), (600, 700, 200)])
+@pytest.mark.parametrize("M,N,K", [(1, 64, 4096), (7, 100, 700), (150, 300, 1500), (300, 260, 128), (600, 700, 200),
+                                   (2100, 1030, 130)])
 def test_product_added_to_c(M, N, K):
     _check_mm(M, N, K, TILE, F32, seed=3, add=True)
     _check_mm(M, N, K, BLOCK, F32, seed=4, add=True, ldc=N + 1)
 
 
-@pytest.mark.parametrize("M,N,K", [(2100, 1030, 300), (1030, 2100, 1153), (4100, 512, 128)])
+# every tile size and its edges: 64 x 64 (with and without the split over two groups), 128 x 128,
+# 256 x 256 (one step and several, whole and partial last runs), and a few rows past a multiple of 256
+@pytest.mark.parametrize("M,N,K", [(2000, 900, 300), (2000, 900, 128), (2000, 900, 40), (2100, 1030, 300),
+                                   (1030, 2100, 1153), (4100, 512, 128), (700, 256, 1040), (300, 500, 131),
+                                   (2900, 2890, 256), (2900, 2890, 100), (2890, 2900, 300), (2900, 2890, 129),
+                                   (2816, 2816, 1000), (8195, 2048, 128), (8195, 2050, 140)])
 def test_product_of_many_tiles(M, N, K):
     _check_mm(M, N, K, BLOCK, BF, seed=5)
-    _check_mm(M, N, K, TILE, F32, seed=6)
+    _check_mm(M, N, K, TILE, BF, seed=6)
+    _check_mm(M, N, K, BLOCK if K % 2 else TILE, F32, seed=6)
 
 
 def test_empty_contraction():
@@ -229,7 +236,8 @@ def test_empty_contraction():
 def test_values_give_what_their_codes_give(M, t):
     """A call that quantises A itself against moe_block_quant and the product of the codes: the same
     bits where the two take the same path, and always within the product's bound."""
-    for N, K, ld, off in ((256, 512, None, 0), (90, 333, 340, 1), (1000, 100, 104, 0)):
+    for N, K, ld, off in ((256, 512, None, 0), (90, 333, 340, 1), (1000, 100, 104, 0), (40, 4096, None, 0),
+                          (24, 4097, 4099, 2), (70, 3, 5, 1), (20, 7, 7, 0)):
         print(f"[case] values M={M} N={N} K={K} type={t}", flush=True)
         x = _x(M + N, M, K, t, spread=1.0)
         b, sb, vb, ldb = _codes(2, N, K, BLOCK)
