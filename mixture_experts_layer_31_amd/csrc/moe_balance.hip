@@ -11,10 +11,11 @@
 // moves; 64 above), each with VPL logits of it in runs of four.  The forward
 // adds p to per-lane sums over the block's tokens, joined at the end over the
 // wave's tokens and the block's waves in a fixed order, and counts the block's ids
-// with LDS atomics (integers: their order does not show); a second launch adds the
-// blocks' partial sums, in 64 bits.  Sums over one block's tokens are fp32: at most
-// a few dozen p <= 1 a lane.  A partial sum in global atomics would be one launch
-// fewer and another result with each run.
+// with LDS atomics (integers: their order does not show).  Up to kBalOneBlock tokens
+// one block does it all; past that a second launch adds the blocks' partial sums, in 64
+// bits, 64 experts a block, and its last block the loss.  Sums over one block's
+// tokens are fp32: at most a few dozen p <= 1 a lane.  Partial sums in global
+// atomics would be one launch fewer and another result with each run.
 #include <type_traits>
 
 #include "moe_args.h"
@@ -26,6 +27,7 @@ namespace {
 constexpr int kBalThreads = 1024;  // forward: 16 waves join their sums in LDS
 constexpr int kBalBwdThreads = 256;
 constexpr int kBalMaxBlocks = 256;
+constexpr int kBalOneBlock = 256;
 constexpr int kMaxExperts = 1024;
 
 struct BalScratch {
@@ -33,12 +35,15 @@ struct BalScratch {
   int32_t* c;    // [blocks][E] counts
   float* z;      // [blocks] sums of lse^2
   int32_t* n;    // [blocks] kept tokens
+  double* dot;   // [E / 64] a finishing block's part of sum f P
+  uint32_t* done;  // finishing blocks that are through; cleared by the pass before
   size_t bytes;
 };
 
 int bal_blocks(int T) {
+  if (T <= kBalOneBlock) return 1;
   const long long b = ceil_div(T, 64);
-  return b < 1 ? 1 : b > kBalMaxBlocks ? kBalMaxBlocks : int(b);
+  return b > kBalMaxBlocks ? kBalMaxBlocks : int(b);
 }
 
 BalScratch bal_scratch(const moe_desc& d, char* base) {
@@ -50,6 +55,8 @@ BalScratch bal_scratch(const moe_desc& d, char* base) {
   s.c = reinterpret_cast<int32_t*>(take(G * E * 4));
   s.z = reinterpret_cast<float*>(take(G * 4));
   s.n = reinterpret_cast<int32_t*>(take(G * 4));
+  s.dot = reinterpret_cast<double*>(take((E + 63) / 64 * 8));
+  s.done = reinterpret_cast<uint32_t*>(take(4));
   s.bytes = o;
   return s;
 }
@@ -119,10 +126,27 @@ __device__ __forceinline__ float softmax_row(float (&z)[VPL], int E, int l) {
   return m + logf(s);
 }
 
+// Sum over the block in a fixed order, valid in thread 0.
+__device__ __forceinline__ double block_sum(double v, double (&red)[kBalThreads / 64]) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kBalThreads / 64; ++w) s += red[w];
+  return s;
+}
+
+struct BalOut {
+  int32_t* counts;
+  float *mean_p, *losses;
+};
+
 template <int LPT, int VPL, bool VEC>
 __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
-    const uint8_t* __restrict__ valid, int T, int E, int K, BalScratch out) {
+    const uint8_t* __restrict__ valid, int T, int E, int K, BalScratch out, BalOut res) {
   constexpr int GROUPS = kBalThreads / LPT, WAVES = kBalThreads / 64, COLS = LPT * VPL;
   __shared__ int32_t hist[COLS];
   __shared__ float red[WAVES][COLS];
@@ -178,85 +202,111 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
     nred[wv] = n;
   }
   __syncthreads();
-  for (int e = tid; e < E; e += kBalThreads) {
-    float s = 0.f;
+  float p = 0.f, z = 0.f;  // thread e: expert e's sum
+  int all = 0;
+  if (tid < E) {
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) s += red[w][e];
-    out.p[size_t(blockIdx.x) * E + e] = s;
-    out.c[size_t(blockIdx.x) * E + e] = hist[e];
+    for (int w = 0; w < WAVES; ++w) p += red[w][tid];
   }
-  if (tid == 0) {
-    float s = 0.f;
-    int c = 0;
-    for (int w = 0; w < WAVES; ++w) {
-      s += zred[w];
-      c += nred[w];
+  for (int w = 0; w < WAVES; ++w) {
+    z += zred[w];
+    all += nred[w];
+  }
+  if (gridDim.x > 1) {
+    if (tid < E) {
+      out.p[size_t(blockIdx.x) * E + tid] = p;
+      out.c[size_t(blockIdx.x) * E + tid] = hist[tid];
     }
-    out.z[blockIdx.x] = s;
-    out.n[blockIdx.x] = c;
+    if (tid == 0) {
+      out.z[blockIdx.x] = z;
+      out.n[blockIdx.x] = all;
+      if (blockIdx.x == 0) *out.done = 0;
+    }
+    return;
+  }
+  double dot = 0.;
+  if (tid < E) {
+    const double mp = all > 0 ? double(p) / all : 0.;
+    res.counts[tid] = hist[tid];
+    res.mean_p[tid] = float(mp);
+    dot = all > 0 ? mp * (double(hist[tid]) / (double(all) * K)) : 0.;
+  }
+  __shared__ double dred[WAVES];
+  dot = block_sum(dot, dred);
+  if (tid == 0) {
+    res.counts[E] = all;
+    res.losses[0] = float(E * dot);
+    res.losses[1] = all > 0 ? float(double(z) / all) : 0.f;
   }
 }
 
-// One block: the partial sums of the forward's blocks, and the losses.
-__global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(
-    BalScratch in, int blocks, int E, int K, int32_t* __restrict__ counts,
-    float* __restrict__ mean_p, float* __restrict__ losses) {
-  __shared__ double ps[kBalThreads];
-  __shared__ int32_t cs[kBalThreads];
-  __shared__ int32_t n_all;
-  const int tid = threadIdx.x;
-  if (tid < 64) {
+// The partial sums of the forward's blocks: 64 experts a block, sixteen threads an expert.  The
+// last block to be through adds the blocks' parts of the loss, in their order.
+__global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalScratch in, int blocks, int E,
+                                                                     int K, BalOut res) {
+  constexpr int ROWS = kBalThreads / 64;
+  __shared__ double ps[ROWS][64], dred[ROWS];
+  __shared__ int32_t cs[ROWS][64], n_all;
+  const int tid = threadIdx.x, l = tid & 63, r = tid >> 6, e = blockIdx.x * 64 + l;
+  if (r == 0) {
     double z = 0.;
     int n = 0;
-    for (int b = tid; b < blocks; b += 64) {
+    for (int b = l; b < blocks; b += 64) {
       z += in.z[b];
       n += in.n[b];
     }
+#pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
       z += __shfl_xor(z, o, 64);
       n += __shfl_xor(n, o, 64);
     }
-    if (tid == 0) {
+    if (l == 0) {
       n_all = n;
-      counts[E] = n;
-      losses[1] = n > 0 ? float(z / n) : 0.f;
+      if (blockIdx.x == 0) {
+        res.counts[E] = n;
+        res.losses[1] = n > 0 ? float(z / n) : 0.f;
+      }
     }
   }
-  // `cols` threads side by side, `rows` of them in each column
-  const int cols = E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : E <= 512 ? 512 : 1024;
-  const int rows = kBalThreads / cols, e = tid & (cols - 1), r = tid / cols;
   double p = 0.;
   int c = 0;
   if (e < E) {
-#pragma unroll 8
-    for (int b = r; b < blocks; b += rows) {
+#pragma unroll 16
+    for (int b = r; b < blocks; b += ROWS) {
       p += in.p[size_t(b) * E + e];
       c += in.c[size_t(b) * E + e];
     }
   }
-  ps[tid] = p;
-  cs[tid] = c;
+  ps[r][l] = p;
+  cs[r][l] = c;
   __syncthreads();
-  const int n = n_all;
   double dot = 0.;
   if (r == 0 && e < E) {
-    for (int k = 1; k < rows; ++k) {
-      p += ps[k * cols + e];
-      c += cs[k * cols + e];
+    const int n = n_all;
+#pragma unroll
+    for (int k = 1; k < ROWS; ++k) {
+      p += ps[k][l];
+      c += cs[k][l];
     }
     const double mp = n > 0 ? p / n : 0.;
-    counts[e] = c;
-    mean_p[e] = float(mp);
+    res.counts[e] = c;
+    res.mean_p[e] = float(mp);
     dot = n > 0 ? mp * (double(c) / (double(n) * K)) : 0.;
   }
-  __syncthreads();
-  ps[tid] = dot;
-  __syncthreads();
-  for (int o = kBalThreads / 2; o >= 1; o >>= 1) {
-    if (tid < o) ps[tid] += ps[tid + o];
-    __syncthreads();
+  dot = block_sum(dot, dred);
+  if (tid == 0) {
+    bool last = true;
+    if (gridDim.x > 1) {
+      __hip_atomic_store(&in.dot[blockIdx.x], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(in.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+      if (last) {
+        dot = 0.;
+        for (unsigned b = 0; b < gridDim.x; ++b)
+          dot += __hip_atomic_load(&in.dot[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    if (last) res.losses[0] = float(E * dot);
   }
-  if (tid == 0) losses[0] = float(E * ps[0]);
 }
 
 template <int LPT, int VPL, bool VEC, bool ROUTER>
@@ -384,17 +434,19 @@ int moe_balance_fwd(const moe_desc* d, const float* logits, const int32_t* topk_
   if (scratch_bytes < sc.bytes) return MOE_ESCRATCH;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int blocks = bal_blocks(d->T);
+  const BalOut out{counts, mean_p, losses};
   const bool vec = d->E % 4 == 0 && aligned_to(logits, 16);
   prof_begin("balance_fwd", s);
   with_shape(d->E, vec, [&](auto lpt, auto vpl, auto v) {
     balance_fwd_kernel<decltype(lpt)::value, decltype(vpl)::value, decltype(v)::value>
-        <<<unsigned(blocks), kBalThreads, 0, s>>>(logits, topk_idx, valid, d->T, d->E, d->K, sc);
+        <<<unsigned(blocks), kBalThreads, 0, s>>>(logits, topk_idx, valid, d->T, d->E, d->K, sc, out);
     return 0;
   });
   prof_end(s);
-  if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+  const int rc1 = launched();
+  if (rc1 || blocks == 1) return rc1;
   prof_begin("balance_finish", s);
-  balance_finish_kernel<<<1, kBalThreads, 0, s>>>(sc, blocks, d->E, d->K, counts, mean_p, losses);
+  balance_finish_kernel<<<unsigned(ceil_div(d->E, 64)), kBalThreads, 0, s>>>(sc, blocks, d->E, d->K, out);
   prof_end(s);
   return launched();
 }

@@ -12,9 +12,16 @@
 // is copied to the device and a captured graph holds its own list.  A tensor is
 // cut into chunks of kChunkBytes counted from the 16-byte line that holds its first
 // element; every chunk is whole 16-byte vectors but for the tensor's first and
-// last, whose elements are taken one by one (no load leaves the tensor).  A
-// workgroup takes a fixed run of chunks and its sum goes to its own slot: the
-// result does not depend on the order in which workgroups run.
+// last, whose elements are taken one by one (no load leaves the tensor).  The
+// workgroups step through the chunks side by side (each in a run of its own: the norm
+// of 1.2 GB took 264 us, so 241), and a workgroup's sum goes to its own slot: the
+// result does not depend on the order in which they run.
+//
+// Lists past kStreamChunks go by with nontemporal loads and stores (1.2 GB: norm 241 -> 187
+// us, 6.5 TB/s; clip 429 -> 417 us, 5.8 TB/s); below, the clip finds part of the list in the
+// memory-side cache (256 MB), which they would cost it (104 MB: 58 us for both calls, 64
+// nontemporal).  Loading the end of a long list plainly and clipping from there lost
+// more than it won (604 -> 655 us).
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -28,6 +35,7 @@ constexpr int kMaxList = 96;          // entries a launch: 96 * 28 bytes of argu
 constexpr int kClipThreads = 256;
 constexpr int kChunkBytes = 16384;    // four 16-byte vectors a thread
 constexpr int kMaxBlocks = 2048;      // workgroups a launch
+constexpr uint32_t kStreamChunks = 144 * 64;  // 144 MB
 
 struct GradList {
   const void* src[kMaxList];
@@ -100,7 +108,13 @@ struct Chunk {
 };
 constexpr int kPer = kChunkBytes / 16 / kClipThreads;  // vectors a thread and chunk
 
-template <class T>
+template <bool STREAM>
+__device__ __forceinline__ uint4 load_vec(const void* p) {
+  if constexpr (STREAM) return load16_nt(p);
+  else return *static_cast<const uint4*>(p);
+}
+
+template <bool STREAM, class T>
 __device__ __forceinline__ double chunk_squares(const void* src, int64_t n, uint32_t c) {
   const Chunk<T> ch(src, n, c);
   double s = 0.;
@@ -109,7 +123,7 @@ __device__ __forceinline__ double chunk_squares(const void* src, int64_t n, uint
   for (int k = 0; k < kPer; ++k) {
     raw[k] = make_uint4(0, 0, 0, 0);
     const int64_t e = ch.elem(k);
-    if (ch.whole(e)) raw[k] = *reinterpret_cast<const uint4*>(ch.src + e);
+    if (ch.whole(e)) raw[k] = load_vec<STREAM>(ch.src + e);
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -131,21 +145,18 @@ __device__ __forceinline__ double chunk_squares(const void* src, int64_t n, uint
   return s;
 }
 
+template <bool STREAM>
 __global__ void __launch_bounds__(kClipThreads) grad_squares_kernel(GradList L,
                                                                     double* __restrict__ out) {
   const uint32_t total = L.first[L.count];
-  const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
-  const uint32_t c1 = min(total, (blockIdx.x + 1) * per);
   double s = 0.;
-  uint32_t c = blockIdx.x * per;
-  if (c < c1) {
-    int i = entry_of(L, c);
-    for (; c < c1; ++c) {
-      while (c >= L.first[i + 1]) ++i;
-      const uint32_t k = c - L.first[i];
-      s += (L.f32[i >> 5] >> (i & 31)) & 1 ? chunk_squares<float>(L.src[i], L.n[i], k)
-                                           : chunk_squares<uint16_t>(L.src[i], L.n[i], k);
-    }
+  int i = 0;
+  if (blockIdx.x < total) i = entry_of(L, blockIdx.x);
+  for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
+    while (c >= L.first[i + 1]) ++i;
+    const uint32_t k = c - L.first[i];
+    s += (L.f32[i >> 5] >> (i & 31)) & 1 ? chunk_squares<STREAM, float>(L.src[i], L.n[i], k)
+                                         : chunk_squares<STREAM, uint16_t>(L.src[i], L.n[i], k);
   }
   __shared__ double red[kClipThreads / 64];
 #pragma unroll
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(1024) grad_norm_kernel(const double* __restric
   }
 }
 
-template <class T>
+template <bool STREAM, class T>
 __device__ __forceinline__ void chunk_scale(const void* src, void* dst, int64_t n, uint32_t c,
                                             float by) {
   const Chunk<T> ch(src, n, c);
@@ -181,7 +192,7 @@ __device__ __forceinline__ void chunk_scale(const void* src, void* dst, int64_t 
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     const int64_t e = ch.elem(k);
-    if (ch.whole(e)) raw[k] = *reinterpret_cast<const uint4*>(ch.src + e);
+    if (ch.whole(e)) raw[k] = load_vec<STREAM>(ch.src + e);
   }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
@@ -191,12 +202,10 @@ __device__ __forceinline__ void chunk_scale(const void* src, void* dst, int64_t 
       Vec<T>::get(raw[k], f);
 #pragma unroll
       for (int i = 0; i < Vec<T>::N; ++i) f[i] *= by;
-      if (lined) {
-        *reinterpret_cast<uint4*>(out + e) = Vec<T>::put(f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < Vec<T>::N; ++i) out[e + i] = Vec<T>::round(f[i]);
-      }
+      const uint4 v = Vec<T>::put(f);
+      if (!lined) store16(out + e, v);
+      else if (STREAM) store16_nt(out + e, v);
+      else *reinterpret_cast<uint4*>(out + e) = v;
     } else if (e < n && e + Vec<T>::N > 0) {
       for (int i = 0; i < Vec<T>::N; ++i)
         if (e + i >= 0 && e + i < n) out[e + i] = Vec<T>::round(Vec<T>::load(ch.src + e + i) * by);
@@ -204,23 +213,21 @@ __device__ __forceinline__ void chunk_scale(const void* src, void* dst, int64_t 
   }
 }
 
+template <bool STREAM>
 __global__ void __launch_bounds__(kClipThreads) grad_scale_kernel(GradList L,
                                                                   const float* __restrict__ norm,
                                                                   float max_norm) {
   const float nm = norm[0];
   const float by = nm <= max_norm ? 1.f : max_norm / nm;  // NaN for a NaN norm
   const uint32_t total = L.first[L.count];
-  const uint32_t per = (total + gridDim.x - 1) / gridDim.x;
-  const uint32_t c1 = min(total, (blockIdx.x + 1) * per);
-  uint32_t c = blockIdx.x * per;
-  if (c >= c1) return;
-  int i = entry_of(L, c);
-  for (; c < c1; ++c) {
+  if (blockIdx.x >= total) return;
+  int i = entry_of(L, blockIdx.x);
+  for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
     while (c >= L.first[i + 1]) ++i;
     if (by == 1.f && L.src[i] == L.dst[i]) continue;
     const uint32_t k = c - L.first[i];
-    if ((L.f32[i >> 5] >> (i & 31)) & 1) chunk_scale<float>(L.src[i], L.dst[i], L.n[i], k, by);
-    else chunk_scale<uint16_t>(L.src[i], L.dst[i], L.n[i], k, by);
+    if ((L.f32[i >> 5] >> (i & 31)) & 1) chunk_scale<STREAM, float>(L.src[i], L.dst[i], L.n[i], k, by);
+    else chunk_scale<STREAM, uint16_t>(L.src[i], L.dst[i], L.n[i], k, by);
   }
 }
 
@@ -339,7 +346,8 @@ int moe_grad_norm(const moe_grad* g, int32_t count, float* norm, void* scratch,
   rc = for_lists(g, count, [&](const GradList& L) {
     const unsigned grid = grid_of(L);
     prof_begin("grad_squares", s);
-    grad_squares_kernel<<<grid, kClipThreads, 0, s>>>(L, part + used);
+    if (L.first[L.count] > kStreamChunks) grad_squares_kernel<true><<<grid, kClipThreads, 0, s>>>(L, part + used);
+    else grad_squares_kernel<false><<<grid, kClipThreads, 0, s>>>(L, part + used);
     prof_end(s);
     used += grid;
     return launched();
@@ -361,7 +369,8 @@ int moe_grad_clip(const moe_grad* g, int32_t count, const float* norm, float max
   hipStream_t s = static_cast<hipStream_t>(stream);
   return for_lists(g, count, [&](const GradList& L) {
     prof_begin("grad_scale", s);
-    grad_scale_kernel<<<grid_of(L), kClipThreads, 0, s>>>(L, norm, max_norm);
+    if (L.first[L.count] > kStreamChunks) grad_scale_kernel<true><<<grid_of(L), kClipThreads, 0, s>>>(L, norm, max_norm);
+    else grad_scale_kernel<false><<<grid_of(L), kClipThreads, 0, s>>>(L, norm, max_norm);
     prof_end(s);
     return launched();
   });
