@@ -178,28 +178,28 @@ def moe_router_bwd(desc, topk_idx, topk_w, dtopk_w, dlogits, stream=None) -> int
                                 _p(dlogits), _stream(stream))
 
 
-def _fits(*tensors) -> bool:
-    """Whether each (tensor, element types, count) is what a call reads or writes: a contiguous GPU
-    tensor of one of those types with that many elements, or, as (tensor, types, rows, columns, row
-    stride), so many rows of its own stride; all of them on the current device, whose stream the call
-    takes.  None and raw addresses are the C side's to check."""
-    dev = None
+def _addresses(*tensors):
+    """The device addresses of (tensor, element types, count) for contiguous GPU tensors of one of those
+    types with that many elements at least, or of (tensor, types, rows, columns, row stride) for so many
+    rows of their own stride; None where one does not fit, all of them on the current device, whose stream
+    the call takes.  None and raw addresses go through: they are the C side's to check."""
+    import torch
+    dev, out = torch.cuda.current_device(), []
     for t, types, n, *row in tensors:
         if t is None or isinstance(t, int):
+            out.append(t)
             continue
-        if dev is None:
-            import torch
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev or t.dtype not in types:
-            return False
+        if t.dtype not in types or t.get_device() != dev:
+            return None
         if row:
             if t.dim() != 2 or t.size(0) < n or t.size(1) < row[0]:
-                return False
+                return None
             if (n > 1 and t.stride(0) != row[1]) or (row[0] > 1 and t.stride(1) != 1):
-                return False
+                return None
         elif t.numel() < n or not t.is_contiguous():
-            return False
-    return True
+            return None
+        out.append(t.data_ptr())
+    return out
 
 
 def _types() -> tuple:
@@ -223,23 +223,23 @@ def moe_balance_scratch_bytes(desc: moe_desc) -> int:
 def moe_balance_fwd(desc, logits, topk_idx, valid, counts, mean_p, losses, scratch, stream=None) -> int:
     T, E, K = desc.T, desc.E, desc.K
     f32, i32, mask, _, _ = _types()
-    if not _fits((logits, f32, T * E), (topk_idx, i32, T * K), (valid, mask, T), (counts, i32, E + 1),
-                 (mean_p, f32, E), (losses, f32, 2)):
+    at = _addresses((logits, f32, T * E), (topk_idx, i32, T * K), (valid, mask, T), (counts, i32, E + 1),
+                    (mean_p, f32, E), (losses, f32, 2))
+    if at is None:
         return MOE_EINVAL
-    return lib().moe_balance_fwd(ctypes.byref(desc), _p(logits), _p(topk_idx), _p(valid), _p(counts),
-                                 _p(mean_p), _p(losses), _p(scratch),
-                                 0 if scratch is None else _nbytes(scratch), _stream(stream))
+    return lib().moe_balance_fwd(ctypes.byref(desc), *at, _p(scratch), 0 if scratch is None else _nbytes(scratch),
+                                 _stream(stream))
 
 
 def moe_balance_bwd(desc, logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, dlogits,
                     stream=None) -> int:
     T, E, K = desc.T, desc.E, desc.K
     f32, i32, mask, _, _ = _types()
-    if not _fits((logits, f32, T * E), (valid, mask, T), (counts, i32, E + 1), (dlosses, f32, 2),
-                 (topk_idx, i32, T * K), (topk_w, f32, T * K), (dtopk_w, f32, T * K), (dlogits, f32, T * E)):
+    at = _addresses((logits, f32, T * E), (valid, mask, T), (counts, i32, E + 1), (dlosses, f32, 2),
+                    (topk_idx, i32, T * K), (topk_w, f32, T * K), (dtopk_w, f32, T * K), (dlogits, f32, T * E))
+    if at is None:
         return MOE_EINVAL
-    return lib().moe_balance_bwd(ctypes.byref(desc), _p(logits), _p(valid), _p(counts), _p(dlosses),
-                                 _p(topk_idx), _p(topk_w), _p(dtopk_w), _p(dlogits), _stream(stream))
+    return lib().moe_balance_bwd(ctypes.byref(desc), *at, _stream(stream))
 
 
 def _code_ld(n: int) -> int:
@@ -259,12 +259,12 @@ def moe_block_quant(desc, x, codes, scales, codes_t=None, scales_t=None, stream=
     rb, cb = (R + 127) // 128, (C + 127) // 128
     block = desc.scale == MOE_SCALE_BLOCK
     f32, _, _, code, io = _types()
-    if not _fits((x, io.get(desc.in_type, ()), R, C, desc.ld_in), (codes, code, R, _code_ld(C), desc.ld_codes),
-                 (codes_t, code, C, _code_ld(R), desc.ld_codes_t), (scales, f32, cb * (rb if block else R)),
-                 (scales_t, f32, rb * (cb if block else C))):
+    at = _addresses((x, io.get(desc.in_type, ()), R, C, desc.ld_in), (codes, code, R, _code_ld(C), desc.ld_codes),
+                    (scales, f32, cb * (rb if block else R)), (codes_t, code, C, _code_ld(R), desc.ld_codes_t),
+                    (scales_t, f32, rb * (cb if block else C)))
+    if at is None:
         return MOE_EINVAL
-    return lib().moe_block_quant(ctypes.byref(desc), _p(x), _p(codes), _p(scales), _p(codes_t),
-                                 _p(scales_t), _stream(stream))
+    return lib().moe_block_quant(ctypes.byref(desc), *at, _stream(stream))
 
 
 def make_block_mm_desc(M, N, K, a_type=MOE_TYPE_E4M3, b_scale=MOE_SCALE_BLOCK, c_type=MOE_TYPE_BF16,
@@ -284,13 +284,14 @@ def moe_block_mm(desc, a, a_scales, b, b_scales, c, scratch=None, stream=None) -
     M, N, K = desc.M, desc.N, desc.K
     steps, own = (K + 127) // 128, desc.a_type == MOE_TYPE_E4M3
     f32, _, _, code, io = _types()
-    if not _fits((a, code if own else io.get(desc.a_type, ()), M, _code_ld(K) if own else K, desc.lda),
-                 (a_scales, f32, steps * M), (b, code, N, _code_ld(K), desc.ldb),
-                 (b_scales, f32, steps * (N if desc.b_scale == MOE_SCALE_TILE else (N + 127) // 128)),
-                 (c, io.get(desc.c_type, ()), M, N, desc.ldc)):
+    at = _addresses((a, code if own else io.get(desc.a_type, ()), M, _code_ld(K) if own else K, desc.lda),
+                    (a_scales, f32, steps * M), (b, code, N, _code_ld(K), desc.ldb),
+                    (b_scales, f32, steps * (N if desc.b_scale == MOE_SCALE_TILE else (N + 127) // 128)),
+                    (c, io.get(desc.c_type, ()), M, N, desc.ldc))
+    if at is None:
         return MOE_EINVAL
-    return lib().moe_block_mm(ctypes.byref(desc), _p(a), _p(a_scales), _p(b), _p(b_scales), _p(c),
-                              _p(scratch), 0 if scratch is None else _nbytes(scratch), _stream(stream))
+    return lib().moe_block_mm(ctypes.byref(desc), *at, _p(scratch), 0 if scratch is None else _nbytes(scratch),
+                              _stream(stream))
 
 
 def make_grad_list(src, dst=None):
@@ -317,16 +318,18 @@ def moe_grad_scratch_bytes(count: int) -> int:
 
 
 def moe_grad_norm(grads, norm, scratch, stream=None) -> int:
-    if not _fits((norm, _types()[0], 1)):
+    at = _addresses((norm, _types()[0], 1))
+    if at is None:
         return MOE_EINVAL
-    return lib().moe_grad_norm(grads, len(grads), _p(norm), _p(scratch),
+    return lib().moe_grad_norm(grads, len(grads), *at, _p(scratch),
                                0 if scratch is None else _nbytes(scratch), _stream(stream))
 
 
 def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> int:
-    if not _fits((norm, _types()[0], 1)):
+    at = _addresses((norm, _types()[0], 1))
+    if at is None:
         return MOE_EINVAL
-    return lib().moe_grad_clip(grads, len(grads), _p(norm), max_norm, _stream(stream))
+    return lib().moe_grad_clip(grads, len(grads), *at, max_norm, _stream(stream))
 
 
 def moe_routing_view(desc, scratch) -> tuple:

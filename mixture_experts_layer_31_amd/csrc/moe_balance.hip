@@ -157,6 +157,13 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
   const int64_t chunk = (int64_t(T) + gridDim.x - 1) / gridDim.x;
   const int64_t t0 = min(int64_t(T), blockIdx.x * chunk), t1 = min(int64_t(T), t0 + chunk);
   const int pairs = int(t1 - t0) * K;
+  float next[VPL];  // the next token's logits: on their way while the ids are counted
+  bool keep = false;
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    keep = t < t1 && (valid == nullptr || valid[t]);
+    if (keep) load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, next);
+  };
+  fetch(t0 + tid / LPT);
   for (int e = tid; e < COLS; e += kBalThreads) hist[e] = 0;
   __syncthreads();
   // ids, one (token, slot) pair a thread
@@ -171,9 +178,12 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
 #pragma unroll
   for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
   for (int64_t t = t0 + tid / LPT; t < t1; t += GROUPS) {
-    if (valid != nullptr && !valid[t]) continue;
     float p[VPL];
-    load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, p);
+    const bool kept = keep;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = next[i];
+    fetch(t + GROUPS);
+    if (!kept) continue;
     const float lse = softmax_row<LPT>(p, E, l);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) acc[i] += p[i];
@@ -240,20 +250,43 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
   }
 }
 
-// The partial sums of the forward's blocks: 64 experts a block, sixteen threads an expert.  The
-// last block to be through adds the blocks' parts of the loss, in their order.
+// The partial sums of the forward's blocks: COLS experts a block (128 where that makes it one
+// block), 1024 / COLS threads an expert.  The last block to be through adds the blocks' parts of
+// the loss, in their order.
+template <int COLS>
 __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalScratch in, int blocks, int E,
                                                                      int K, BalOut res) {
-  constexpr int ROWS = kBalThreads / 64;
-  __shared__ double ps[ROWS][64], dred[ROWS];
-  __shared__ int32_t cs[ROWS][64], n_all;
-  const int tid = threadIdx.x, l = tid & 63, r = tid >> 6, e = blockIdx.x * 64 + l;
-  if (r == 0) {
+  constexpr int ROWS = kBalThreads / COLS;
+  __shared__ double ps[ROWS][COLS], dred[kBalThreads / 64];
+  __shared__ int32_t cs[ROWS][COLS], n_all;
+  const int tid = threadIdx.x, l = tid % COLS, r = tid / COLS, e = blockIdx.x * COLS + l;
+  constexpr int NB = kBalMaxBlocks / 64;
+  float zb[NB] = {};
+  int nb[NB] = {};
+  if (tid < 64) {
+#pragma unroll
+    for (int q = 0; q < NB; ++q)
+      if (l + 64 * q < blocks) {
+        zb[q] = in.z[l + 64 * q];
+        nb[q] = in.n[l + 64 * q];
+      }
+  }
+  double p = 0.;
+  int c = 0;
+  if (e < E) {
+#pragma unroll 16
+    for (int b = r; b < blocks; b += ROWS) {
+      p += in.p[size_t(b) * E + e];
+      c += in.c[size_t(b) * E + e];
+    }
+  }
+  if (tid < 64) {
     double z = 0.;
     int n = 0;
-    for (int b = l; b < blocks; b += 64) {
-      z += in.z[b];
-      n += in.n[b];
+#pragma unroll
+    for (int q = 0; q < NB; ++q) {
+      z += zb[q];
+      n += nb[q];
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
@@ -266,15 +299,6 @@ __global__ void __launch_bounds__(kBalThreads) balance_finish_kernel(BalScratch 
         res.counts[E] = n;
         res.losses[1] = n > 0 ? float(z / n) : 0.f;
       }
-    }
-  }
-  double p = 0.;
-  int c = 0;
-  if (e < E) {
-#pragma unroll 16
-    for (int b = r; b < blocks; b += ROWS) {
-      p += in.p[size_t(b) * E + e];
-      c += in.c[size_t(b) * E + e];
     }
   }
   ps[r][l] = p;
@@ -315,10 +339,27 @@ __global__ void __launch_bounds__(kBalBwdThreads) balance_bwd_kernel(
     const int32_t* __restrict__ counts, const float* __restrict__ dlosses,
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w,
     const float* __restrict__ dtopk_w, int T, int E, int K, float* __restrict__ dlogits) {
-  constexpr int GROUPS = kBalBwdThreads / LPT;
-  __shared__ int32_t s_j[ROUTER ? GROUPS : 1][64];
-  __shared__ float s_w[ROUTER ? GROUPS : 1][64], s_dw[ROUTER ? GROUPS : 1][64];
+  constexpr int GROUPS = kBalBwdThreads / LPT, COLS = LPT * VPL;
+  // a group's row of the router's gradient, zero between tokens
+  __shared__ __attribute__((aligned(16))) float s_g[ROUTER ? GROUPS : 1][ROUTER ? COLS : 4];
   const int tid = threadIdx.x, l = tid & (LPT - 1), g = tid / LPT;
+  const int64_t step = int64_t(gridDim.x) * GROUPS, first = int64_t(blockIdx.x) * GROUPS + g;
+  float p[VPL];
+  bool keep = false;
+  int id = -1;
+  float w = 0.f, dw = 0.f;
+  // a token's logits and slot l of its routing
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+    if (t >= T) return;
+    keep = valid == nullptr || valid[t];
+    if (keep) load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, p);
+    if (ROUTER && l < K) {
+      id = topk_idx[size_t(t) * K + l];
+      w = topk_w[size_t(t) * K + l];
+      dw = dtopk_w[size_t(t) * K + l];
+    }
+  };
+  fetch(first);
   const int n = counts[E];
   const float per = n > 0 ? 1.f / float(n) : 0.f;
   const float a = dlosses[0] * (float(E) * per), b = dlosses[1] * (2.f * per);
@@ -328,11 +369,13 @@ __global__ void __launch_bounds__(kBalBwdThreads) balance_bwd_kernel(
     const int e = expert_of<LPT>(l, i);
     f[i] = e < E ? float(counts[e]) * (per / float(K)) : 0.f;
   }
-  for (int64_t t = int64_t(blockIdx.x) * GROUPS + g; t < T; t += int64_t(gridDim.x) * GROUPS) {
-    const bool keep = valid == nullptr || valid[t];
-    float p[VPL];
+  if constexpr (ROUTER) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s_g[g][expert_of<LPT>(l, i)] = 0.f;
+  }
+  for (int64_t t = first; t < T; t += step) {
+    if (t != first) fetch(t);
     if (keep) {
-      load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, p);
       const float lse = softmax_row<LPT>(p, E, l);
       float s = 0.f;
 #pragma unroll
@@ -346,30 +389,31 @@ __global__ void __launch_bounds__(kBalBwdThreads) balance_bwd_kernel(
       for (int i = 0; i < VPL; ++i) p[i] = 0.f;
     }
     if constexpr (ROUTER) {
-      // w_k (dw_k - sum w dw) on the selected experts, slots in order; the group's
-      // lanes are in one wave, whose LDS accesses stay in order
-      for (int k = l; k < K; k += LPT) {
-        s_j[g][k] = topk_idx[size_t(t) * K + k];
-        s_w[g][k] = topk_w[size_t(t) * K + k];
-        s_dw[g][k] = dtopk_w[size_t(t) * K + k];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      float c = 0.f;
-      for (int k = 0; k < K; ++k) c += s_w[g][k] * s_dw[g][k];
-      for (int k = 0; k < K; ++k) {
-        const int j = s_j[g][k];
-        const float v = s_w[g][k] * (s_dw[g][k] - c);
-        // j = 4 (l + LPT q) + r is value 4 q + r of lane l
-        const bool mine = j >= 0 && j < E && ((j >> 2) & (LPT - 1)) == l;
-        const int at = mine ? 4 * ((j >> 2) / LPT) + (j & 3) : -1;
+      // w_k (dw_k - sum w dw) into the group's row at the selected experts; the group's lanes are in
+      // one wave, whose LDS accesses stay in order
+      float c = w * dw;
+      for (int k = l + LPT; k < K; k += LPT) c += topk_w[size_t(t) * K + k] * dtopk_w[size_t(t) * K + k];
+      c = group_sum<LPT>(c);
+      auto add = [&](int j, float v) __attribute__((always_inline)) {
+        if (j >= 0 && j < E) __hip_atomic_fetch_add(&s_g[g][j], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+      };
+      auto order = [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      };
+      if (l < K) add(id, w * (dw - c));
+      for (int k = l + LPT; k < K; k += LPT)
+        add(topk_idx[size_t(t) * K + k], topk_w[size_t(t) * K + k] * (dtopk_w[size_t(t) * K + k] - c));
+      order();
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) p[i] += at == i ? v : 0.f;
+      for (int q = 0; q < VPL / 4; ++q) {
+        float4* row = reinterpret_cast<float4*>(&s_g[g][expert_of<LPT>(l, 4 * q)]);
+        const float4 v = *row;
+        *row = make_float4(0.f, 0.f, 0.f, 0.f);
+        p[4 * q] += v.x; p[4 * q + 1] += v.y; p[4 * q + 2] += v.z; p[4 * q + 3] += v.w;
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      order();
     }
     float* out = dlogits + size_t(t) * E;
 #pragma unroll
@@ -446,7 +490,10 @@ int moe_balance_fwd(const moe_desc* d, const float* logits, const int32_t* topk_
   const int rc1 = launched();
   if (rc1 || blocks == 1) return rc1;
   prof_begin("balance_finish", s);
-  balance_finish_kernel<<<unsigned(ceil_div(d->E, 64)), kBalThreads, 0, s>>>(sc, blocks, d->E, d->K, out);
+  if (d->E > 64 && d->E <= 128)
+    balance_finish_kernel<128><<<1, kBalThreads, 0, s>>>(sc, blocks, d->E, d->K, out);
+  else
+    balance_finish_kernel<64><<<unsigned(ceil_div(d->E, 64)), kBalThreads, 0, s>>>(sc, blocks, d->E, d->K, out);
   prof_end(s);
   return launched();
 }

@@ -98,8 +98,7 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // the codes go back through LDS so that eight lanes store a row's 128 bytes.
 template <class T, bool BLOCK>
 __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
-  constexpr int PAD = sizeof(T) == 2 ? 2 : 1;  // elements: columns apart by an odd count of words
-  constexpr int LD = 128 + PAD;
+  constexpr int LD = 128 + 16 / sizeof(T);  // rows apart in banks, 16-byte aligned
   __shared__ __attribute__((aligned(16))) char smem[128 * LD * sizeof(T)];
   __shared__ float red[4];
   const int rt = blockIdx.x / p.ctiles, ct = blockIdx.x - rt * p.ctiles;
@@ -163,13 +162,19 @@ __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
   }
   if (p.qt == nullptr) return;
 #pragma unroll
-  for (int it = 0; it < 8; ++it)
+  for (int it = 0; it < 8; ++it) {
+    uint4* at = reinterpret_cast<uint4*>(tile + (it * 16 + rw) * LD + 8 * l16);
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      T* at = tile + (it * 16 + rw) * LD + 8 * l16 + i;
-      if constexpr (sizeof(T) == 2) *at = uint16_t(__float_as_uint(v[it][i]) >> 16);
-      else *at = v[it][i];
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[it][i]);
+    if constexpr (sizeof(T) == 2) {
+      at[0] = make_uint4((w[0] >> 16) | (w[1] & 0xffff0000u), (w[2] >> 16) | (w[3] & 0xffff0000u),
+                         (w[4] >> 16) | (w[5] & 0xffff0000u), (w[6] >> 16) | (w[7] & 0xffff0000u));
+    } else {
+      at[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      at[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
+  }
   __syncthreads();
   // column q, rows 64 h .. 64 h + 63
   const int q = wv * 32 + (lane & 31), h = lane >> 5;
@@ -748,7 +753,13 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
     arrive(i + 1);
     issue(i + S);
     read(i + 1, nxt);
+    __builtin_amdgcn_sched_barrier(0);  // the reads ahead of the products that hide them
     multiply(cur);
+    // and the promotions here, not sunk into the next step behind its wait
+#pragma unroll
+    for (int r = 0; r < MB; ++r)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(acc[r][j]));
   };
   int i = 0;
   for (; i + 2 < n; i += 2) {
