@@ -324,18 +324,28 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
                : "memory", "m0");
 }
 
-// Large products, bf16 results: 256 x 256 tiles, eight waves of 128 x 64.
-template <bool B_TILE>
-__global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
-  constexpr int BM = 256, BN = 256, WAVES = 8, MB = 8, NB = 4;
-  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES + 2048;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+// Large products with bf16 results: 256 x 256 tiles of eight waves, 128 x 64 each, or, where those
+// are too few, 128 x 128 tiles of two groups of four waves, 64 x 64 each, that share the runs and
+// are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
+template <int MB_, int WGM_, int WGN_, int KG_>
+struct LargeTile {
+  static constexpr int MB = MB_, NB = 4, WGM = WGM_, WGN = WGN_, KG = KG_;
+  static constexpr int BM = 16 * MB * WGM, BN = 16 * NB * WGN, WAVES = WGM * WGN, THREADS = 64 * WAVES * KG;
+};
+
+template <class TL, bool B_TILE>
+__global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p) {
+  constexpr int BM = TL::BM, BN = TL::BN, WAVES = TL::WAVES, MB = TL::MB, NB = TL::NB, KG = TL::KG;
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES + (BM + BN) * 4, RING = 2 * STAGE;
+  __shared__ __attribute__((aligned(1024))) char lds[KG * RING];
   const int l = xcd_remap(blockIdx.x, gridDim.x);
   int mt, nt;
   wgrad_mn(l, p.ntm, p.ntn, mt, nt);
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = wv / WAVES, wave = wv % WAVES, wm = wave / TL::WGN, wn = wave % TL::WGN;
+  const int group_tid = wave * 64 + lane;
+  char* smem = lds + kg * RING;
   const int m0 = mt * BM, n0 = nt * BN;
   const int mrows = min(BM, p.M - m0), nrows = min(BN, p.N - n0);
   const int kbytes = (p.K + 15) & ~15;
@@ -347,18 +357,21 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
           [&](int r) { return r < nrows ? int(r * p.ldb) : -1; }, wave, lane);
   const uint32_t base = lds_addr(smem);
   const int nblocks = (p.N + 127) / 128;
-  const bool sis_a = wave < 4;
+  constexpr int QA = BM / 64;  // 64 scales a wave: A's, then B's
+  static_assert(QA + BN / 64 == WAVES, "a load of scales a wave");
+  const bool sis_a = wave < QA;
   const i32x4 rs = sis_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
                          : make_rsrc(p.SB, uint32_t(p.ksteps) * uint32_t(B_TILE ? p.N : nblocks) * 4u);
-  const int sr = (wave & 3) * 64 + lane;
+  const int sr = (sis_a ? wave : wave - QA) * 64 + lane;
   const int sstep = sis_a ? p.ldsa * 4 : B_TILE ? p.N * 4 : 4;
   const int soff = sr >= (sis_a ? mrows : nrows) ? int(0x80000000u)
                    : sis_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ksteps * 4;
-  // Loads of step kt into stage s, the q-th of nine; past the last step they miss every
-  // buffer (no traffic).
+  // Loads of the group's i-th step (run i KG + kg) into stage s, the q-th of NL; past the last
+  // run they miss every buffer (no traffic) and bring zeros.
   constexpr int NL = decltype(sa)::NI + decltype(sb)::NI + 1;
-  auto issue1 = [&](int s, int kt, int q) __attribute__((always_inline)) {
+  auto issue1 = [&](int s, int i, int q) __attribute__((always_inline)) {
     const uint32_t st = base + s * STAGE;
+    const int kt = i * KG + kg;
     const bool there = kt < p.ksteps;
     constexpr int NA = decltype(sa)::NI, NBI = decltype(sb)::NI;
     const int kb = there ? kt * 128 : 0x40000000;
@@ -367,9 +380,9 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
       dma16(sb.rsrc, st + A_BYTES + uint32_t(wave * NBI + q - NA) * 1024u, sb.vb[q - NA] + kb);
     else dma4(rs, st + A_BYTES + B_BYTES + wave * 256, there ? soff + kt * sstep : int(0x80000000u));
   };
-  auto issue = [&](int s, int kt) __attribute__((always_inline)) {
+  auto issue = [&](int s, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < NL; ++q) issue1(s, kt, q);
+    for (int q = 0; q < NL; ++q) issue1(s, i, q);
   };
   f32x4 acc[MB][NB];
 #pragma unroll
@@ -385,11 +398,11 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
     const i32x4 y = *reinterpret_cast<const i32x4*>(f1 + at);
     return i32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   };
-  const char* sap = smem + A_BYTES + B_BYTES + (wm * 128 + l16) * 4;
-  const char* sbp = smem + A_BYTES + B_BYTES + BM * 4 + (wn * 64 + (B_TILE ? 4 * g : 0)) * 4;
-  auto frag_a = [&](int st, int i) __attribute__((always_inline)) { return frag(st + (wm * 128 + i * 16) * 128); };
+  const char* sap = smem + A_BYTES + B_BYTES + (wm * 16 * MB + l16) * 4;
+  const char* sbp = smem + A_BYTES + B_BYTES + BM * 4 + (wn * 16 * NB + (B_TILE ? 4 * g : 0)) * 4;
+  auto frag_a = [&](int st, int i) __attribute__((always_inline)) { return frag(st + (wm * MB + i) * 2048); };
   auto frag_b = [&](int st, int j) __attribute__((always_inline)) {
-    return frag(st + A_BYTES + (wn * 64 + j * 16) * 128);
+    return frag(st + A_BYTES + (wn * NB + j) * 2048);
   };
   auto scale_a = [&](int st, int i) __attribute__((always_inline)) {
     return *reinterpret_cast<const float*>(sap + st + i * 64);
@@ -457,37 +470,47 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
   // the last step's codes behind column K become 0, once its stage has arrived
   const bool tail = p.K % 128 != 0;
   auto mend = [&](int st) __attribute__((always_inline)) {
-    const int kr = p.K % 128;
-    for (int r = threadIdx.x; r < BM + BN; r += 512) {
-      char* at = smem + st + r * 128;  // B's rows follow A's
-      const int w8 = swz_k(r & 255);
-      for (int c = kr >> 4; c < 8; ++c) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(at + ((c ^ w8) << 4));
+    if ((p.ksteps - 1) % KG == kg) {
+      const int kr = p.K % 128;
+      for (int r = group_tid; r < BM + BN; r += 64 * WAVES) {
+        char* at = smem + st + r * 128;  // B's rows follow A's
+        const int w8 = swz_k(r < BM ? r : r - BM);
+        for (int c = kr >> 4; c < 8; ++c) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(at + ((c ^ w8) << 4));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int keep = kr - c * 16 - 4 * j;  // bytes of this word that exist
-          if (keep <= 0) w[j] = 0;
-          else if (keep < 4) w[j] &= (1u << (8 * keep)) - 1;
+          for (int j = 0; j < 4; ++j) {
+            const int keep = kr - c * 16 - 4 * j;  // bytes of this word that exist
+            if (keep <= 0) w[j] = 0;
+            else if (keep < 4) w[j] &= (1u << (8 * keep)) - 1;
+          }
         }
       }
     }
     __syncthreads();
   };
+  const int n = (p.ksteps + KG - 1) / KG;  // steps a group
+  // A step's loads are spread over the one before it (in one burst behind the barrier they hold up
+  // the fragment reads): over its rows, or, where a step is too short for them to arrive
+  // in (128 x 128: 59 us, so 51, at 1536 x 2048 x 8197; 256 x 256: 275 us, so 287, at 16384 x 4096 x 4096),
+  // over the last products of the step before that, into the stage that they have just freed.
+  constexpr bool EARLY = MB < 8;
   issue(0, 0);
-  wait_vmcnt<0>();
+  if constexpr (EARLY) issue(1, 1);
+  wait_vmcnt<EARLY ? NL : 0>();
   __builtin_amdgcn_s_barrier();
-  if (tail && p.ksteps == 1) mend(0);
+  if (tail && n == 1) mend(0);
   open(0);
   int kt = 0, st = 0;
-  const int straight = p.ksteps - 1 - (tail ? 1 : 0);  // steps whose successor needs no mending
+  const int straight = n - 1 - (tail ? 1 : 0);  // steps whose successor needs no mending
   for (; kt < straight; ++kt) {
     const int sn = STAGE - st;
 #pragma unroll
     for (int i = 0; i < MB - 3; ++i) {
-      // the next step's loads, spread: in one burst they hold up the fragment reads
-      // behind the barrier
-      if (i * 2 < NL) issue1(st ? 0 : 1, kt + 1, i * 2);
-      if (i * 2 + 1 < NL) issue1(st ? 0 : 1, kt + 1, i * 2 + 1);
+      if constexpr (!EARLY) {
+        constexpr int PR = (NL + MB - 4) / (MB - 3);
+#pragma unroll
+        for (int q = i * PR; q < (i + 1) * PR && q < NL; ++q) issue1(st ? 0 : 1, kt + 1, q);
+      }
       row(st, i, true);
     }
     // with the last two blocks of A in registers the stage is read: the next one takes
@@ -505,6 +528,10 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
     for (int j = 0; j < NB; ++j) {
       const f32x4 q6 = mfma(b[j], a6), q7 = mfma(b[j], a7);
       b[j] = frag_b(sn, j);
+      if constexpr (EARLY) {
+#pragma unroll
+        for (int q = j * NL / NB; q < (j + 1) * NL / NB; ++q) issue1(st ? 1 : 0, kt + 2, q);
+      }
       if (j == 0) {
         rest(MB - 3);
       } else {
@@ -522,8 +549,8 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
     st = sn;
     __builtin_amdgcn_sched_barrier(0);
   }
-  if (tail && p.ksteps > 1) {
-    issue(st ? 0 : 1, kt + 1);
+  if (tail && n > 1) {
+    if constexpr (!EARLY) issue(st ? 0 : 1, kt + 1);
 #pragma unroll
     for (int i = 0; i < MB; ++i) row(st, i, i + 1 < MB);
     rest(MB - 1);
@@ -537,6 +564,43 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
 #pragma unroll
   for (int i = 0; i < MB; ++i) row(st, i, i + 1 < MB);
   rest(MB - 1);
+  wait_vmcnt<0>();  // the loads that missed still write their zeros
+  if constexpr (KG > 1) {  // join the groups' sums
+    constexpr int LDR = BN + 4;
+    static_assert(RING >= BM * LDR * 4, "the join fits a group's ring");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        *reinterpret_cast<f32x4*>(smem + (((wm * MB + i) * 16 + l16) * LDR + (wn * NB + j) * 16 + 4 * g) * 4) = acc[i][j];
+    __syncthreads();
+    uint16_t* c = static_cast<uint16_t*>(p.C) + int64_t(m0) * p.ldc + n0;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < BM * BN / 8; e += TL::THREADS) {
+      const int r = e / (BN / 8), col = e % (BN / 8) * 8;
+      if (r >= mrows || col >= nrows) continue;
+      f32x4 v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const char* at = lds + (r * LDR + col + 4 * q) * 4;
+        v[q] = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll
+        for (int x = 1; x < KG; ++x) v[q] += *reinterpret_cast<const f32x4*>(at + x * RING);
+      }
+      const uint32_t w[4] = {pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
+                             pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
+      uint16_t* dst = c + r * p.ldc + col;
+      if (col + 8 <= nrows) {
+        store16(dst, make_uint4(w[0], w[1], w[2], w[3]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (col + q < nrows) dst[q] = uint16_t(w[q >> 1] >> (16 * (q & 1)));
+      }
+    }
+    return;
+  }
   // Epilogue: the whole bf16 tile through LDS, whole rows out
   __syncthreads();
   BandTile<2> t{smem, BN};
@@ -544,16 +608,16 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      *reinterpret_cast<uint2*>(t.at(wm * 128 + i * 16 + l16, wn * 64 + j * 16 + 4 * g)) =
+      *reinterpret_cast<uint2*>(t.at((wm * MB + i) * 16 + l16, (wn * NB + j) * 16 + 4 * g)) =
           pack4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
   __syncthreads();
   uint16_t* c = static_cast<uint16_t*>(p.C) + int64_t(m0) * p.ldc + n0;
 #pragma unroll 4
-  for (int k = threadIdx.x; k < BM * 32; k += 512) {
-    const int row = k >> 5, ch = k & 31;
-    if (row >= mrows || ch * 8 >= nrows) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(smem + row * 512 + ((ch ^ (row & 31)) << 4));
-    uint16_t* dst = c + row * p.ldc + ch * 8;
+  for (int k = threadIdx.x; k < BM * (BN / 8); k += TL::THREADS) {
+    const int r = k / (BN / 8), ch = k % (BN / 8);
+    if (r >= mrows || ch * 8 >= nrows) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(smem + r * BN * 2 + ((ch ^ (r & 31)) << 4));
+    uint16_t* dst = c + r * p.ldc + ch * 8;
     if (ch * 8 + 8 <= nrows) {
       store16(dst, v);
     } else {
@@ -565,14 +629,15 @@ __global__ void __launch_bounds__(512, 2) block_mm_large_kernel(MmArgs p) {
   }
 }
 
+template <class TL>
 int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
   MmArgs p = a;
-  p.ntm = int(ceil_div(p.M, 256));
-  p.ntn = int(ceil_div(p.N, 256));
+  p.ntm = int(ceil_div(p.M, TL::BM));
+  p.ntn = int(ceil_div(p.N, TL::BN));
   const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
   prof_begin("block_mm_large", s);
-  if (b_tile) block_mm_large_kernel<true><<<grid, 512, 0, s>>>(p);
-  else block_mm_large_kernel<false><<<grid, 512, 0, s>>>(p);
+  if (b_tile) block_mm_large_kernel<TL, true><<<grid, TL::THREADS, 0, s>>>(p);
+  else block_mm_large_kernel<TL, false><<<grid, TL::THREADS, 0, s>>>(p);
   prof_end(s);
   return launched();
 }
@@ -1044,13 +1109,13 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 
 // Which kernel a product takes.  Measured on an MI355X (256 CUs, one workgroup of 256 x 256 or 128 x
 // 128, or two of 64 x 64, a CU), in us a round of workgroups with `steps` runs:
-//   256 x 256             5   + 1.72 steps  (4096 x 4096 x 4096 60.5, 16384 x 4096 x 4096 4 x 68)
-//   128 x 128             2.5 + 0.8  steps  (2048 x 2048 x 2048 16.0)
+//   256 x 256             5   + 1.72 steps  (4096 x 4096 x 4096 61.7, 16384 x 4096 x 4096 4 x 68)
+//   128 x 128             5.7 + 0.53 steps  (2048 x 2048 x 2048 14.2, 2048 x 2048 x 8192 39.6)
 //   64 x 64, two a CU     2   + 0.5  steps  (2048 x 2048 x 2048 19.6 in two rounds)
 //   64 x 64, two groups   3   + 0.28 steps  (256 x 4096 x 4096 11.1, 12.6 with one group)
-// The sizes' best is the least of these, and so for fp32 results, whose steps all take about 1.6
-// times as long (there is no 256 x 256 kernel for them).  Where a few rows past a multiple of 256
-// cost a further round, they go to a launch of 64 x 64 tiles.
+// The sizes' best is the least of these.  fp32 results have no 256 x 256 kernel and another 128 x 128
+// one (2.5 + 0.8 against 2 + 0.5 of the 64 x 64 tiles, all of its steps 1.6 times as long).  Where a few
+// rows past a multiple of 256 cost a further round, they go to a launch of 64 x 64 tiles.
 enum MmKind { MM_LARGE, MM_128, MM_64, MM_64X2 };
 struct MmPlan {
   MmKind kind;
@@ -1068,7 +1133,7 @@ MmPlan mm_plan(long long M, long long N, int steps, bool f32) {
                      : MmPlan{MM_64, ceil_div(t, 2 * kCus) * (2 + 0.5 * steps), 0};
   };
   MmPlan best = small(M);
-  const double mid = ceil_div(tiles(M, 128), kCus) * (2.5 + 0.8 * steps);
+  const double mid = ceil_div(tiles(M, 128), kCus) * (f32 ? 2.5 + 0.8 * steps : 5.7 + 0.53 * steps);
   if (mid < best.us) best = {MM_128, mid, 0};
   if (f32) return best;
   if (large(M) < best.us) best = {MM_LARGE, large(M), 0};
@@ -1085,17 +1150,20 @@ int launch_mm(const MmArgs& p, bool b_tile, bool f32, hipStream_t s) {
   switch (plan.kind) {
     case MM_64X2: return launch_mm_mid<MidTile<64, 64, 2, 2, 2>>(p, b_tile, f32, s);
     case MM_64: return launch_mm_mid<MidTile<64, 64, 2, 2, 1>>(p, b_tile, f32, s);
-    case MM_128: return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
+    case MM_128:
+      if (!f32) return launch_mm_large<LargeTile<4, 2, 2, 2>>(p, b_tile, s);
+      return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
     case MM_LARGE: break;
   }
-  if (plan.peel == 0) return launch_mm_large(p, b_tile, s);
+  using Large = LargeTile<8, 2, 4, 1>;
+  if (plan.peel == 0) return launch_mm_large<Large>(p, b_tile, s);
   MmArgs head = p, rest = p;
   head.M = p.M - plan.peel;
   rest.M = plan.peel;
   rest.A += int64_t(head.M) * p.lda;
   rest.SA += head.M;
   rest.C = static_cast<uint16_t*>(p.C) + int64_t(head.M) * p.ldc;
-  if (const int rc = launch_mm_large(head, b_tile, s)) return rc;
+  if (const int rc = launch_mm_large<Large>(head, b_tile, s)) return rc;
   return launch_mm(rest, b_tile, f32, s);
 }
 

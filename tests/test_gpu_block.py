@@ -213,7 +213,7 @@ def test_product_added_to_c(M, N, K):
 # every tile size and its edges: 64 x 64 (with and without the split over two groups), 128 x 128,
 # 256 x 256 (one step and several, whole and partial last runs), and a few rows past a multiple of 256
 @pytest.mark.parametrize("M,N,K", [(2000, 900, 300), (2000, 900, 128), (2000, 900, 40), (2100, 1030, 300),
-                                   (1030, 2100, 1153), (4100, 512, 128), (700, 256, 1040), (300, 500, 131),
+                                   (1030, 2100, 1153), (2100, 1030, 1280), (1100, 1900, 520), (4100, 512, 128), (700, 256, 1040), (300, 500, 131),
                                    (2900, 2890, 256), (2900, 2890, 100), (2890, 2900, 300), (2900, 2890, 129),
                                    (2816, 2816, 1000), (8195, 2048, 128), (8195, 2050, 140)])
 def test_product_of_many_tiles(M, N, K):
