@@ -363,8 +363,8 @@ int moe_balance_fwd(const moe_desc* d, const float* logits, const int32_t* topk_
  * (MOE_EUNSUPPORTED).  counts: moe_balance_fwd's [E+1] (a job of several ranks
  * may sum them over the ranks in between: f and n are taken from it, n from
  * counts[E]); dlosses: device float32 [2]; dlogits: device float32 [T, E], every
- * entry written, not `logits` itself.  Other requirements as moe_balance_fwd.  With T = 0 it returns
- * MOE_OK and touches nothing. */
+ * entry written, apart from every input (MOE_EINVAL).  Other requirements as
+ * moe_balance_fwd.  With T = 0 it returns MOE_OK and touches nothing. */
 int moe_balance_bwd(const moe_desc* d, const float* logits, const uint8_t* valid,
                     const int32_t* counts, const float* dlosses, const int32_t* topk_idx,
                     const float* topk_w, const float* dtopk_w, float* dlogits, void* stream);
@@ -382,8 +382,9 @@ enum moe_scale { MOE_SCALE_TILE = 0, MOE_SCALE_BLOCK = 1 };
  *   MOE_SCALE_BLOCK  a scale for each 128 x 128 block: [ceil(R/128), ceil(C/128)].
  * Its last runs and blocks may be partial.  scale = amax / 448 (fp32 division; 1
  * where that is 0), code = e4m3(x / scale) of the fp32 quotient, to nearest even,
- * saturating at 448; the value is code * scale.  A NaN keeps its code NaN, and
- * an infinity makes its run or block NaN. */
+ * saturating at 448; the value is code * scale.  A NaN keeps its code NaN and
+ * leaves the rest of its run as it was; an infinity gives its run or block the
+ * scale inf and the codes of x / inf, whose values are NaN. */
 typedef struct moe_block_quant_desc {
   int32_t rows, cols;
   int32_t in_type;     /* MOE_TYPE_F32 or MOE_TYPE_BF16 */
@@ -404,10 +405,10 @@ typedef struct moe_block_quant_desc {
  * sizes, types other than those above and row strides that are too small.
  * The bytes of a row of codes from its last column to the next multiple of 16
  * are written 0; those behind them are left as they were.  codes and codes_t
- * 16-byte aligned, their strides multiples of 16, scales 4-byte, x aligned to its element
- * (MOE_EALIGN).  A stride of 2^22 or more, or scales or tiles past 2^31 bytes or
- * launches, are MOE_EUNSUPPORTED.  An empty matrix is MOE_OK and touches
- * nothing.  Asynchronous on `stream`; allocates nothing. */
+ * 16-byte aligned, their strides multiples of 16, scales 4-byte, x aligned to its
+ * element (MOE_EALIGN).  A stride of codes of 2^22 or more, one of x of 2^40 or
+ * more, and ceil(rows/16) ceil(cols/128) >= 2^24 are MOE_EUNSUPPORTED.  An empty
+ * matrix is MOE_OK and touches nothing.  Asynchronous on `stream`; allocates nothing. */
 int moe_block_quant(const moe_block_quant_desc* q, const void* x, uint8_t* codes, float* scales,
                     uint8_t* codes_t, float* scales_t, void* stream);
 
@@ -442,7 +443,8 @@ typedef struct moe_block_mm_desc {
  * moe_block_mm_scratch_bytes(m) (MOE_ESCRATCH; 0 bytes: it may be NULL), used only
  * during the call.  MOE_EINVAL for null pointers, negative sizes, bad types or
  * flags and strides that are too small; MOE_EUNSUPPORTED for strides of 2^22 or more
- * (lda, ldb) or scales past 2^31 bytes; moe_block_mm_scratch_bytes is then 0.
+ * (lda, ldb), scales past 2^31 bytes, values past moe_block_quant's limits (the
+ * scratch size is 0 for all of these) and more tiles than a launch holds (2^23).
  * The order of the sums depends on the sizes alone: the same inputs give
  * the same bits.  Asynchronous on `stream`; allocates nothing. */
 size_t moe_block_mm_scratch_bytes(const moe_block_mm_desc* m);
@@ -481,8 +483,8 @@ int moe_grad_norm(const moe_grad* g, int32_t count, float* norm, void* scratch,
  * one 0, or NaN where src is not finite); the product is fp32, rounded once.
  * norm is read on the GPU when the call runs (moe_grad_norm's, or that of
  * several ranks together).  max_norm >= 0 and finite (MOE_EINVAL).  Where dst is src
- * and c is 1 nothing is written.  Overlapping memory as described at moe_grad is
- * MOE_EINVAL.  Other requirements as moe_grad_norm. */
+ * and c is 1 nothing is written.  Overlapping memory as described at moe_grad, and
+ * norm inside a dst, are MOE_EINVAL.  Other requirements as moe_grad_norm. */
 int moe_grad_clip(const moe_grad* g, int32_t count, const float* norm, float max_norm,
                   void* stream);
 

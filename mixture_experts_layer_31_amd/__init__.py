@@ -202,6 +202,14 @@ def _addresses(*tensors):
     return out
 
 
+def _scratch(t) -> tuple:
+    """(address, bytes) of a scratch tensor on the current GPU; (None, 0) where it does not fit or is None."""
+    import torch
+    if t is None or t.get_device() != torch.cuda.current_device() or not t.is_contiguous():
+        return None, 0
+    return t.data_ptr(), _nbytes(t)
+
+
 def _types() -> tuple:
     """(fp32, int32, masks, codes, values by moe_type)"""
     global _type_sets
@@ -227,8 +235,7 @@ def moe_balance_fwd(desc, logits, topk_idx, valid, counts, mean_p, losses, scrat
                     (mean_p, f32, E), (losses, f32, 2))
     if at is None:
         return MOE_EINVAL
-    return lib().moe_balance_fwd(ctypes.byref(desc), *at, _p(scratch), 0 if scratch is None else _nbytes(scratch),
-                                 _stream(stream))
+    return lib().moe_balance_fwd(ctypes.byref(desc), *at, *_scratch(scratch), _stream(stream))
 
 
 def moe_balance_bwd(desc, logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, dlogits,
@@ -290,14 +297,13 @@ def moe_block_mm(desc, a, a_scales, b, b_scales, c, scratch=None, stream=None) -
                     (c, io.get(desc.c_type, ()), M, N, desc.ldc))
     if at is None:
         return MOE_EINVAL
-    return lib().moe_block_mm(ctypes.byref(desc), *at, _p(scratch), 0 if scratch is None else _nbytes(scratch),
-                              _stream(stream))
+    return lib().moe_block_mm(ctypes.byref(desc), *at, *_scratch(scratch), _stream(stream))
 
 
 def make_grad_list(src, dst=None):
     """The moe_grad array of contiguous GPU tensors (float32 or bfloat16) and of where their clipped
     values go (default: in place).  It holds addresses: keep the tensors alive, and make it anew when
-    they move."""
+    they move.  The calls that take it refuse it with another GPU current than the tensors'."""
     import torch
     types = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
     src = list(src)
@@ -309,8 +315,15 @@ def make_grad_list(src, dst=None):
             raise ValueError("gradients are float32 or bfloat16, their destinations alike")
         if not (s.is_cuda and d.device == s.device == src[0].device and s.is_contiguous() and d.is_contiguous()):
             raise ValueError("gradients and destinations are contiguous tensors on one GPU")
-    return (moe_grad * len(src))(*[moe_grad(s.data_ptr(), d.data_ptr(), s.numel(), types[s.dtype], 0)
-                                   for s, d in zip(src, dst)])
+    grads = (moe_grad * len(src))(*[moe_grad(s.data_ptr(), d.data_ptr(), s.numel(), types[s.dtype], 0)
+                                    for s, d in zip(src, dst)])
+    grads.device = src[0].get_device() if src else None
+    return grads
+
+
+def _grads_elsewhere(grads) -> bool:
+    import torch
+    return getattr(grads, "device", None) not in (None, torch.cuda.current_device())
 
 
 def moe_grad_scratch_bytes(count: int) -> int:
@@ -319,15 +332,14 @@ def moe_grad_scratch_bytes(count: int) -> int:
 
 def moe_grad_norm(grads, norm, scratch, stream=None) -> int:
     at = _addresses((norm, _types()[0], 1))
-    if at is None:
+    if at is None or _grads_elsewhere(grads):
         return MOE_EINVAL
-    return lib().moe_grad_norm(grads, len(grads), *at, _p(scratch),
-                               0 if scratch is None else _nbytes(scratch), _stream(stream))
+    return lib().moe_grad_norm(grads, len(grads), *at, *_scratch(scratch), _stream(stream))
 
 
 def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> int:
     at = _addresses((norm, _types()[0], 1))
-    if at is None:
+    if at is None or _grads_elsewhere(grads):
         return MOE_EINVAL
     return lib().moe_grad_clip(grads, len(grads), *at, max_norm, _stream(stream))
 

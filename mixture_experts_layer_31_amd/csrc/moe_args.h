@@ -9,6 +9,12 @@ namespace moe {
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline int launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
 inline size_t type_bytes(int32_t t) { return t == MOE_TYPE_F32 ? 4 : t == MOE_TYPE_BF16 ? 2 : 1; }
+// HIP counts a launch's threads in 32 bits.
+inline bool launchable(long long blocks, int threads) { return blocks * threads < (1LL << 32); }
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
 inline long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Sixteen bytes at any element's address: gfx950 takes global accesses that are not

@@ -14,8 +14,9 @@
 // with LDS atomics (integers: their order does not show).  Up to kBalOneBlock tokens
 // one block does it all; past that a second launch adds the blocks' partial sums, in 64
 // bits, 64 experts a block, and its last block the loss.  Sums over one block's
-// tokens are fp32: at most a few dozen p <= 1 a lane.  Partial sums in global
-// atomics would be one launch fewer and another result with each run.
+// tokens are fp32: T / 16384 p <= 1 a lane past 16384 tokens, T / 4096 past 256 experts.
+// Partial sums in global atomics would be one launch fewer and another result with
+// each run.
 #include <type_traits>
 
 #include "moe_args.h"
@@ -509,13 +510,16 @@ int moe_balance_bwd(const moe_desc* d, const float* logits, const uint8_t* valid
   }
   if (router && d->K > 64) return MOE_EUNSUPPORTED;
   if (d->T == 0) return MOE_OK;
-  if (logits == nullptr || counts == nullptr || dlosses == nullptr || dlogits == nullptr ||
-      static_cast<const void*>(dlogits) == logits)
-    return MOE_EINVAL;
+  if (logits == nullptr || counts == nullptr || dlosses == nullptr || dlogits == nullptr) return MOE_EINVAL;
   if (!aligned_to(logits, 4) || !aligned_to(counts, 4) || !aligned_to(dlosses, 4) ||
       !aligned_to(topk_idx, 4) || !aligned_to(topk_w, 4) || !aligned_to(dtopk_w, 4) ||
       !aligned_to(dlogits, 4))
     return MOE_EALIGN;
+  const size_t T = d->T, E = d->E, pairs = T * d->K, out = T * E * 4;
+  if (overlap(dlogits, out, logits, out) || overlap(dlogits, out, valid, T) || overlap(dlogits, out, counts, E * 4 + 4) ||
+      overlap(dlogits, out, dlosses, 8) || overlap(dlogits, out, topk_idx, pairs * 4) ||
+      overlap(dlogits, out, topk_w, pairs * 4) || overlap(dlogits, out, dtopk_w, pairs * 4))
+    return MOE_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool vec = d->E % 4 == 0 && aligned_to(logits, 16) && aligned_to(dlogits, 16);
   prof_begin("balance_bwd", s);

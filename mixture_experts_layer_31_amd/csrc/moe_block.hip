@@ -48,6 +48,7 @@ struct Quant {
     up = scale < 0x1p-60f ? 0x1p+80f : 1.f;
     s = scale * up;
     r = 1.f / s;
+    if (r == 0.f) s = 1.f;  // an infinite scale: 0 of what is finite, NaN of what is not
   }
   __device__ __forceinline__ float quotient(float x) const {
     x *= up;
@@ -667,6 +668,7 @@ int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
   MmArgs p = a;
   p.ntm = int(ceil_div(p.M, TL::BM));
   p.ntn = int(ceil_div(p.N, TL::BN));
+  if (!launchable((long long)p.ntm * p.ntn, TL::THREADS)) return MOE_EUNSUPPORTED;
   const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
   prof_begin("block_mm_large", s);
   if (b_tile) block_mm_large_kernel<TL, true><<<grid, TL::THREADS, 0, s>>>(p);
@@ -926,6 +928,7 @@ int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
   MmArgs p = a;
   p.ntm = int(ceil_div(p.M, TL::BM));
   p.ntn = int(ceil_div(p.N, TL::BN));
+  if (!launchable((long long)p.ntm * p.ntn, TL::THREADS)) return MOE_EUNSUPPORTED;
   const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
   prof_begin("block_mm_mid", s);
   if (b_tile) {
@@ -1135,9 +1138,9 @@ int launch_direct(const DirectArgs& a, bool b_tile, bool f32, hipStream_t s) {
 
 // C = 0: a product over nothing.
 template <class T>
-__global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int N) {
-  T* row = C + int64_t(blockIdx.x) * ldc;
-  for (int j = threadIdx.x; j < N; j += 256) row[j] = T(0);
+__global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int M, int N) {
+  for (int64_t r = blockIdx.x; r < M; r += gridDim.x)
+    for (int64_t j = threadIdx.x; j < N; j += 256) C[r * ldc + j] = T(0);
 }
 
 // Which kernel a product takes.  Measured on an MI355X (256 CUs, one workgroup of 256 x 256 or 128 x
@@ -1238,10 +1241,10 @@ int check_mm_desc(const moe_block_mm_desc* m) {
   if ((m->flags & MOE_MM_ACCUMULATE) && m->c_type != MOE_TYPE_F32) return MOE_EINVAL;
   if (m->lda < m->K || m->ldb < m->K || m->ldc < m->N) return MOE_EINVAL;
   if (m->lda >= kMaxStride || m->ldb >= kMaxStride) return MOE_EUNSUPPORTED;
-  // scale entries and tile numbers are counted in 31 bits, offsets into C's rows in 63
+  // scale entries are counted in 31 bits, offsets into C's rows in 63
   const long long steps = ceil_div(m->K, 128), wide = m->M > m->N ? m->M : m->N;
   if (steps * wide * 4 >= (1LL << 31) || m->ldc >= (1LL << 40)) return MOE_EUNSUPPORTED;
-  if (ceil_div(m->M, 16) * ceil_div(m->N, 16) >= (1LL << 31)) return MOE_EUNSUPPORTED;
+  if (quantised_by_call(*m) && !launchable(ceil_div(m->M, 16) * steps, 256)) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
@@ -1275,7 +1278,7 @@ int moe_block_quant(const moe_block_quant_desc* q, const void* x, uint8_t* codes
     return MOE_EALIGN;
   if (q->ld_in >= (1LL << 40) || (codes && q->ld_codes >= kMaxStride) ||
       (codes_t && q->ld_codes_t >= kMaxStride) ||
-      ceil_div(q->rows, 128) * ceil_div(q->cols, 128) >= (1LL << 31))
+      !launchable(ceil_div(q->rows, 16) * ceil_div(q->cols, 128), 256))
     return MOE_EUNSUPPORTED;
   QuantArgs a = quant_args(x, q->rows, q->cols, q->ld_in);
   a.q = codes;
@@ -1315,8 +1318,9 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
   if (m->K == 0) {
     if (m->flags & MOE_MM_ACCUMULATE) return MOE_OK;
     prof_begin("block_zero", s);
-    if (f32) block_zero_kernel<<<unsigned(m->M), 256, 0, s>>>(static_cast<float*>(c), m->ldc, m->N);
-    else block_zero_kernel<<<unsigned(m->M), 256, 0, s>>>(static_cast<uint16_t*>(c), m->ldc, m->N);
+    const unsigned grid = unsigned(m->M < 65536 ? m->M : 65536);
+    if (f32) block_zero_kernel<<<grid, 256, 0, s>>>(static_cast<float*>(c), m->ldc, m->M, m->N);
+    else block_zero_kernel<<<grid, 256, 0, s>>>(static_cast<uint16_t*>(c), m->ldc, m->M, m->N);
     prof_end(s);
     return launched();
   }

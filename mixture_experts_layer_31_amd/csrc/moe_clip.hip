@@ -252,8 +252,8 @@ struct Range {
   int32_t entry;
 };
 
-// Whether some dst overlaps another dst, or a src other than its own whole one.
-int check_overlaps(const moe_grad* g, int32_t count) {
+// Whether some dst overlaps another dst, a src other than its own whole one, or the norm.
+int check_overlaps(const moe_grad* g, int32_t count, const float* norm) {
   if (count == 0) return MOE_OK;
   Range* r = new (std::nothrow) Range[count];
   if (r == nullptr) return MOE_EHIP;
@@ -268,6 +268,7 @@ int check_overlaps(const moe_grad* g, int32_t count) {
     if (r[k].a < r[k - 1].b) rc = MOE_EINVAL;
   for (int32_t i = 0; rc == MOE_OK && i < count; ++i) {
     if (g[i].n == 0) continue;
+    if (overlap(g[i].dst, size_t(g[i].n) * type_bytes(g[i].type), norm, 4)) rc = MOE_EINVAL;
     const uintptr_t a = reinterpret_cast<uintptr_t>(g[i].src);
     const uintptr_t b = a + uintptr_t(g[i].n) * type_bytes(g[i].type);
     // the dsts are disjoint and sorted: the first that ends past a
@@ -365,7 +366,7 @@ int moe_grad_clip(const moe_grad* g, int32_t count, const float* norm, float max
   if (rc && rc != MOE_EALIGN) return rc;
   if (norm == nullptr || !(max_norm >= 0.f) || std::isinf(max_norm)) return MOE_EINVAL;
   if (rc || !aligned_to(norm, 4)) return MOE_EALIGN;
-  if ((rc = check_overlaps(g, count))) return rc;
+  if ((rc = check_overlaps(g, count, norm))) return rc;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return for_lists(g, count, [&](const GradList& L) {
     prof_begin("grad_scale", s);

@@ -143,6 +143,25 @@ def test_quantiser_of_nan_and_inf():
     assert np.isfinite(v[0]).sum() == 255 and np.isnan(v[1, 128:]).all() and np.isfinite(v[1, :128]).all()
 
 
+@pytest.mark.parametrize("t", [BF, F32])
+def test_infinite_scales_follow_the_definition(t):
+    """x / inf: codes 0, NaN (either sign) where x is infinite; and the padding stays 0."""
+    x = _x(5, 130, 140, t)
+    x[3, 7], x[100, 139], x[129, 0] = float("inf"), -float("inf"), float("inf")
+    f = x.float().numpy()
+    with np.errstate(invalid="ignore"):
+        for scale in (TILE, BLOCK):
+            q, s, qt, st = _quant(x, scale, t=t)
+            want = [bk.quant_tiles(f), bk.quant_tiles(f.T)] if scale == TILE else [bk.quant_blocks(f)]
+            if scale == BLOCK:
+                want.append((want[0][0].T, want[0][1].T))
+            # inf / inf is a NaN, which the oracle's encoder does not take
+            for got, sc, n, nan, (wq, ws) in ((q, s, 140, np.isinf(f), want[0]), (qt, st, 130, np.isinf(f.T), want[1])):
+                assert np.array_equal(sc, ws) and np.isinf(ws).any()
+                _same_codes(np.where(np.pad(nan, ((0, 0), (0, got.shape[1] - n))), 0, got), np.where(nan, 0, wq), n)
+                assert np.isnan(q8.e4m3_decode(got[:, :n][nan])).all()
+
+
 # ---------------------------------------------------------------- product
 
 def _codes(seed, R, K, scale, ld_extra=16, junk=0x7F):
@@ -368,4 +387,10 @@ def test_binding_refuses_tensors_that_do_not_fit():
                 (a, sa, torch.zeros(32, 8, dtype=torch.uint8, device="cuda").t(), sb, c)):
         assert moe.moe_block_mm(d, *bad, scratch) == moe.MOE_EINVAL
     assert moe.moe_block_mm(d, a.view(torch.float8_e4m3fn), sa, b, sb, c, scratch) == moe.MOE_OK
+    v = moe.make_block_mm_desc(4, 8, 32, a_type=BF)
+    x = torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda")
+    room = torch.zeros(moe.moe_block_mm_scratch_bytes(v), dtype=torch.uint8)
+    assert moe.moe_block_mm(v, x, None, b, sb, c, room.cuda()) == moe.MOE_OK
+    for bad in (room, None):
+        assert moe.moe_block_mm(v, x, None, b, sb, c, bad) == moe.MOE_EINVAL
     torch.cuda.synchronize()

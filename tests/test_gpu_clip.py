@@ -165,3 +165,14 @@ def test_same_bits_other_stream_and_graph():
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(ref, [norm, *out]))
+
+
+def test_binding_refuses_what_is_elsewhere():
+    x, norm = torch.ones(10, device="cuda"), torch.ones(1, device="cuda")
+    lst, room = moe.make_grad_list([x]), torch.zeros(moe.moe_grad_scratch_bytes(1), dtype=torch.uint8)
+    assert moe.moe_grad_norm(lst, norm, room) == moe.MOE_EINVAL  # scratch in host memory
+    assert moe.moe_grad_norm(lst, norm.cpu(), room.cuda()) == moe.MOE_EINVAL
+    lst.device = 1  # gradients of another GPU than the current one
+    assert moe.moe_grad_norm(lst, norm, room.cuda()) == moe.MOE_EINVAL
+    assert moe.moe_grad_clip(lst, norm, 1.0) == moe.MOE_EINVAL
+    assert moe.moe_grad_clip(moe.make_grad_list([x]), x, 1.0) == moe.MOE_EINVAL  # the norm among the gradients

@@ -41,6 +41,10 @@ def test_balance_refusals():
         assert _bal_bwd(ok, **{k: None}) == EINVAL, k
         assert _bal_bwd(ok, **{k: FAKE + 2}) == EALIGN, k
     assert _bal_bwd(ok, dz=FAKE) == EINVAL  # dlogits over the logits
+    far = FAKE + (1 << 30)
+    for at, k in ((far, "z"), (far + 64 * 128 * 4 - 4, "counts"), (far - 4, "dl"), (far - 8, "valid"), (far - 64 * 8 * 4 + 4, "idx")):
+        parts = dict(idx=FAKE + (1 << 20), w=FAKE + (1 << 20), dw=FAKE + (1 << 20))
+        assert _bal_bwd(ok, **{**parts, "dz": far, k: at}) == EINVAL, k
     for part in (dict(idx=FAKE), dict(idx=FAKE, w=FAKE), dict(w=FAKE, dw=FAKE)):
         assert _bal_bwd(ok, **part) == EINVAL, part
     assert _bal_bwd(ok, idx=FAKE, w=FAKE + 1, dw=FAKE) == EALIGN
@@ -78,6 +82,20 @@ def test_block_quant_refusals():
 
 def _mm(m, a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, c=FAKE, scratch=None, n=0):
     return moe.lib().moe_block_mm(ctypes.byref(m), a, sa, b, sb, c, scratch, n, None)
+
+
+def test_block_quant_limits():
+    mk = moe.make_block_quant_desc
+    assert _quant(mk(2 ** 31 - 1, 1)) == EUNSUP
+    assert _quant(mk(1, 2 ** 31 - 1), codes=None, scales=None, codes_t=FAKE, scales_t=FAKE) == EUNSUP
+    assert _quant(mk(4096, 4096, ld_in=1 << 40)) == EUNSUP
+
+
+def test_block_mm_limits():
+    mk = moe.make_block_mm_desc
+    assert _mm(mk(2 ** 28, 2 ** 16, 16), n=0) == EUNSUP  # 2^32 tiles of 64 x 64 or more
+    big = mk(2 ** 28, 64, 16, a_type=moe.MOE_TYPE_BF16)
+    assert _mm(big, sa=None, scratch=FAKE, n=1 << 62) == EUNSUP and moe.moe_block_mm_scratch_bytes(big) == 0
 
 
 def test_block_mm_refusals():
@@ -167,7 +185,9 @@ def test_overlapping_destinations_are_refused():
         [(a, a, 100, F32, 0), (a + 396, b, 1, F32, 0)],           # reads what another writes
     )
     for e in overlapping:
-        assert _clip(_list(*e)) == EINVAL, e
+        assert _clip(_list(*e), norm=a - 64) == EINVAL, e
+    for norm in (b, b + 396):  # a dst over the norm
+        assert _clip(_list((a, b, 100, F32, 0)), norm=norm) == EINVAL
 
 
 def test_binding_refuses_tensors_that_do_not_fit():
