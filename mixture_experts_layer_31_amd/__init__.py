@@ -180,26 +180,27 @@ def moe_router_bwd(desc, topk_idx, topk_w, dtopk_w, dlogits, stream=None) -> int
 
 def _addresses(*tensors):
     """The device addresses of (tensor, element types, count) for contiguous GPU tensors of one of those
-    types with that many elements at least, or of (tensor, types, rows, columns, row stride) for so many
-    rows of their own stride; None where one does not fit, all of them on the current device, whose stream
-    the call takes.  None and raw addresses go through: they are the C side's to check."""
+    types with that many elements at least (count None: _rows_fit has seen to it); None where one does not
+    fit, all of them on the current device, whose stream the call takes.  None and raw addresses go through:
+    they are the C side's to check."""
     import torch
     dev, out = torch.cuda.current_device(), []
-    for t, types, n, *row in tensors:
-        if t is None or isinstance(t, int):
+    for t, types, n in tensors:
+        if t is None or t.__class__ is int:
             out.append(t)
-            continue
-        if t.dtype not in types or t.get_device() != dev:
+        elif t.dtype in types and t.get_device() == dev and (n is None or t.numel() >= n and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
             return None
-        if row:
-            if t.dim() != 2 or t.size(0) < n or t.size(1) < row[0]:
-                return None
-            if (n > 1 and t.stride(0) != row[1]) or (row[0] > 1 and t.stride(1) != 1):
-                return None
-        elif t.numel() < n or not t.is_contiguous():
-            return None
-        out.append(t.data_ptr())
     return out
+
+
+def _rows_fit(t, rows: int, cols: int, ld: int) -> bool:
+    """Whether a tensor has that many rows and columns, ld elements between its rows."""
+    if t is None or t.__class__ is int:
+        return True
+    return t.dim() == 2 and t.size(0) >= rows and t.size(1) >= cols and \
+        (rows <= 1 or t.stride(0) == ld) and (cols <= 1 or t.stride(1) == 1)
 
 
 def _scratch(t) -> tuple:
@@ -266,8 +267,11 @@ def moe_block_quant(desc, x, codes, scales, codes_t=None, scales_t=None, stream=
     rb, cb = (R + 127) // 128, (C + 127) // 128
     block = desc.scale == MOE_SCALE_BLOCK
     f32, _, _, code, io = _types()
-    at = _addresses((x, io.get(desc.in_type, ()), R, C, desc.ld_in), (codes, code, R, _code_ld(C), desc.ld_codes),
-                    (scales, f32, cb * (rb if block else R)), (codes_t, code, C, _code_ld(R), desc.ld_codes_t),
+    if not (_rows_fit(x, R, C, desc.ld_in) and _rows_fit(codes, R, _code_ld(C), desc.ld_codes)
+            and _rows_fit(codes_t, C, _code_ld(R), desc.ld_codes_t)):
+        return MOE_EINVAL
+    at = _addresses((x, io.get(desc.in_type, ()), None), (codes, code, None),
+                    (scales, f32, cb * (rb if block else R)), (codes_t, code, None),
                     (scales_t, f32, rb * (cb if block else C)))
     if at is None:
         return MOE_EINVAL
@@ -291,10 +295,13 @@ def moe_block_mm(desc, a, a_scales, b, b_scales, c, scratch=None, stream=None) -
     M, N, K = desc.M, desc.N, desc.K
     steps, own = (K + 127) // 128, desc.a_type == MOE_TYPE_E4M3
     f32, _, _, code, io = _types()
-    at = _addresses((a, code if own else io.get(desc.a_type, ()), M, _code_ld(K) if own else K, desc.lda),
-                    (a_scales, f32, steps * M), (b, code, N, _code_ld(K), desc.ldb),
+    ldk = _code_ld(K)
+    if not (_rows_fit(a, M, ldk if own else K, desc.lda) and _rows_fit(b, N, ldk, desc.ldb)
+            and _rows_fit(c, M, N, desc.ldc)):
+        return MOE_EINVAL
+    at = _addresses((a, code if own else io.get(desc.a_type, ()), None), (a_scales, f32, steps * M), (b, code, None),
                     (b_scales, f32, steps * (N if desc.b_scale == MOE_SCALE_TILE else (N + 127) // 128)),
-                    (c, io.get(desc.c_type, ()), M, N, desc.ldc))
+                    (c, io.get(desc.c_type, ()), None))
     if at is None:
         return MOE_EINVAL
     return lib().moe_block_mm(ctypes.byref(desc), *at, *_scratch(scratch), _stream(stream))
