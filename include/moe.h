@@ -441,7 +441,7 @@ typedef struct moe_block_mm_desc {
  * MOE_OK and touches nothing.  a, b (codes) 16-byte aligned; values, C and
  * scales aligned to their element (MOE_EALIGN); scratch 16-byte aligned, of
  * moe_block_mm_scratch_bytes(m) (MOE_ESCRATCH; 0 bytes: it may be NULL), used only
- * during the call.  MOE_EINVAL for null pointers, negative sizes, bad types or
+ * during the call (the codes of values; the sums of a long contraction's parts).  MOE_EINVAL for null pointers, negative sizes, bad types or
  * flags and strides that are too small; MOE_EUNSUPPORTED for strides of 2^22 or more
  * (lda, ldb), scales past 2^31 bytes, values past moe_block_quant's limits (the
  * scratch size is 0 for all of these) and more tiles than a launch holds (2^23).

@@ -336,7 +336,28 @@ struct MmArgs {
   int64_t lda, ldb, ldc;
   void* C;
   bool add;         // C +=
+  int ldsb;         // BLOCK: entries between rows of SB
+  // The contraction in parts of `per` runs, a part a workgroup: the parts' sums go to
+  // part [parts][M][ldp] and are added by block_join_kernel (null: one part, to C).
+  int per;
+  float* part;
+  int64_t ldp;
 };
+
+// Makes p the arguments of the part that holds workgroup l; returns l's place in it.
+template <bool B_TILE>
+__device__ __forceinline__ int take_part(MmArgs& p, int l) {
+  if (p.part == nullptr) return l;
+  const int tiles = p.ntm * p.ntn, s = l / tiles, k0 = s * p.per;
+  p.A += int64_t(k0) * 128;
+  p.B += int64_t(k0) * 128;
+  p.SA += int64_t(k0) * p.ldsa;
+  p.SB += B_TILE ? int64_t(k0) * p.N : k0;
+  p.part += int64_t(s) * p.M * p.ldp;
+  p.K = min(p.K - k0 * 128, p.per * 128);
+  p.ksteps = min(p.ksteps - k0, p.per);
+  return l - s * tiles;
+}
 
 // Eight of the fragment's codes as bf16 (exact), the eighth part s of its 32.
 __device__ __forceinline__ bf16x8 widen(const i32x8& f, int s) {
@@ -372,7 +393,8 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   constexpr int BM = TL::BM, BN = TL::BN, WAVES = TL::WAVES, MB = TL::MB, NB = TL::NB, KG = TL::KG;
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES + (BM + BN) * 4, RING = 2 * STAGE;
   __shared__ __attribute__((aligned(1024))) char lds[KG * RING];
-  const int l = xcd_remap(blockIdx.x, gridDim.x);
+  int l = xcd_remap(blockIdx.x, gridDim.x);
+  if constexpr (KG > 1) l = take_part<B_TILE>(p, l);
   int mt, nt;
   wgrad_mn(l, p.ntm, p.ntn, mt, nt);
   const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4;
@@ -395,11 +417,11 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   static_assert(QA + BN / 64 == WAVES, "a load of scales a wave");
   const bool sis_a = wave < QA;
   const i32x4 rs = sis_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
-                         : make_rsrc(p.SB, uint32_t(p.ksteps) * uint32_t(B_TILE ? p.N : nblocks) * 4u);
+                         : make_rsrc(p.SB, (B_TILE ? uint32_t(p.ksteps) * p.N : uint32_t(nblocks) * p.ldsb) * 4u);
   const int sr = (sis_a ? wave : wave - QA) * 64 + lane;
   const int sstep = sis_a ? p.ldsa * 4 : B_TILE ? p.N * 4 : 4;
   const int soff = sr >= (sis_a ? mrows : nrows) ? int(0x80000000u)
-                   : sis_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ksteps * 4;
+                   : sis_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ldsb * 4;
   // Loads of the group's i-th step (run i KG + kg) into stage s, the q-th of NL; past the last
   // run they miss every buffer (no traffic) and bring zeros.
   constexpr int NL = decltype(sa)::NI + decltype(sb)::NI + 1;
@@ -622,6 +644,12 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
 #pragma unroll
         for (int x = 1; x < KG; ++x) v[q] += *reinterpret_cast<const f32x4*>(at + x * RING);
       }
+      if (p.part != nullptr) {
+        float* dst = p.part + int64_t(m0 + r) * p.ldp + n0 + col;
+        *reinterpret_cast<f32x4*>(dst) = v[0];
+        if (col + 4 < nrows) *reinterpret_cast<f32x4*>(dst + 4) = v[1];
+        continue;
+      }
       const uint32_t w[4] = {pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
                              pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
       uint16_t* dst = c + r * p.ldc + col;
@@ -668,8 +696,9 @@ int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
   MmArgs p = a;
   p.ntm = int(ceil_div(p.M, TL::BM));
   p.ntn = int(ceil_div(p.N, TL::BN));
-  if (!launchable((long long)p.ntm * p.ntn, TL::THREADS)) return MOE_EUNSUPPORTED;
-  const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
+  const long long tiles = (long long)p.ntm * p.ntn * (p.part ? ceil_div(p.ksteps, p.per) : 1);
+  if (!launchable(tiles, TL::THREADS)) return MOE_EUNSUPPORTED;
+  const unsigned grid = unsigned(tiles);
   prof_begin("block_mm_large", s);
   if (b_tile) block_mm_large_kernel<TL, true><<<grid, TL::THREADS, 0, s>>>(p);
   else block_mm_large_kernel<TL, false><<<grid, TL::THREADS, 0, s>>>(p);
@@ -695,7 +724,7 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
   constexpr int LDR = BN + 4;  // join: rows apart in banks
   static_assert(RING >= BM * LDR * 4, "the join fits a group's ring");
   __shared__ __attribute__((aligned(1024))) char smem[KG * RING];
-  const int l = xcd_remap(blockIdx.x, gridDim.x);
+  const int l = take_part<B_TILE>(p, xcd_remap(blockIdx.x, gridDim.x));
   int mt, nt;
   wgrad_mn(l, p.ntm, p.ntn, mt, nt);
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
@@ -719,11 +748,11 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
   const int sq = wave % (QA + QB);
   const bool of_a = sq < QA;
   const i32x4 rs = of_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
-                        : make_rsrc(p.SB, uint32_t(p.ksteps) * uint32_t(B_TILE ? p.N : nblocks) * 4u);
+                        : make_rsrc(p.SB, (B_TILE ? uint32_t(p.ksteps) * p.N : uint32_t(nblocks) * p.ldsb) * 4u);
   const int sr = (of_a ? sq : sq - QA) * 64 + lane;
   const int sstep = of_a ? p.ldsa * 4 : B_TILE ? p.N * 4 : 4;
   const int soff = sr >= (of_a ? mrows : nrows) ? int(0x80000000u)
-                   : of_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ksteps * 4;
+                   : of_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ldsb * 4;
   const uint32_t base = lds_addr(ring);
   // the group's i-th step is run i KG + kg; one past the last misses every buffer and loads zeros
   auto issue = [&](int i) __attribute__((always_inline)) {
@@ -897,6 +926,13 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
       for (int k = 1; k < KG; ++k) t += *reinterpret_cast<const f32x4*>(smem + k * RING + (row * LDR + col + q) * 4);
       v[q] = t[0]; v[q + 1] = t[1]; v[q + 2] = t[2]; v[q + 3] = t[3];
     }
+    if (p.part != nullptr) {
+      float* dst = p.part + int64_t(m0 + row) * p.ldp + n0 + col;
+#pragma unroll
+      for (int q = 0; q < VE; q += 4)
+        if (col + q < nrows) *reinterpret_cast<f32x4*>(dst + q) = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
+      continue;
+    }
     T* dst = c + row * p.ldc + col;
     if (col + VE <= nrows) {
       if constexpr (OUT_F32) {
@@ -928,8 +964,9 @@ int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
   MmArgs p = a;
   p.ntm = int(ceil_div(p.M, TL::BM));
   p.ntn = int(ceil_div(p.N, TL::BN));
-  if (!launchable((long long)p.ntm * p.ntn, TL::THREADS)) return MOE_EUNSUPPORTED;
-  const unsigned grid = unsigned(p.ntm) * unsigned(p.ntn);
+  const long long tiles = (long long)p.ntm * p.ntn * (p.part ? ceil_div(p.ksteps, p.per) : 1);
+  if (!launchable(tiles, TL::THREADS)) return MOE_EUNSUPPORTED;
+  const unsigned grid = unsigned(tiles);
   prof_begin("block_mm_mid", s);
   if (b_tile) {
     if (f32) block_mm_mid_kernel<TL, true, true><<<grid, TL::THREADS, 0, s>>>(p);
@@ -1136,6 +1173,28 @@ int launch_direct(const DirectArgs& a, bool b_tile, bool f32, hipStream_t s) {
   return launched();
 }
 
+// C (+)= the sum of the parts, in their order; four columns a thread.
+template <class T>
+__global__ void __launch_bounds__(256) block_join_kernel(MmArgs p, int parts) {
+  const int quads = int(p.ldp / 4);
+  const int64_t step = int64_t(p.M) * p.ldp;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < int64_t(p.M) * quads; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / quads;
+    const int col = int(i - r * quads) * 4;
+    const float* src = p.part + r * p.ldp + col;
+    f32x4 v = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll 4
+    for (int k = 1; k < parts; ++k) v += *reinterpret_cast<const f32x4*>(src + k * step);
+    T* dst = static_cast<T*>(p.C) + r * p.ldc + col;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (col + q < p.N) {
+        if constexpr (sizeof(T) == 4) dst[q] = p.add ? dst[q] + v[q] : v[q];
+        else dst[q] = uint16_t(pack_bf16x2(v[q], 0.f));
+      }
+  }
+}
+
 // C = 0: a product over nothing.
 template <class T>
 __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int M, int N) {
@@ -1152,65 +1211,100 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 // The sizes' best is the least of these.  fp32 results have no 256 x 256 kernel and another 128 x 128
 // one (2.5 + 0.8 against 2 + 0.5 of the 64 x 64 tiles, all of its steps 1.6 times as long).  Where a few
 // rows past a multiple of 256 cost a further round, they go to a launch of 64 x 64 tiles.
+// With too few tiles for the chip the contraction is cut into parts, whose sums take a second launch:
+// 4 us and their bytes at 3 TB/s, written and read (256 x 256 x 16384 in 16 parts of 8 runs 12.0, whole 31.6;
+// 512 x 512 x 8192 in 4 of 16 13.0, whole 18.2).
 enum MmKind { MM_LARGE, MM_128, MM_64, MM_64X2 };
 struct MmPlan {
   MmKind kind;
   double us;
-  int peel;  // rows at the end that take a launch of their own
+  int peel;   // rows at the end that take a launch of their own
+  int parts, per;  // of the contraction, and runs in each
 };
+constexpr double kPartBytes = 64 << 20;  // most of the parts' sums
 
-MmPlan mm_plan(long long M, long long N, int steps, bool f32) {
+MmPlan mm_plan(long long M, long long N, int steps, bool f32, bool whole = false) {
   constexpr int kCus = 256;
   const auto tiles = [&](long long m, int b) { return ceil_div(m, b) * ceil_div(N, b); };
   const auto large = [&](long long m) { return ceil_div(tiles(m, 256), kCus) * (5 + 1.72 * steps); };
-  const auto small = [&](long long m) {
-    const long long t = tiles(m, 64);
-    return t <= kCus ? MmPlan{MM_64X2, 3 + 0.28 * steps, 0}
-                     : MmPlan{MM_64, ceil_div(t, 2 * kCus) * (2 + 0.5 * steps), 0};
+  MmPlan best{MM_64, 1e30, 0, 1, steps};
+  const auto consider = [&](MmKind kind, long long m, int b, int slots, double fix, double each) {
+    const long long t = tiles(m, b);
+    for (int parts = 1; parts <= 64; parts = parts < 4 ? parts + 1 : parts < 16 ? parts + 2 : parts * 2) {
+      const int per = int(ceil_div(steps, parts));
+      const double bytes = 4. * parts * double(m) * double(N);
+      if (parts > 1 && (whole || t * parts > 2 * slots || per < 4 || bytes > kPartBytes)) break;
+      const double us = ceil_div(t * parts, slots) * (fix + each * per) + (parts > 1 ? 4 + 2 * bytes / 3e6 : 0);
+      if (us < best.us) best = {kind, us, 0, int(ceil_div(steps, per)), per};
+    }
   };
-  MmPlan best = small(M);
-  const double mid = ceil_div(tiles(M, 128), kCus) * (f32 ? 2.5 + 0.8 * steps : 5.7 + 0.53 * steps);
-  if (mid < best.us) best = {MM_128, mid, 0};
+  const double slow = f32 ? 1.6 : 1;
+  consider(MM_64X2, M, 64, kCus, 3, 0.28 * slow);
+  consider(MM_64, M, 64, 2 * kCus, 2, 0.5 * slow);
+  if (f32) consider(MM_128, M, 128, kCus, 2.5, 0.8 * slow);
+  else consider(MM_128, M, 128, kCus, 5.7, 0.53);
   if (f32) return best;
-  if (large(M) < best.us) best = {MM_LARGE, large(M), 0};
+  if (large(M) < best.us) best = {MM_LARGE, large(M), 0, 1, steps};
   const int rest = int(M % 256);
   if (M > 256 && rest > 0 && rest <= 64) {
-    const double us = large(M - rest) + small(rest).us + 1.5;
-    if (us < best.us) best = {MM_LARGE, us, rest};
+    const double us = large(M - rest) + mm_plan(rest, N, steps, f32, true).us + 1.5;
+    if (us < best.us) best = {MM_LARGE, us, rest, 1, steps};
   }
   return best;
 }
 
-int launch_mm(const MmArgs& p, bool b_tile, bool f32, hipStream_t s) {
-  const MmPlan plan = mm_plan(p.M, p.N, p.ksteps, f32);
-  switch (plan.kind) {
-    case MM_64X2: return launch_mm_mid<MidTile<64, 64, 2, 2, 2>>(p, b_tile, f32, s);
-    case MM_64: return launch_mm_mid<MidTile<64, 64, 2, 2, 1>>(p, b_tile, f32, s);
-    case MM_128:
-      if (!f32) return launch_mm_large<LargeTile<4, 2, 2, 2>>(p, b_tile, s);
-      return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
-    case MM_LARGE: break;
+size_t part_bytes(long long M, long long N, const MmPlan& plan) {
+  return plan.parts > 1 ? size_t(plan.parts) * M * (ceil_div(N, 4) * 4) * sizeof(float) : 0;
+}
+
+// Where the plan peels rows, their launch's plan does not use parts.
+int launch_mm(const MmArgs& a, const MmPlan& plan, bool b_tile, bool f32, float* part, hipStream_t s) {
+  MmArgs p = a;
+  p.per = plan.per;
+  p.ldp = (int64_t(p.N) + 3) / 4 * 4;
+  p.part = plan.parts > 1 ? part : nullptr;
+  const auto one = [&]() {
+    switch (plan.kind) {
+      case MM_64X2: return launch_mm_mid<MidTile<64, 64, 2, 2, 2>>(p, b_tile, f32, s);
+      case MM_64: return launch_mm_mid<MidTile<64, 64, 2, 2, 1>>(p, b_tile, f32, s);
+      case MM_128:
+        if (!f32) return launch_mm_large<LargeTile<4, 2, 2, 2>>(p, b_tile, s);
+        return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
+      case MM_LARGE: break;
+    }
+    return launch_mm_large<LargeTile<8, 2, 4, 1>>(p, b_tile, s);
+  };
+  if (plan.peel > 0) {
+    MmArgs rest = p;
+    p.M -= plan.peel;
+    rest.M = plan.peel;
+    rest.A += int64_t(p.M) * p.lda;
+    rest.SA += p.M;
+    rest.C = static_cast<uint16_t*>(p.C) + int64_t(p.M) * p.ldc;
+    if (const int rc = one()) return rc;
+    return launch_mm(rest, mm_plan(rest.M, rest.N, rest.ksteps, f32, true), b_tile, f32, nullptr, s);
   }
-  using Large = LargeTile<8, 2, 4, 1>;
-  if (plan.peel == 0) return launch_mm_large<Large>(p, b_tile, s);
-  MmArgs head = p, rest = p;
-  head.M = p.M - plan.peel;
-  rest.M = plan.peel;
-  rest.A += int64_t(head.M) * p.lda;
-  rest.SA += head.M;
-  rest.C = static_cast<uint16_t*>(p.C) + int64_t(head.M) * p.ldc;
-  if (const int rc = launch_mm_large<Large>(head, b_tile, s)) return rc;
-  return launch_mm(rest, b_tile, f32, s);
+  const int rc = one();
+  if (rc || plan.parts == 1) return rc;
+  const long long blocks = ceil_div((long long)p.M * (p.ldp / 4), 256);
+  const unsigned grid = unsigned(blocks < 4096 ? blocks : 4096);
+  prof_begin("block_join", s);
+  if (f32) block_join_kernel<float><<<grid, 256, 0, s>>>(p, plan.parts);
+  else block_join_kernel<uint16_t><<<grid, 256, 0, s>>>(p, plan.parts);
+  prof_end(s);
+  return launched();
 }
 
 // Whether the one-launch kernel takes the product: for values, up to the work of quantising A again
 // in every workgroup (in runs of 128 values: 64 x 1024 x 1024, 32768 runs, takes 5.8 us against 7.1
 // in two launches, 128 x 1024 x 1024, 65536, 7.9 against 7.2 and a launch's host time, 16 x 4096 x 4096, 131072,
 // 13.9 against 12.1); for codes, up to 4096 runs of tiles (128 x 1024 x 1024: 4.5 us against 4.9; 256 x
-// 1024 x 1024: 7.6 against 5.0), and with one row of tiles up to 16384 (16 x 4096 x 4096: 7.3 against 9.8).
+// 1024 x 1024: 7.6 against 5.0), and with one row of tiles up to 16384 (16 x 4096 x 4096: 7.3 against 9.8),
+// as long as a wave has four runs at most (16 x 512 x 8192: 11.1 against 8.3 in parts and a launch's
+// host time; 16 x 512 x 16384: 19.5 against 9.8).
 bool use_direct(long long M, long long N, long long K, bool values) {
   const long long steps = ceil_div(K, 128), tm = ceil_div(M, 16), tn = ceil_div(N, 16);
-  if (!values) return tm * tn * steps <= (M <= 16 ? 16384 : 4096);
+  if (!values) return steps <= 4 * kDirectWaves && tm * tn * steps <= (M <= 16 ? 16384 : 4096);
   if (K > kDirectK) return false;
   long long wk = 1;
   while (wk < kDirectWaves && wk < steps) wk *= 2;
@@ -1246,6 +1340,10 @@ int check_mm_desc(const moe_block_mm_desc* m) {
   if (steps * wide * 4 >= (1LL << 31) || m->ldc >= (1LL << 40)) return MOE_EUNSUPPORTED;
   if (quantised_by_call(*m) && !launchable(ceil_div(m->M, 16) * steps, 256)) return MOE_EUNSUPPORTED;
   return MOE_OK;
+}
+
+MmPlan plan_of(const moe_block_mm_desc& m) {
+  return mm_plan(m.M, m.N, int(ceil_div(m.K, 128)), m.c_type == MOE_TYPE_F32);
 }
 
 size_t mm_quant_bytes(const moe_block_mm_desc& m, size_t* scales) {
@@ -1293,7 +1391,9 @@ int moe_block_quant(const moe_block_quant_desc* q, const void* x, uint8_t* codes
 size_t moe_block_mm_scratch_bytes(const moe_block_mm_desc* m) {
   if (check_mm_desc(m) != MOE_OK) return 0;
   size_t at;
-  return mm_quant_bytes(*m, &at);
+  const size_t codes = mm_quant_bytes(*m, &at);
+  if (m->M == 0 || m->N == 0 || m->K == 0 || use_direct(m->M, m->N, m->K, quantised_by_call(*m))) return codes;
+  return codes + part_bytes(m->M, m->N, plan_of(*m));
 }
 
 int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scales,
@@ -1339,6 +1439,7 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
   p.C = c;
   p.ldc = m->ldc;
   p.add = (m->flags & MOE_MM_ACCUMULATE) != 0;
+  p.ldsb = p.ksteps;
   const bool bt = m->b_scale == MOE_SCALE_TILE;
   if (use_direct(m->M, m->N, m->K, quant)) {
     const DirectArgs dp{p, a, m->lda, 0};
@@ -1346,10 +1447,10 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
     if (m->a_type == MOE_TYPE_BF16) return launch_direct<A_BF16>(dp, bt, f32, s);
     return launch_direct<A_F32>(dp, bt, f32, s);
   }
+  char* sc = static_cast<char*>(scratch);
+  size_t at;
+  float* part = reinterpret_cast<float*>(sc + mm_quant_bytes(*m, &at));
   if (quant) {
-    char* sc = static_cast<char*>(scratch);
-    size_t at;
-    (void)mm_quant_bytes(*m, &at);
     QuantArgs q = quant_args(a, m->M, m->K, m->lda);
     q.q = reinterpret_cast<uint8_t*>(sc);
     q.ldq = code_ld(m->K);
@@ -1359,7 +1460,7 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
     p.lda = q.ldq;
     p.SA = q.sc;
   }
-  return launch_mm(p, bt, f32, s);
+  return launch_mm(p, plan_of(*m), bt, f32, part, s);
 }
 
 }  // extern "C"

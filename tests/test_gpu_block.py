@@ -241,6 +241,20 @@ def test_product_of_many_tiles(M, N, K):
     _check_mm(M, N, K, BLOCK if K % 2 else TILE, F32, seed=6)
 
 
+@pytest.mark.parametrize("M,N,K", [(64, 300, 2000), (65, 67, 16000), (200, 129, 9000), (257, 131, 16389), (300, 700, 5000),
+                                   (1000, 90, 8100)])
+@pytest.mark.parametrize("ct", [BF, F32])
+def test_long_contraction_in_parts(M, N, K, ct):
+    """Too few tiles for the chip: the contraction over a workgroup's waves, or in parts that a second
+    launch joins."""
+    parts = moe.moe_block_mm_scratch_bytes(moe.make_block_mm_desc(M, N, K, c_type=ct)) // (M * N * 4)
+    assert parts >= 2 or K == 2000
+    for b_scale in (TILE, BLOCK):
+        one = _check_mm(M, N, K, b_scale, ct, ldc=N + 3, off=1, add=ct == F32)
+        if ct == BF:
+            assert np.array_equal(one, _check_mm(M, N, K, b_scale, ct))
+
+
 def test_empty_contraction():
     for ct in (BF, F32):
         c = torch.full((5, 9), 3.0, dtype=DT[ct], device="cuda")
