@@ -8,7 +8,9 @@
 //
 // Both passes read each logit once into registers.  LPT lanes share a token (16 up
 // to 256 experts, so a wave holds four tokens and a row reduction is four DPP
-// moves; 64 above), each with VPL logits of it in runs of four.  The forward
+// moves; 64 above, where 16 would hold 32 logits a lane), each with VPL logits of it in
+// runs of four: 65536 tokens, forward + backward in us, 16 lanes against 64: 64 experts
+// 21.8, 47; 128 experts 29.9, 50; 256 experts 47.4, 52; 512 experts 112, 82.  The forward
 // adds p to per-lane sums over the block's tokens, joined at the end over the
 // wave's tokens and the block's waves in a fixed order, and counts the block's ids
 // with LDS atomics (integers: their order does not show).  Up to kBalOneBlock tokens
@@ -16,7 +18,12 @@
 // bits, 64 experts a block, and its last block the loss.  Sums over one block's
 // tokens are fp32: T / 16384 p <= 1 a lane past 16384 tokens, T / 4096 past 256 experts.
 // Partial sums in global atomics would be one launch fewer and another result with
-// each run.
+// each run.  256 tokens of 128 experts take 9.2 us in one launch and 7.7 in two, whose
+// second costs the host 4; 512 tokens 14.8 against 7.6.
+//
+// Bound by launches up to some 16384 x 128 (9.8 us forward, 6.7 backward), by memory from
+// 65536 x 256 on: 65536 x 512 (134 MB) 33.9 forward, 4 TB/s read, and 48.5 backward, 5.5 TB/s
+// read and written.
 #include <type_traits>
 
 #include "moe_args.h"
@@ -27,8 +34,11 @@ namespace {
 
 constexpr int kBalThreads = 1024;  // forward: 16 waves join their sums in LDS
 constexpr int kBalBwdThreads = 256;
-constexpr int kBalMaxBlocks = 256;
-constexpr int kBalOneBlock = 256;
+constexpr int kBalMaxBlocks = 256;     // forward: one a CU
+// Backward: the next token's values on their way over several tokens a group (65536 x 128: 15.5 us,
+// 21.4 with 4096 blocks and a token or two each).
+constexpr int kBalBwdBlocks = 1024;
+constexpr int kBalOneBlock = 256;      // tokens
 constexpr int kMaxExperts = 1024;
 
 struct BalScratch {
@@ -345,19 +355,20 @@ __global__ void __launch_bounds__(kBalBwdThreads) balance_bwd_kernel(
   __shared__ __attribute__((aligned(16))) float s_g[ROUTER ? GROUPS : 1][ROUTER ? COLS : 4];
   const int tid = threadIdx.x, l = tid & (LPT - 1), g = tid / LPT;
   const int64_t step = int64_t(gridDim.x) * GROUPS, first = int64_t(blockIdx.x) * GROUPS + g;
-  float p[VPL];
-  bool keep = false;
-  int id = -1;
-  float w = 0.f, dw = 0.f;
-  // a token's logits and slot l of its routing
+  // a token's logits and slot l of its routing, a token ahead
+  struct Token {
+    float z[VPL], w = 0.f, dw = 0.f;
+    int id = -1;
+    bool keep = false;
+  } next;
   auto fetch = [&](int64_t t) __attribute__((always_inline)) {
     if (t >= T) return;
-    keep = valid == nullptr || valid[t];
-    if (keep) load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, p);
+    next.keep = valid == nullptr || valid[t];
+    if (next.keep) load_row<LPT, VPL, VEC>(logits + size_t(t) * E, E, l, next.z);
     if (ROUTER && l < K) {
-      id = topk_idx[size_t(t) * K + l];
-      w = topk_w[size_t(t) * K + l];
-      dw = dtopk_w[size_t(t) * K + l];
+      next.id = topk_idx[size_t(t) * K + l];
+      next.w = topk_w[size_t(t) * K + l];
+      next.dw = dtopk_w[size_t(t) * K + l];
     }
   };
   fetch(first);
@@ -375,7 +386,13 @@ __global__ void __launch_bounds__(kBalBwdThreads) balance_bwd_kernel(
     for (int i = 0; i < VPL; ++i) s_g[g][expert_of<LPT>(l, i)] = 0.f;
   }
   for (int64_t t = first; t < T; t += step) {
-    if (t != first) fetch(t);
+    float p[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = next.z[i];
+    const float w = next.w, dw = next.dw;
+    const int id = next.id;
+    const bool keep = next.keep;
+    fetch(t + step);
     if (keep) {
       const float lse = softmax_row<LPT>(p, E, l);
       float s = 0.f;
@@ -527,7 +544,7 @@ int moe_balance_bwd(const moe_desc* d, const float* logits, const uint8_t* valid
     constexpr int LPT = decltype(lpt)::value, VPL = decltype(vpl)::value;
     constexpr bool VEC = decltype(v)::value;
     const long long want = ceil_div(d->T, kBalBwdThreads / LPT);
-    const unsigned grid = unsigned(want < 4096 ? want : 4096);
+    const unsigned grid = unsigned(want < kBalBwdBlocks ? want : kBalBwdBlocks);
     if (router)
       balance_bwd_kernel<LPT, VPL, VEC, true><<<grid, kBalBwdThreads, 0, s>>>(
           logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, d->T, d->E, d->K, dlogits);

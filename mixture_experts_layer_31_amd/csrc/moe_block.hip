@@ -289,10 +289,10 @@ __global__ void __launch_bounds__(256) block_quant_rows_kernel(QuantArgs p) {
 
 template <class T>
 void launch_quant_rows(const QuantArgs& a, hipStream_t s) {
-  // as many rows a thread as still leave a few workgroups a CU
+  // two rows a thread where there are many (bf16, one against two: 256 x 4096 2.58 us, 2.71; 2048 x 4096
+  // 6.43, 6.48; 4096 x 4096 12.1, 11.7; 16384 x 4096 37.2, 33.5 = 6 TB/s read and written; eight: 36.9)
   const long long slabs = ceil_div(a.rows, 16) * a.ctiles;
-  if (slabs >= 16384) block_quant_rows_kernel<T, 8><<<unsigned(ceil_div(a.rows, 128) * a.ctiles), 256, 0, s>>>(a);
-  else if (slabs >= 4096) block_quant_rows_kernel<T, 2><<<unsigned(ceil_div(a.rows, 32) * a.ctiles), 256, 0, s>>>(a);
+  if (slabs >= 8192) block_quant_rows_kernel<T, 2><<<unsigned(ceil_div(a.rows, 32) * a.ctiles), 256, 0, s>>>(a);
   else block_quant_rows_kernel<T, 1><<<unsigned(slabs), 256, 0, s>>>(a);
 }
 
@@ -1210,7 +1210,8 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 //   64 x 64, two groups   3   + 0.28 steps  (256 x 4096 x 4096 11.1, 12.6 with one group)
 // The sizes' best is the least of these.  fp32 results have no 256 x 256 kernel and another 128 x 128
 // one (2.5 + 0.8 against 2 + 0.5 of the 64 x 64 tiles, all of its steps 1.6 times as long).  Where a few
-// rows past a multiple of 256 cost a further round, they go to a launch of 64 x 64 tiles.
+// rows past a multiple of 256 cost a further round, they go to a launch of 64 x 64 tiles (8197 x 2048 x
+// 1536: 34.3, in one launch 48.6; 4128 x 4096 x 2048: 40.3, 57.2).
 // With too few tiles for the chip the contraction is cut into parts, whose sums take a second launch:
 // 4 us and their bytes at 3 TB/s, written and read (256 x 256 x 16384 in 16 parts of 8 runs 12.0, whole 31.6;
 // 512 x 512 x 8192 in 4 of 16 13.0, whole 18.2).
