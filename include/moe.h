@@ -45,7 +45,8 @@
  *     moe_profile_collect.
  *   - Inputs are never modified.  Calls on distinct scratch buffers are
  *     independent; the library keeps no state except the opt-in profiler.
- *   - Buffers must be 16-byte aligned and must not overlap.
+ *   - Buffers must be 16-byte aligned and must not overlap, unless a call says
+ *     otherwise.
  *
  * Errors: every call returns MOE_OK (0) or a negative MOE_E* code found on the
  * host before anything is enqueued.  Errors found by the GPU (an expert id out
@@ -443,8 +444,8 @@ typedef struct moe_block_mm_desc {
  * moe_block_mm_scratch_bytes(m) (MOE_ESCRATCH; 0 bytes: it may be NULL), used only
  * during the call (the codes of values; the sums of a long contraction's parts).  MOE_EINVAL for null pointers, negative sizes, bad types or
  * flags and strides that are too small; MOE_EUNSUPPORTED for strides of 2^22 or more
- * (lda, ldb), scales past 2^31 bytes, values past moe_block_quant's limits (the
- * scratch size is 0 for all of these) and more tiles than a launch holds (2^23).
+ * (lda, ldb), scales past 2^31 bytes, values past moe_block_quant's limits and
+ * ceil(M/64) ceil(N/64) >= 2^23; the scratch size is 0 for all of these.
  * The order of the sums depends on the sizes alone: the same inputs give
  * the same bits.  Asynchronous on `stream`; allocates nothing. */
 size_t moe_block_mm_scratch_bytes(const moe_block_mm_desc* m);

@@ -697,7 +697,6 @@ int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
   p.ntm = int(ceil_div(p.M, TL::BM));
   p.ntn = int(ceil_div(p.N, TL::BN));
   const long long tiles = (long long)p.ntm * p.ntn * (p.part ? ceil_div(p.ksteps, p.per) : 1);
-  if (!launchable(tiles, TL::THREADS)) return MOE_EUNSUPPORTED;
   const unsigned grid = unsigned(tiles);
   prof_begin("block_mm_large", s);
   if (b_tile) block_mm_large_kernel<TL, true><<<grid, TL::THREADS, 0, s>>>(p);
@@ -965,7 +964,6 @@ int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
   p.ntm = int(ceil_div(p.M, TL::BM));
   p.ntn = int(ceil_div(p.N, TL::BN));
   const long long tiles = (long long)p.ntm * p.ntn * (p.part ? ceil_div(p.ksteps, p.per) : 1);
-  if (!launchable(tiles, TL::THREADS)) return MOE_EUNSUPPORTED;
   const unsigned grid = unsigned(tiles);
   prof_begin("block_mm_mid", s);
   if (b_tile) {
@@ -1340,6 +1338,7 @@ int check_mm_desc(const moe_block_mm_desc* m) {
   const long long steps = ceil_div(m->K, 128), wide = m->M > m->N ? m->M : m->N;
   if (steps * wide * 4 >= (1LL << 31) || m->ldc >= (1LL << 40)) return MOE_EUNSUPPORTED;
   if (quantised_by_call(*m) && !launchable(ceil_div(m->M, 16) * steps, 256)) return MOE_EUNSUPPORTED;
+  if (!launchable(ceil_div(m->M, 64) * ceil_div(m->N, 64), 512)) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
