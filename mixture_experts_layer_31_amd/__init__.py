@@ -178,13 +178,27 @@ def moe_router_bwd(desc, topk_idx, topk_w, dtopk_w, dlogits, stream=None) -> int
                                 _p(dlogits), _stream(stream))
 
 
-def _addresses(*tensors):
-    """The device addresses of (tensor, element types, count) for contiguous GPU tensors of one of those
-    types with that many elements at least (count None: _rows_fit has seen to it); None where one does not
-    fit, all of them on the current device, whose stream the call takes.  None and raw addresses go through:
-    they are the C side's to check."""
+_look = None
+
+
+def _lookups() -> tuple:
+    """What the operators beside the layer look up in torch, once: (functions for the current GPU and its
+    stream's raw handle, fp32, int32, masks, codes, values by moe_type)"""
+    global _look
     import torch
-    dev, out = torch.cuda.current_device(), []
+    torch.cuda.current_device()  # raises where there is no GPU
+    f32 = (torch.float32,)
+    _look = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, f32, (torch.int32,),
+             (torch.uint8, torch.bool), (torch.uint8, torch.float8_e4m3fn),
+             {MOE_TYPE_F32: f32, MOE_TYPE_BF16: (torch.bfloat16,)})
+    return _look
+
+
+def _addresses(dev: int, *tensors):
+    """The device addresses of (tensor, element types, count) for contiguous tensors on GPU `dev`, the current
+    one, of one of those types with that many elements at least (count None: _rows_fit has seen to it); None
+    where one does not fit.  None and raw addresses go through: they are the C side's to check."""
+    out = []
     for t, types, n in tensors:
         if t is None or t.__class__ is int:
             out.append(t)
@@ -199,30 +213,16 @@ def _rows_fit(t, rows: int, cols: int, ld: int) -> bool:
     """Whether a tensor has that many rows and columns, ld elements between its rows."""
     if t is None or t.__class__ is int:
         return True
-    return t.dim() == 2 and t.size(0) >= rows and t.size(1) >= cols and \
-        (rows <= 1 or t.stride(0) == ld) and (cols <= 1 or t.stride(1) == 1)
+    size, stride = t.shape, t.stride()
+    return len(size) == 2 and size[0] >= rows and size[1] >= cols and \
+        (rows <= 1 or stride[0] == ld) and (cols <= 1 or stride[1] == 1)
 
 
-def _scratch(t) -> tuple:
-    """(address, bytes) of a scratch tensor on the current GPU; (None, 0) where it does not fit or is None."""
-    import torch
-    if t is None or t.get_device() != torch.cuda.current_device() or not t.is_contiguous():
+def _scratch(t, dev: int) -> tuple:
+    """(address, bytes) of a scratch tensor on GPU `dev`; (None, 0) where it does not fit or is None."""
+    if t is None or t.get_device() != dev or not t.is_contiguous():
         return None, 0
-    return t.data_ptr(), _nbytes(t)
-
-
-def _types() -> tuple:
-    """(fp32, int32, masks, codes, values by moe_type)"""
-    global _type_sets
-    if _type_sets is None:
-        import torch
-        _type_sets = ((torch.float32,), (torch.int32,), (torch.uint8, torch.bool),
-                      (torch.uint8, torch.float8_e4m3fn),
-                      {MOE_TYPE_F32: (torch.float32,), MOE_TYPE_BF16: (torch.bfloat16,)})
-    return _type_sets
-
-
-_type_sets = None
+    return t.data_ptr(), t.nbytes
 
 
 def moe_balance_scratch_bytes(desc: moe_desc) -> int:
@@ -231,23 +231,26 @@ def moe_balance_scratch_bytes(desc: moe_desc) -> int:
 
 def moe_balance_fwd(desc, logits, topk_idx, valid, counts, mean_p, losses, scratch, stream=None) -> int:
     T, E, K = desc.T, desc.E, desc.K
-    f32, i32, mask, _, _ = _types()
-    at = _addresses((logits, f32, T * E), (topk_idx, i32, T * K), (valid, mask, T), (counts, i32, E + 1),
+    device, raw, f32, i32, mask, _, _ = _look or _lookups()
+    dev = device()
+    at = _addresses(dev, (logits, f32, T * E), (topk_idx, i32, T * K), (valid, mask, T), (counts, i32, E + 1),
                     (mean_p, f32, E), (losses, f32, 2))
     if at is None:
         return MOE_EINVAL
-    return lib().moe_balance_fwd(ctypes.byref(desc), *at, *_scratch(scratch), _stream(stream))
+    return lib().moe_balance_fwd(ctypes.byref(desc), *at, *_scratch(scratch, dev),
+                                 raw(dev) if stream is None else _stream(stream))
 
 
 def moe_balance_bwd(desc, logits, valid, counts, dlosses, topk_idx, topk_w, dtopk_w, dlogits,
                     stream=None) -> int:
     T, E, K = desc.T, desc.E, desc.K
-    f32, i32, mask, _, _ = _types()
-    at = _addresses((logits, f32, T * E), (valid, mask, T), (counts, i32, E + 1), (dlosses, f32, 2),
+    device, raw, f32, i32, mask, _, _ = _look or _lookups()
+    dev = device()
+    at = _addresses(dev, (logits, f32, T * E), (valid, mask, T), (counts, i32, E + 1), (dlosses, f32, 2),
                     (topk_idx, i32, T * K), (topk_w, f32, T * K), (dtopk_w, f32, T * K), (dlogits, f32, T * E))
     if at is None:
         return MOE_EINVAL
-    return lib().moe_balance_bwd(ctypes.byref(desc), *at, _stream(stream))
+    return lib().moe_balance_bwd(ctypes.byref(desc), *at, raw(dev) if stream is None else _stream(stream))
 
 
 def _code_ld(n: int) -> int:
@@ -266,16 +269,17 @@ def moe_block_quant(desc, x, codes, scales, codes_t=None, scales_t=None, stream=
     R, C = desc.rows, desc.cols
     rb, cb = (R + 127) // 128, (C + 127) // 128
     block = desc.scale == MOE_SCALE_BLOCK
-    f32, _, _, code, io = _types()
+    device, raw, f32, _, _, code, io = _look or _lookups()
+    dev = device()
     if not (_rows_fit(x, R, C, desc.ld_in) and _rows_fit(codes, R, _code_ld(C), desc.ld_codes)
             and _rows_fit(codes_t, C, _code_ld(R), desc.ld_codes_t)):
         return MOE_EINVAL
-    at = _addresses((x, io.get(desc.in_type, ()), None), (codes, code, None),
+    at = _addresses(dev, (x, io.get(desc.in_type, ()), None), (codes, code, None),
                     (scales, f32, cb * (rb if block else R)), (codes_t, code, None),
                     (scales_t, f32, rb * (cb if block else C)))
     if at is None:
         return MOE_EINVAL
-    return lib().moe_block_quant(ctypes.byref(desc), *at, _stream(stream))
+    return lib().moe_block_quant(ctypes.byref(desc), *at, raw(dev) if stream is None else _stream(stream))
 
 
 def make_block_mm_desc(M, N, K, a_type=MOE_TYPE_E4M3, b_scale=MOE_SCALE_BLOCK, c_type=MOE_TYPE_BF16,
@@ -294,17 +298,20 @@ def moe_block_mm_scratch_bytes(desc: moe_block_mm_desc) -> int:
 def moe_block_mm(desc, a, a_scales, b, b_scales, c, scratch=None, stream=None) -> int:
     M, N, K = desc.M, desc.N, desc.K
     steps, own = (K + 127) // 128, desc.a_type == MOE_TYPE_E4M3
-    f32, _, _, code, io = _types()
+    device, raw, f32, _, _, code, io = _look or _lookups()
+    dev = device()
     ldk = _code_ld(K)
     if not (_rows_fit(a, M, ldk if own else K, desc.lda) and _rows_fit(b, N, ldk, desc.ldb)
             and _rows_fit(c, M, N, desc.ldc)):
         return MOE_EINVAL
-    at = _addresses((a, code if own else io.get(desc.a_type, ()), None), (a_scales, f32, steps * M), (b, code, None),
+    at = _addresses(dev, (a, code if own else io.get(desc.a_type, ()), None), (a_scales, f32, steps * M),
+                    (b, code, None),
                     (b_scales, f32, steps * (N if desc.b_scale == MOE_SCALE_TILE else (N + 127) // 128)),
                     (c, io.get(desc.c_type, ()), None))
     if at is None:
         return MOE_EINVAL
-    return lib().moe_block_mm(ctypes.byref(desc), *at, *_scratch(scratch), _stream(stream))
+    return lib().moe_block_mm(ctypes.byref(desc), *at, *_scratch(scratch, dev),
+                              raw(dev) if stream is None else _stream(stream))
 
 
 def make_grad_list(src, dst=None):
@@ -328,27 +335,27 @@ def make_grad_list(src, dst=None):
     return grads
 
 
-def _grads_elsewhere(grads) -> bool:
-    import torch
-    return getattr(grads, "device", None) not in (None, torch.cuda.current_device())
-
-
 def moe_grad_scratch_bytes(count: int) -> int:
     return lib().moe_grad_scratch_bytes(count)
 
 
 def moe_grad_norm(grads, norm, scratch, stream=None) -> int:
-    at = _addresses((norm, _types()[0], 1))
-    if at is None or _grads_elsewhere(grads):
+    device, raw, f32, *_ = _look or _lookups()
+    dev = device()
+    at = _addresses(dev, (norm, f32, 1))
+    if at is None or getattr(grads, "device", dev) not in (dev, None):
         return MOE_EINVAL
-    return lib().moe_grad_norm(grads, len(grads), *at, *_scratch(scratch), _stream(stream))
+    return lib().moe_grad_norm(grads, len(grads), *at, *_scratch(scratch, dev),
+                               raw(dev) if stream is None else _stream(stream))
 
 
 def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> int:
-    at = _addresses((norm, _types()[0], 1))
-    if at is None or _grads_elsewhere(grads):
+    device, raw, f32, *_ = _look or _lookups()
+    dev = device()
+    at = _addresses(dev, (norm, f32, 1))
+    if at is None or getattr(grads, "device", dev) not in (dev, None):
         return MOE_EINVAL
-    return lib().moe_grad_clip(grads, len(grads), *at, max_norm, _stream(stream))
+    return lib().moe_grad_clip(grads, len(grads), *at, max_norm, raw(dev) if stream is None else _stream(stream))
 
 
 def moe_routing_view(desc, scratch) -> tuple:
