@@ -380,8 +380,8 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
 }
 
 // Large products with bf16 results: 256 x 256 tiles of eight waves, 128 x 64 each, or, where those
-// are too few, 128 x 128 tiles of two groups of four waves, 64 x 64 each, that share the runs and
-// are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
+// are too few, 128 x 128 (96 x 128) tiles of two groups of four waves, 64 x 64 (48 x 64) each, that
+// share the runs and are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
 template <int MB_, int WGM_, int WGN_, int KG_>
 struct LargeTile {
   static constexpr int MB = MB_, NB = 4, WGM = WGM_, WGN = WGN_, KG = KG_;
@@ -391,7 +391,8 @@ struct LargeTile {
 template <class TL, bool B_TILE>
 __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p) {
   constexpr int BM = TL::BM, BN = TL::BN, WAVES = TL::WAVES, MB = TL::MB, NB = TL::NB, KG = TL::KG;
-  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES + (BM + BN) * 4, RING = 2 * STAGE;
+  constexpr int QA = (BM + 63) / 64;  // 64 scales a wave: A's, then B's
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES + (64 * QA + BN) * 4, RING = 2 * STAGE;
   __shared__ __attribute__((aligned(1024))) char lds[KG * RING];
   int l = xcd_remap(blockIdx.x, gridDim.x);
   if constexpr (KG > 1) l = take_part<B_TILE>(p, l);
@@ -413,7 +414,6 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
           [&](int r) { return r < nrows ? int(r * p.ldb) : -1; }, wave, lane);
   const uint32_t base = lds_addr(smem);
   const int nblocks = (p.N + 127) / 128;
-  constexpr int QA = BM / 64;  // 64 scales a wave: A's, then B's
   static_assert(QA + BN / 64 == WAVES, "a load of scales a wave");
   const bool sis_a = wave < QA;
   const i32x4 rs = sis_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     return i32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   };
   const char* sap = smem + A_BYTES + B_BYTES + (wm * 16 * MB + l16) * 4;
-  const char* sbp = smem + A_BYTES + B_BYTES + BM * 4 + (wn * 16 * NB + (B_TILE ? 4 * g : 0)) * 4;
+  const char* sbp = smem + A_BYTES + B_BYTES + QA * 256 + (wn * 16 * NB + (B_TILE ? 4 * g : 0)) * 4;
   auto frag_a = [&](int st, int i) __attribute__((always_inline)) { return frag(st + (wm * MB + i) * 2048); };
   auto frag_b = [&](int st, int j) __attribute__((always_inline)) {
     return frag(st + A_BYTES + (wn * NB + j) * 2048);
@@ -1204,6 +1204,7 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 // 128, or two of 64 x 64, a CU), in us a round of workgroups with `steps` runs:
 //   256 x 256             5   + 1.72 steps  (4096 x 4096 x 4096 61.7, 16384 x 4096 x 4096 4 x 68)
 //   128 x 128             5.7 + 0.53 steps  (2048 x 2048 x 2048 14.2, 2048 x 2048 x 8192 39.6)
+//   96 x 128              4.9 + 0.52 steps  (1536 x 2048 x 2048 12.6 in 256 tiles, 14.2 in 192 of 128 x 128)
 //   64 x 64, two a CU     2   + 0.5  steps  (2048 x 2048 x 2048 19.6 in two rounds)
 //   64 x 64, two groups   3   + 0.28 steps  (256 x 4096 x 4096 11.1, 12.6 with one group)
 // The sizes' best is the least of these.  fp32 results have no 256 x 256 kernel and another 128 x 128
@@ -1213,7 +1214,7 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 // With too few tiles for the chip the contraction is cut into parts, whose sums take a second launch:
 // 4 us and their bytes at 3 TB/s, written and read (256 x 256 x 16384 in 16 parts of 8 runs 12.0, whole 31.6;
 // 512 x 512 x 8192 in 4 of 16 13.0, whole 18.2).
-enum MmKind { MM_LARGE, MM_128, MM_64, MM_64X2 };
+enum MmKind { MM_LARGE, MM_128, MM_96, MM_64, MM_64X2 };
 struct MmPlan {
   MmKind kind;
   double us;
@@ -1224,25 +1225,25 @@ constexpr double kPartBytes = 64 << 20;  // most of the parts' sums
 
 MmPlan mm_plan(long long M, long long N, int steps, bool f32, bool whole = false) {
   constexpr int kCus = 256;
-  const auto tiles = [&](long long m, int b) { return ceil_div(m, b) * ceil_div(N, b); };
-  const auto large = [&](long long m) { return ceil_div(tiles(m, 256), kCus) * (5 + 1.72 * steps); };
+  const auto tiles = [&](long long m, int bm, int bn) { return ceil_div(m, bm) * ceil_div(N, bn); };
+  const auto large = [&](long long m) { return ceil_div(tiles(m, 256, 256), kCus) * (5 + 1.72 * steps); };
   MmPlan best{MM_64, 1e30, 0, 1, steps};
-  const auto consider = [&](MmKind kind, long long m, int b, int slots, double fix, double each) {
-    const long long t = tiles(m, b);
+  const auto consider = [&](MmKind kind, int bm, int bn, int slots, double fix, double each) {
+    const long long t = tiles(M, bm, bn);
     for (int parts = 1; parts <= 64; parts = parts < 4 ? parts + 1 : parts < 16 ? parts + 2 : parts * 2) {
       const int per = int(ceil_div(steps, parts));
-      const double bytes = 4. * parts * double(m) * double(N);
+      const double bytes = 4. * parts * double(M) * double(N);
       if (parts > 1 && (whole || t * parts > 2 * slots || per < 4 || bytes > kPartBytes)) break;
       const double us = ceil_div(t * parts, slots) * (fix + each * per) + (parts > 1 ? 4 + 2 * bytes / 3e6 : 0);
       if (us < best.us) best = {kind, us, 0, int(ceil_div(steps, per)), per};
     }
   };
   const double slow = f32 ? 1.6 : 1;
-  consider(MM_64X2, M, 64, kCus, 3, 0.28 * slow);
-  consider(MM_64, M, 64, 2 * kCus, 2, 0.5 * slow);
-  if (f32) consider(MM_128, M, 128, kCus, 2.5, 0.8 * slow);
-  else consider(MM_128, M, 128, kCus, 5.7, 0.53);
+  consider(MM_64X2, 64, 64, kCus, 3, 0.28 * slow);
+  consider(MM_64, 64, 64, 2 * kCus, 2, 0.5 * slow);
+  consider(MM_128, 128, 128, kCus, f32 ? 2.5 : 5.7, f32 ? 0.8 * slow : 0.53);
   if (f32) return best;
+  consider(MM_96, 96, 128, kCus, 4.9, 0.52);
   if (large(M) < best.us) best = {MM_LARGE, large(M), 0, 1, steps};
   const int rest = int(M % 256);
   if (M > 256 && rest > 0 && rest <= 64) {
@@ -1269,6 +1270,7 @@ int launch_mm(const MmArgs& a, const MmPlan& plan, bool b_tile, bool f32, float*
       case MM_128:
         if (!f32) return launch_mm_large<LargeTile<4, 2, 2, 2>>(p, b_tile, s);
         return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
+      case MM_96: return launch_mm_large<LargeTile<3, 2, 2, 2>>(p, b_tile, s);
       case MM_LARGE: break;
     }
     return launch_mm_large<LargeTile<8, 2, 4, 1>>(p, b_tile, s);

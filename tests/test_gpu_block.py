@@ -255,6 +255,13 @@ def test_long_contraction_in_parts(M, N, K, ct):
             assert np.array_equal(one, _check_mm(M, N, K, b_scale, ct))
 
 
+@pytest.mark.parametrize("M,N,K", [(1500, 1900, 300), (1537, 1793, 1100), (1440, 2048, 256), (1441, 2047, 128)])
+def test_product_of_tiles_of_96_rows(M, N, K):
+    """Between a round of 128 x 128 tiles and a full chip."""
+    for b_scale in (TILE, BLOCK):
+        _check_mm(M, N, K, b_scale, BF, ldc=N + 5)
+
+
 def test_empty_contraction():
     for ct in (BF, F32):
         c = torch.full((5, 9), 3.0, dtype=DT[ct], device="cuda")
