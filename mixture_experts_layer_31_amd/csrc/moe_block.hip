@@ -100,7 +100,9 @@ __device__ __forceinline__ float amax8(const float (&v)[8]) {
 // outputs: 8.5 us against 10.8 us with the values through LDS and coded twice).  With
 // tiles the values do: a thread then holds half a column (64 values, the other half is
 // in lane ^ 32), and its codes go back through LDS so that eight lanes store a row's
-// 128 bytes.
+// 128 bytes.  16384 x 4096 bf16 in tiles: the transpose alone 36 us, 5.6 TB/s; both orientations 62 us,
+// 4.3 TB/s, bound by two exact quotients a value.  (Column pairs in 32-bit LDS reads free of bank
+// conflicts took the same time.)
 template <class T, bool BLOCK>
 __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
   constexpr int LD = 128 + 16 / sizeof(T);  // values: rows apart in banks, 16-byte aligned
@@ -382,6 +384,10 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
 // Large products with bf16 results: 256 x 256 tiles of eight waves, 128 x 64 each, or, where those
 // are too few, 128 x 128 (96 x 128) tiles of two groups of four waves, 64 x 64 (48 x 64) each, that
 // share the runs and are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
+// 16384 x 4096 x 4096: 239 us, 2.3 PFLOP/s (a library's unscaled product 188 us).  Of a tile's 60 us five are
+// its first loads and its epilogue; in a step the promotion's vector instructions share the wave's issue
+// slots with the matrix instructions, at the clock that the power allows.  The 256 x 256 kernel spills some 200
+// bytes a lane, outside its main loop.  The 128 x 128 tiles are bound by the L2's 12 to 13 TB/s into LDS.
 template <int MB_, int WGM_, int WGN_, int KG_>
 struct LargeTile {
   static constexpr int MB = MB_, NB = 4, WGM = WGM_, WGN = WGN_, KG = KG_;
@@ -709,7 +715,7 @@ int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
 // waves in 16 x 16 blocks, KG such groups a workgroup that share the runs of the contraction and
 // are joined at the end.  Where tiles or steps are few, a step's latency is what it costs: a
 // ring of four stages is filled four steps ahead, a step's fragments are read one step before
-// their products, and a product's sums are promoted one step behind it.
+// their products, and a product's sums are promoted one step behind it (256 x 4096 x 4096 bf16 12.7 us, fp32 17.7).
 template <int BM_, int BN_, int WGM_, int WGN_, int KG_>
 struct MidTile {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, KG = KG_;
@@ -984,7 +990,8 @@ int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
 // fragment holds row l & 15 and bytes 32 (l >> 4) .. + 31 of a run, for A and B alike; with B as
 // the first operand a lane's results are row l & 15 of C and columns 4 (l >> 4) .. + 3.
 // Every workgroup of a row of tiles quantises its A again, which costs less than a second launch
-// up to the size in use_direct.
+// up to the size in use_direct.  1 x 4096 x 2048 from bf16: 4.6 us in a graph, 8.4 MB of codes, of it 3 a
+// launch's; 33 x 1000 x 1363 from fp32: 7.6, of it 2 the quotients.
 enum AKind { A_CODES = 0, A_BF16 = 1, A_F32 = 2 };
 constexpr int kDirectWaves = 16, kDirectK = 4096;
 
