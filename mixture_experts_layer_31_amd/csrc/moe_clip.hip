@@ -35,6 +35,9 @@ constexpr int kMaxList = 96;          // entries a launch: 96 * 28 bytes of argu
 constexpr int kClipThreads = 256;
 constexpr int kChunkBytes = 16384;    // four 16-byte vectors a thread
 constexpr int kMaxBlocks = 2048;      // workgroups a launch
+// Chunks up to which one workgroup takes the norm in one launch: 4 chunks 4.9 us eager and 3.4 in a graph, 8
+// 5.7 and 5.2, 16 9.2 and 8.7, against 9.1 and 4.5 in two launches.
+constexpr uint32_t kOneBlock = 8;
 constexpr uint32_t kStreamChunks = 144 * 64;  // 144 MB
 
 struct GradList {
@@ -96,13 +99,13 @@ template <> struct Vec<uint16_t> {
 template <class T>
 struct Chunk {
   const T* src;
-  int64_t n, v0;
+  int64_t n, v0;  // v0: this thread's first vector
   int off;
   __device__ __forceinline__ Chunk(const void* s, int64_t count, uint32_t c)
-      : src(static_cast<const T*>(s)), n(count), v0(int64_t(c) * (kChunkBytes / 16)),
+      : src(static_cast<const T*>(s)), n(count), v0(int64_t(c) * (kChunkBytes / 16) + threadIdx.x % kClipThreads),
         off(int((reinterpret_cast<uintptr_t>(s) & 15) / sizeof(T))) {}
   __device__ __forceinline__ int64_t elem(int k) const {  // first element of this thread's k-th vector
-    return (v0 + threadIdx.x + k * kClipThreads) * Vec<T>::N - off;
+    return (v0 + k * kClipThreads) * Vec<T>::N - off;
   }
   __device__ __forceinline__ bool whole(int64_t e) const { return e >= 0 && e + Vec<T>::N <= n; }
 };
@@ -164,6 +167,30 @@ __global__ void __launch_bounds__(kClipThreads) grad_squares_kernel(GradList L,
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) out[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// A short list's norm by one workgroup, four chunks at a time.
+__global__ void __launch_bounds__(1024) grad_norm_one_kernel(GradList L, float* __restrict__ norm) {
+  const uint32_t total = L.first[L.count];
+  const uint32_t c0 = threadIdx.x / kClipThreads;
+  double s = 0.;
+  int i = 0;
+  for (uint32_t c = c0; c < total; c += 1024 / kClipThreads) {
+    while (c >= L.first[i + 1]) ++i;
+    const uint32_t k = c - L.first[i];
+    s += (L.f32[i >> 5] >> (i & 31)) & 1 ? chunk_squares<false, float>(L.src[i], L.n[i], k)
+                                         : chunk_squares<false, uint16_t>(L.src[i], L.n[i], k);
+  }
+  __shared__ double red[16];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.;
+    for (int w = 0; w < 16; ++w) t += red[w];
+    norm[0] = float(sqrt(t));
+  }
 }
 
 __global__ void __launch_bounds__(1024) grad_norm_kernel(const double* __restrict__ in, int64_t n,
@@ -344,8 +371,16 @@ int moe_grad_norm(const moe_grad* g, int32_t count, float* norm, void* scratch,
   hipStream_t s = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(scratch);
   int64_t used = 0;
+  bool done = false;  // one workgroup took it all
   rc = for_lists(g, count, [&](const GradList& L) {
     const unsigned grid = grid_of(L);
+    if (count <= kMaxList && L.first[L.count] <= kOneBlock) {
+      done = true;
+      prof_begin("grad_norm", s);
+      grad_norm_one_kernel<<<1, 1024, 0, s>>>(L, norm);
+      prof_end(s);
+      return launched();
+    }
     prof_begin("grad_squares", s);
     if (L.first[L.count] > kStreamChunks) grad_squares_kernel<true><<<grid, kClipThreads, 0, s>>>(L, part + used);
     else grad_squares_kernel<false><<<grid, kClipThreads, 0, s>>>(L, part + used);
@@ -353,7 +388,7 @@ int moe_grad_norm(const moe_grad* g, int32_t count, float* norm, void* scratch,
     used += grid;
     return launched();
   });
-  if (rc) return rc;
+  if (rc || done) return rc;
   prof_begin("grad_norm", s);
   grad_norm_kernel<<<1, 1024, 0, s>>>(part, used, norm);
   prof_end(s);

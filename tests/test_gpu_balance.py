@@ -119,6 +119,13 @@ def test_shapes(T, E, K):
     _check(z, idx, rng.random(T) < 0.6, name="masked", off=1)
 
 
+@pytest.mark.parametrize("T,E,K", [(33000, 40, 3), (17001, 100, 4), (16500, 200, 8), (9000, 300, 5), (4200, 700, 20)])
+def test_several_tokens_a_group(T, E, K):
+    z, idx, router, rng = _inputs(T + E, T, E, K)
+    _check(z, idx, rng.random(T) < 0.7, router=router, name="masked")
+    _check(z, idx, None, router=router, name="plain", off=1)
+
+
 def test_every_slot_of_many_experts():
     z, idx, _, _ = _inputs(5, 20, 200, 200)
     _check(z, idx, None, name="K=E")  # the loss's gradient has no limit of 64 slots
