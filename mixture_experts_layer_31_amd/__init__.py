@@ -5,6 +5,9 @@ libmoe_mi355x.so built in-tree by ``mixture_experts_layer_31_amd.build``.  The
 functions below carry the C names; tensors are torch tensors on the GPU (or
 None for optional pointers) and `stream` defaults to torch's current stream.
 Loading fails loudly when the library has not been built: there is no fallback.
+The calls of the operators beside the layer (moe_balance_*, moe_block_*, moe_grad_*)
+also look at their tensors: one of another type, device or stride than the call takes,
+or with too few elements, is MOE_EINVAL.
 """
 from __future__ import annotations
 

@@ -231,3 +231,35 @@ def test_binding_refuses_tensors_that_do_not_fit():
     for bad in (z.cpu(), z.double(), z[:3], torch.zeros(8, 4, device="cuda").t()):
         assert moe.moe_balance_fwd(d, bad, idx, None, *out) == moe.MOE_EINVAL
     assert moe.moe_balance_fwd(d, z, idx.long(), None, *out) == moe.MOE_EINVAL
+
+
+def test_offsets_past_2_31_elements():
+    """The rows of a small batch over and over: what the last tokens get, 2^33 bytes into the logits."""
+    P, E, K, times = 4099, 512, 2, 1024
+    z, idx, _, _ = _inputs(11, P, E, K)
+    T = P * times
+    assert T * E > 2 ** 31
+    print(f"[case] balance large T={T} E={E}", flush=True)
+    d = moe.make_desc(T, 0, 0, E, K)
+    zt, it = _dev(z).repeat(times, 1), _dev(idx.astype(np.int32)).repeat(times, 1)
+    counts = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    mp, losses, dz = torch.empty(E, device="cuda"), torch.empty(2, device="cuda"), torch.empty(T, E, device="cuda")
+    scratch = torch.empty(moe.moe_balance_scratch_bytes(d), dtype=torch.uint8, device="cuda")
+    dl = np.float32([1.0, 0.25])
+    moe.check(moe.moe_balance_fwd(d, zt, it, None, counts, mp, losses, scratch))
+    moe.check(moe.moe_balance_bwd(d, zt, None, counts, _dev(dl), None, None, None, dz))
+    torch.cuda.synchronize()
+    f = bo.forward(z, idx, None)
+    assert np.array_equal(counts.cpu().numpy(), f["counts"] * times)
+    zk = z.astype(np.float64)
+    e = ((zk.max(axis=1, keepdims=True) - zk).max() + E / 16 + 77) * U
+    assert np.all(np.abs(mp.cpu().numpy() - f["mean_p"]) <= (e + (T / 64 + 25) * U) * f["mean_p"])
+    ref = bo.backward(z, idx, None, dl.astype(np.float64), f) / times  # each token's share of a longer batch
+    for at in (0, T - P):
+        got = dz[at:at + P].double().cpu().numpy()
+        # |f_j - s| and lse of this batch: at most (f_j + s) and 1 + log 512 in size, as in the bound above
+        share = f["counts"][:E] / (P * K)
+        s = (f["p"] * share).sum(axis=1, keepdims=True)
+        lse = np.abs(f["lse"])[:, None]
+        bound = f["p"] * ((E / T * (share + s) + 0.5 / T * lse) * (2 * e + 12 * U) + 0.5 / T * (e + 4 * U * (2 * lse + 20)))
+        assert np.all(np.abs(got - ref) <= bound + TINY)

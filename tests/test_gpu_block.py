@@ -396,6 +396,48 @@ def test_offsets_past_2_31_bytes():
     assert not c[:, N:N + 64].any()
 
 
+@pytest.mark.parametrize("scale", [TILE, BLOCK])
+def test_quantiser_offsets_past_2_32_bytes(scale):
+    """Rows of x 16 MB apart, and codes 4 MB apart, against the same matrix in compact rows."""
+    R, C, ld_in, ld = 600, 300, 8 << 20, (4 << 20) - 16
+    print(f"[case] quant large scale={scale}", flush=True)
+    x = _x(3, R, C)
+    far = torch.empty(R, ld_in, dtype=torch.bfloat16, device="cuda")
+    far[:, :C] = x.cuda()
+    q, s, qt, st = _quant(x, scale)
+    codes = torch.zeros(R, ld, dtype=torch.uint8, device="cuda")
+    codes_t = torch.zeros(C, ld, dtype=torch.uint8, device="cuda")
+    sc, sct = torch.empty(s.shape, device="cuda"), torch.empty(st.shape, device="cuda")
+    d = moe.make_block_quant_desc(R, C, BF, scale, ld_in=ld_in, ld_codes=ld, ld_codes_t=ld)
+    assert moe.moe_block_quant(d, far, codes, sc, codes_t, sct) == moe.MOE_OK
+    torch.cuda.synchronize()
+    assert np.array_equal(codes[:, :C].cpu().numpy(), q[:, :C]) and np.array_equal(codes_t[:, :R].cpu().numpy(), qt[:, :R])
+    assert np.array_equal(sc.cpu().numpy(), s) and np.array_equal(sct.cpu().numpy(), st)
+    assert not codes[:, 304:320].any() and not codes_t[:, 608:620].any()
+
+
+def test_two_streams_at_once():
+    """Products on two streams, each with scratch of its own."""
+    jobs = []
+    for M, N, K in ((300, 260, 9000), (130, 700, 5000)):
+        x = _x(M, M, K).cuda()
+        b, sb, _, ldb = _codes(2, N, K, BLOCK)
+        d = moe.make_block_mm_desc(M, N, K, a_type=BF, ldb=ldb)
+        scratch = torch.empty(moe.moe_block_mm_scratch_bytes(d), dtype=torch.uint8, device="cuda")
+        jobs.append((d, x, b, sb, torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), scratch, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for d, x, b, sb, c, scratch, side in jobs:
+            with torch.cuda.stream(side):
+                moe.check(moe.moe_block_mm(d, x, None, b, sb, c, scratch))
+    torch.cuda.synchronize()
+    for d, x, b, sb, c, scratch, _ in jobs:
+        got = c.clone()
+        moe.check(moe.moe_block_mm(d, x, None, b, sb, c, scratch))
+        torch.cuda.synchronize()
+        assert torch.equal(got, c)
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     d = moe.make_block_mm_desc(4, 8, 32)
     a, b = (torch.zeros(n, 32, dtype=torch.uint8, device="cuda") for n in (4, 8))

@@ -176,3 +176,44 @@ def test_binding_refuses_what_is_elsewhere():
     assert moe.moe_grad_norm(lst, norm, room.cuda()) == moe.MOE_EINVAL
     assert moe.moe_grad_clip(lst, norm, 1.0) == moe.MOE_EINVAL
     assert moe.moe_grad_clip(moe.make_grad_list([x]), x, 1.0) == moe.MOE_EINVAL  # the norm among the gradients
+
+
+def test_offsets_past_2_31_elements():
+    n = 2 ** 31 + 1003
+    print(f"[case] clip large n={n}", flush=True)
+    x = torch.full((n,), 0.5, dtype=B, device="cuda")
+    x[-5:] = 2.0
+    lst = moe.make_grad_list([x])
+    norm = _norm(lst)
+    ref = np.sqrt((n - 5) * 0.25 + 5 * 4.0)
+    moe.check(moe.moe_grad_clip(lst, norm, float(ref) / 4))
+    torch.cuda.synchronize()
+    assert abs(float(norm) - ref) <= 2.0 ** -23 * ref
+    # a quarter of each, within half a step of bf16 and the norm's rounding
+    for part, want in ((x[:10], 0.125), (x[2 ** 31 - 8:2 ** 31 + 8], 0.125), (x[-5:], 0.5)):
+        assert (part.float() - want).abs().max() <= want * (2.0 ** -8 + 3 * 2.0 ** -24)
+    assert bool((x[:-5] == x[0]).all())
+
+
+def test_two_streams_at_once():
+    """Two lists on two streams, each with scratch of its own."""
+    jobs = []
+    for seed in (1, 2):
+        xs = [v for _, v in _tensors(seed, [(300000, B, 3), (513, F, 1), (90000, F, 0)])]
+        out = [torch.empty_like(v) for v in xs]
+        lst = moe.make_grad_list(xs, out)
+        jobs.append((lst, xs, out, torch.zeros(1, device="cuda"),
+                     torch.empty(moe.moe_grad_scratch_bytes(3), dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for lst, _, _, norm, scratch, side in jobs:
+            with torch.cuda.stream(side):
+                moe.check(moe.moe_grad_norm(lst, norm, scratch))
+                moe.check(moe.moe_grad_clip(lst, norm, 0.5))
+    torch.cuda.synchronize()
+    for lst, xs, out, norm, _, _ in jobs:
+        got, n = [o.clone() for o in out], float(norm)
+        one = _norm(lst)
+        moe.check(moe.moe_grad_clip(lst, one, 0.5))
+        torch.cuda.synchronize()
+        assert float(one) == n and all(torch.equal(a, b) for a, b in zip(got, out))
