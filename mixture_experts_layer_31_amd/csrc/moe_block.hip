@@ -13,14 +13,13 @@
 //
 // Product.  C[m, n] = sum over runs b of 128 of sA[b, m] sB[b, n] P_b[m, n], P_b =
 // sum_{k in b} A[m, k] B[n, k] from the matrix core; each run's P_b is promoted
-// into the fp32 result on the vector ALU.  How P_b is summed goes by C's type:
-//   bf16: the e4m3 matrix instruction (unit scales; 4.5 PFLOP/s in registers).  It
-//     adds eight products at a time, each cut at 13 bits below the largest one's
-//     leading bit (measured: beside products of +-2^16 one of 2^3 survives and one
-//     of 2^2 does not), then accumulates in fp32.  The sums come out 1.5e-5 off
-//     (relative 2-norm, normal data), a hundredth of bf16's own rounding, 1.7e-3.
-//   fp32: too coarse there, so the codes become bf16 (exact) for the bf16 matrix
-//     instruction, whose sums are fp32's (5e-9 to 4e-8 off), at 2.3 PFLOP/s.
+// into the fp32 result on the vector ALU.  The codes become bf16 (exact) in registers for
+// the bf16 matrix instruction, whose products are exact and whose sums are fp32's (5e-9 to 4e-8
+// off, relative 2-norm, normal data), at 2.3 PFLOP/s in registers.  The e4m3 matrix instruction has
+// twice that rate and is not used: it adds eight products at a time, each cut at 13 bits below
+// the largest one's leading bit (beside products of +-2^16 one of 2^3 survives and one of 2^2
+// does not), so where large terms cancel the rest of the sum is lost.  Its results are 1.5e-5 off on normal
+// data, and 16384 x 4096 x 4096 took 232 us with it against 490.
 #include <type_traits>
 
 #include "moe_args.h"
@@ -381,13 +380,13 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
                : "memory", "m0");
 }
 
-// Large products with bf16 results: 256 x 256 tiles of eight waves, 128 x 64 each, or, where those
+// Large products with bf16 results: 256 x 128 tiles of eight waves, 64 x 64 each, or, where those
 // are too few, 128 x 128 (96 x 128) tiles of two groups of four waves, 64 x 64 (48 x 64) each, that
 // share the runs and are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
-// 16384 x 4096 x 4096: 239 us, 2.3 PFLOP/s (a library's unscaled product 188 us).  Of a tile's 60 us five are
-// its first loads and its epilogue; in a step the promotion's vector instructions share the wave's issue
-// slots with the matrix instructions, at the clock that the power allows.  The 256 x 256 kernel spills some 200
-// bytes a lane, outside its main loop.  The 128 x 128 tiles are bound by the L2's 12 to 13 TB/s into LDS.
+// 16384 x 4096 x 4096: 490 us, 1.12 PFLOP/s, 2048 x 2048 x 8192: 63 us, 1.08 (a library's bf16 product on
+// values of the same sizes 425 us, 1.29 PFLOP/s).  Bound by the matrix instructions at the clock that the power
+// allows: without the widening, or without the promotion, the same product takes 489 to 504 us.  256 x 256
+// tiles took 476, and 637 with tile scales: their sums and operands do not fit the registers.
 template <int MB_, int WGM_, int WGN_, int KG_>
 struct LargeTile {
   static constexpr int MB = MB_, NB = 4, WGM = WGM_, WGN = WGN_, KG = KG_;
@@ -420,11 +419,14 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
           [&](int r) { return r < nrows ? int(r * p.ldb) : -1; }, wave, lane);
   const uint32_t base = lds_addr(smem);
   const int nblocks = (p.N + 127) / 128;
-  static_assert(QA + BN / 64 == WAVES, "a load of scales a wave");
-  const bool sis_a = wave < QA;
+  // scales, 64 a load; with more waves than loads some come twice
+  constexpr int QB = BN / 64;
+  static_assert(QA + QB <= WAVES, "a load of scales a wave");
+  const int sq = wave % (QA + QB);
+  const bool sis_a = sq < QA;
   const i32x4 rs = sis_a ? make_rsrc(p.SA, uint32_t(p.ksteps) * p.ldsa * 4u)
                          : make_rsrc(p.SB, (B_TILE ? uint32_t(p.ksteps) * p.N : uint32_t(nblocks) * p.ldsb) * 4u);
-  const int sr = (sis_a ? wave : wave - QA) * 64 + lane;
+  const int sr = (sis_a ? sq : sq - QA) * 64 + lane;
   const int sstep = sis_a ? p.ldsa * 4 : B_TILE ? p.N * 4 : 4;
   const int soff = sr >= (sis_a ? mrows : nrows) ? int(0x80000000u)
                    : sis_a ? (m0 + sr) * 4 : B_TILE ? (n0 + sr) * 4 : (n0 + sr) / 128 * p.ldsb * 4;
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     if (q < NA) dma16(sa.rsrc, st + uint32_t(wave * NA + q) * 1024u, sa.vb[q] + kb);
     else if (q < NA + NBI)
       dma16(sb.rsrc, st + A_BYTES + uint32_t(wave * NBI + q - NA) * 1024u, sb.vb[q - NA] + kb);
-    else dma4(rs, st + A_BYTES + B_BYTES + wave * 256, there ? soff + kt * sstep : int(0x80000000u));
+    else dma4(rs, st + A_BYTES + B_BYTES + sq * 256, there ? soff + kt * sstep : int(0x80000000u));
   };
   auto issue = [&](int s, int i) __attribute__((always_inline)) {
 #pragma unroll
@@ -474,19 +476,33 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   auto scale_b = [&](int st, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const SB_*>(sbp + st + j * 64);
   };
-  i32x8 b[NB], a;
-  SB_ sbv[NS];
-  float sav;
+  // A step goes over its MB blocks of 16 rows of A against the NB blocks of B, two of those at a time.
+  // A block's codes are widened while the one before it is multiplied, and a pair's run sums are promoted
+  // during the next pair's products: a wave that promotes right behind its own product stalls on it.
+  bf16x8 wb[NB][4], wa[4];
+  i32x8 rb[2];        // the last pair of B, widened during the step's first products
+  SB_ sbv[NS] = {};
+  float sav = 0.f, sp = 0.f;  // scales of the current block of A and of the one before it
+  f32x4 R[2] = {};    // run sums of the last pair
+  auto widen_all = [&](const i32x8& f, bf16x8 (&w)[4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = widen(f, e);
+  };
   auto open = [&](int st) __attribute__((always_inline)) {
-    a = frag_a(st, 0);
+    widen_all(frag_a(st, 0), wa);
     sav = scale_a(st, 0);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) b[j] = frag_b(st, j);
-#pragma unroll
-    for (int j = 0; j < NS; ++j) sbv[j] = scale_b(st, j);
+    for (int j = 0; j < 2; ++j) {
+      widen_all(frag_b(st, j), wb[j]);
+      rb[j] = frag_b(st, j + 2);
+    }
   };
-  auto mfma = [&](const i32x8& x, const i32x8& y) __attribute__((always_inline)) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{}, 0, 0, 0, 0, 0, 0);
+  auto products = [&](int j0, f32x4 (&q)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        q[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j0 + j][e], wa[e], e ? q[j] : f32x4{}, 0, 0, 0);
   };
   auto promote = [&](int i, int j, const f32x4& part, float sr_) __attribute__((always_inline)) {
 #pragma unroll
@@ -496,39 +512,64 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
       acc[i][j][e] = __builtin_fmaf(part[e], sc, acc[i][j][e]);
     }
   };
-  // One 16-row block of A against the step's four of B, the block after it on the way.
-  // Each product's run sums wait a whole block in P before they are promoted, between the
-  // next block's products: a wave that promotes right behind its own product stalls on it.
-  f32x4 P[NB];
-  float sp = 0.f;
-  auto row = [&](int st, int i, bool more) __attribute__((always_inline)) {
-    i32x8 an = a;
-    float sn = sav;
-    if (more) {
-      an = frag_a(st, i + 1);
-      sn = scale_a(st, i + 1);
+  // Block i of stage st; `next` is what follows: 0 its next block, 1 the first one of stage sn, 2 nothing
+  // that can be read yet.  `loads(q)` issues what goes with quarter q of it.
+  auto row = [&](auto next, int st, int i, int sn, auto loads) __attribute__((always_inline)) {
+    constexpr int NEXT = decltype(next)::value;
+    i32x8 an, bn[2];
+    float san = 0.f;
+    if constexpr (NEXT < 2) {
+      an = NEXT ? frag_a(sn, 0) : frag_a(st, i + 1);
+      san = NEXT ? scale_a(sn, 0) : scale_a(st, i + 1);
     }
+    if constexpr (NEXT == 1) {
+      bn[0] = frag_b(sn, 0);
+      bn[1] = frag_b(sn, 1);
+    }
+    f32x4 Q[2];
+    loads(0);
+    products(0, Q);
+    loads(1);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const f32x4 q = mfma(b[j], a);
-      if (i > 0) promote(i - 1, j, P[j], sp);
-      P[j] = q;
+    for (int j = 0; j < 2; ++j) promote(i > 0 ? i - 1 : MB - 1, j + 2, R[j], sp);
+    if (i == 0) {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) sbv[j] = scale_b(st, j);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) widen_all(rb[j], wb[j + 2]);
     }
+    if constexpr (NEXT == 1) {
+      rb[0] = frag_b(sn, 2);
+      rb[1] = frag_b(sn, 3);
+    }
+    loads(2);
+    products(2, R);
+    loads(3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) promote(i, j, Q[j], sav);
     sp = sav;
-    a = an;
-    sav = sn;
-    if (more) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+    if constexpr (NEXT < 2) {
+      widen_all(an, wa);
+      sav = san;
+    }
+    if constexpr (NEXT == 1) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, B_TILE ? 8 : 5, 0);
+      for (int j = 0; j < 2; ++j) widen_all(bn[j], wb[j]);
+    }
+    if constexpr (NEXT == 0) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto rest = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < NB; ++j) promote(i, j, P[j], sp);
-  };
+  using same_stage = std::integral_constant<int, 0>;
+  using next_stage = std::integral_constant<int, 1>;
+  using nothing = std::integral_constant<int, 2>;
+  const auto none = [](int) __attribute__((always_inline)) {};
   // the last step's codes behind column K become 0, once its stage has arrived
   const bool tail = p.K % 128 != 0;
   auto mend = [&](int st) __attribute__((always_inline)) {
@@ -551,14 +592,11 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     __syncthreads();
   };
   const int n = (p.ksteps + KG - 1) / KG;  // steps a group
-  // A step's loads are spread over the one before it (in one burst behind the barrier they hold up
-  // the fragment reads): over its rows, or, where a step is too short for them to arrive
-  // in (128 x 128: 59 us, so 51, at 1536 x 2048 x 8197; 256 x 256: 275 us, so 287, at 16384 x 4096 x 4096),
-  // over the last products of the step before that, into the stage that they have just freed.
-  constexpr bool EARLY = MB < 8;
+  // A step's loads are issued over the last products of the step two before it, into the stage that has
+  // just been read, a quarter with each eight products (in one burst they hold up the fragment reads).
   issue(0, 0);
-  if constexpr (EARLY) issue(1, 1);
-  wait_vmcnt<EARLY ? NL : 0>();
+  issue(1, 1);
+  wait_vmcnt<NL>();
   __builtin_amdgcn_s_barrier();
   if (tail && n == 1) mend(0);
   open(0);
@@ -567,55 +605,25 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   for (; kt < straight; ++kt) {
     const int sn = STAGE - st;
 #pragma unroll
-    for (int i = 0; i < MB - 3; ++i) {
-      if constexpr (!EARLY) {
-        constexpr int PR = (NL + MB - 4) / (MB - 3);
-#pragma unroll
-        for (int q = i * PR; q < (i + 1) * PR && q < NL; ++q) issue1(st ? 0 : 1, kt + 1, q);
-      }
-      row(st, i, true);
-    }
-    // with the last two blocks of A in registers the stage is read: the next one takes
-    // over, its fragments replacing those of B as the last products release them
-    const i32x8 a6 = frag_a(st, MB - 2), a7 = frag_a(st, MB - 1);
-    const float s6 = scale_a(st, MB - 2), s7 = scale_a(st, MB - 1);
-    row(st, MB - 3, false);
+    for (int i = 0; i < MB - 1; ++i) row(same_stage{}, st, i, sn, none);
+    // with the last block of A in registers the stage is read: the next one takes over, its
+    // fragments replacing those of B as the last products release them
     wait_lgkm0();
     wait_vmcnt<0>();
     __builtin_amdgcn_s_barrier();
-    a = frag_a(sn, 0);
-    sav = scale_a(sn, 0);
-    f32x4 P6, P7;
+    row(next_stage{}, st, MB - 1, sn, [&](int r) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const f32x4 q6 = mfma(b[j], a6), q7 = mfma(b[j], a7);
-      b[j] = frag_b(sn, j);
-      if constexpr (EARLY) {
-#pragma unroll
-        for (int q = j * NL / NB; q < (j + 1) * NL / NB; ++q) issue1(st ? 1 : 0, kt + 2, q);
-      }
-      if (j == 0) {
-        rest(MB - 3);
-      } else {
-        promote(MB - 2, j - 1, P6, s6);
-        promote(MB - 1, j - 1, P7, s7);
-      }
-      P6 = q6;
-      P7 = q7;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    promote(MB - 2, NB - 1, P6, s6);
-    promote(MB - 1, NB - 1, P7, s7);
-#pragma unroll
-    for (int j = 0; j < NS; ++j) sbv[j] = scale_b(sn, j);
+      for (int q = r * NL / 4; q < (r + 1) * NL / 4; ++q) issue1(st ? 1 : 0, kt + 2, q);
+    });
     st = sn;
-    __builtin_amdgcn_sched_barrier(0);
   }
-  if (tail && n > 1) {
-    if constexpr (!EARLY) issue(st ? 0 : 1, kt + 1);
+  const auto last_rows = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) row(st, i, i + 1 < MB);
-    rest(MB - 1);
+    for (int i = 0; i < MB - 1; ++i) row(same_stage{}, st, i, 0, none);
+    row(nothing{}, st, MB - 1, 0, none);
+  };
+  if (tail && n > 1) {
+    last_rows();
     wait_lgkm0();
     wait_vmcnt<0>();
     __builtin_amdgcn_s_barrier();
@@ -623,9 +631,9 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     mend(st);
     open(st);
   }
+  last_rows();
 #pragma unroll
-  for (int i = 0; i < MB; ++i) row(st, i, i + 1 < MB);
-  rest(MB - 1);
+  for (int j = 0; j < 2; ++j) promote(MB - 1, j + 2, R[j], sp);
   wait_vmcnt<0>();  // the loads that missed still write their zeros
   if constexpr (KG > 1) {  // join the groups' sums
     constexpr int LDR = BN + 4;
@@ -670,6 +678,7 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     return;
   }
   // Epilogue: the whole bf16 tile through LDS, whole rows out
+  static_assert(BN / 8 <= 32 && RING >= BM * BN * 2, "the tile fits the ring, its rows have at most 32 chunks");
   __syncthreads();
   BandTile<2> t{smem, BN};
 #pragma unroll
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   for (int k = threadIdx.x; k < BM * (BN / 8); k += TL::THREADS) {
     const int r = k / (BN / 8), ch = k % (BN / 8);
     if (r >= mrows || ch * 8 >= nrows) continue;
-    const uint4 v = *reinterpret_cast<const uint4*>(smem + r * BN * 2 + ((ch ^ (r & 31)) << 4));
+    const uint4 v = *reinterpret_cast<const uint4*>(smem + r * BN * 2 + ((ch ^ (r & (BN / 8 - 1))) << 4));
     uint16_t* dst = c + r * p.ldc + ch * 8;
     if (ch * 8 + 8 <= nrows) {
       store16(dst, v);
@@ -818,29 +827,19 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
       for (int j = 0; j < NB; ++j) promote(i, j);
   };
   auto multiply = [&](const Step& x) __attribute__((always_inline)) {
-    if constexpr (OUT_F32) {
-      promote_all();
+    promote_all();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        bf16x8 wb[NB];
+    for (int e = 0; e < 4; ++e) {
+      bf16x8 wb[NB];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) wb[j] = widen(x.b[j], e);
+      for (int j = 0; j < NB; ++j) wb[j] = widen(x.b[j], e);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const bf16x8 wa = widen(x.a[i], e);
+      for (int i = 0; i < MB; ++i) {
+        const bf16x8 wa = widen(x.a[i], e);
 #pragma unroll
-          for (int j = 0; j < NB; ++j)
-            P[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, e ? P[i][j] : f32x4{}, 0, 0, 0);
-        }
+        for (int j = 0; j < NB; ++j)
+          P[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, e ? P[i][j] : f32x4{}, 0, 0, 0);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          promote(i, j);
-          P[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x.b[j], x.a[i], f32x4{}, 0, 0, 0, 0, 0, 0);
-        }
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i) psa[i] = x.sa[i];
@@ -1119,13 +1118,9 @@ __global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectA
     }
     const i32x8 b = cur.b.codes();
     f32x4 part = {};
-    if constexpr (OUT_F32) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b, e), widen(a, e), part, 0, 0, 0);
-    } else {
-      part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, part, 0, 0, 0, 0, 0, 0);
-    }
+    for (int e = 0; e < 4; ++e)
+      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b, e), widen(a, e), part, 0, 0, 0);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], sa * cur.sb[B_TILE ? e : 0], acc[e]);
     cur = next;
@@ -1207,20 +1202,21 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
     for (int64_t j = threadIdx.x; j < N; j += 256) C[r * ldc + j] = T(0);
 }
 
-// Which kernel a product takes.  Measured on an MI355X (256 CUs, one workgroup of 256 x 256 or 128 x
+// Which kernel a product takes.  Measured on an MI355X (256 CUs, one workgroup of 256 x 128 or 128 x
 // 128, or two of 64 x 64, a CU), in us a round of workgroups with `steps` runs:
-//   256 x 256             5   + 1.72 steps  (4096 x 4096 x 4096 61.7, 16384 x 4096 x 4096 4 x 68)
-//   128 x 128             5.7 + 0.53 steps  (2048 x 2048 x 2048 14.2, 2048 x 2048 x 8192 39.6)
-//   96 x 128              4.9 + 0.52 steps  (1536 x 2048 x 2048 12.6 in 256 tiles, 14.2 in 192 of 128 x 128)
-//   64 x 64, two a CU     2   + 0.5  steps  (2048 x 2048 x 2048 19.6 in two rounds)
-//   64 x 64, two groups   3   + 0.28 steps  (256 x 4096 x 4096 11.1, 12.6 with one group)
-// The sizes' best is the least of these.  fp32 results have no 256 x 256 kernel and another 128 x 128
-// one (2.5 + 0.8 against 2 + 0.5 of the 64 x 64 tiles, all of its steps 1.6 times as long).  Where a few
-// rows past a multiple of 256 cost a further round, they go to a launch of 64 x 64 tiles (8197 x 2048 x
-// 1536: 34.3, in one launch 48.6; 4128 x 4096 x 2048: 40.3, 57.2).
+//   256 x 128             5.5 + 1.75 steps  (4096 x 4096 x 4096 122 in two rounds, 8192 x 2048 x 1536 52)
+//   128 x 128             6   + 0.92 steps  (2048 x 2048 x 2048 20.8, 2048 x 2048 x 8192 63 to 73)
+//   96 x 128              5.3 + 0.76 steps  (1536 x 2048 x 2048 17.1, 1536 x 2048 x 8192 54.5)
+//   64 x 64, two a CU     3.9 + 0.73 steps  (2048 x 1024 x 2048 15.4, 2048 x 1024 x 8192 51)
+//   64 x 64, two groups   3.9 + 0.36 steps  (1024 x 1024 x 2048 9.6, 1024 x 1024 x 8192 27.6)
+// and with fp32 results, which have other 128 x 128 tiles and none larger,
+//   128 x 128             2.5 + 1.28 steps  (2048 x 2048 x 2048 24.9)
+//   64 x 64, two a CU     2   + 0.8  steps  (2048 x 1024 x 2048 16.1)
+//   64 x 64, two groups   3   + 0.45 steps  (1024 x 1024 x 2048 10)
+// The sizes' best is the least of these.  Where a few rows past a multiple of 256 cost a further round, they
+// go to a launch of 64 x 64 tiles.
 // With too few tiles for the chip the contraction is cut into parts, whose sums take a second launch:
-// 4 us and their bytes at 3 TB/s, written and read (256 x 256 x 16384 in 16 parts of 8 runs 12.0, whole 31.6;
-// 512 x 512 x 8192 in 4 of 16 13.0, whole 18.2).
+// 4 us and their bytes at 3 TB/s, written and read.
 enum MmKind { MM_LARGE, MM_128, MM_96, MM_64, MM_64X2 };
 struct MmPlan {
   MmKind kind;
@@ -1233,7 +1229,7 @@ constexpr double kPartBytes = 64 << 20;  // most of the parts' sums
 MmPlan mm_plan(long long M, long long N, int steps, bool f32, bool whole = false) {
   constexpr int kCus = 256;
   const auto tiles = [&](long long m, int bm, int bn) { return ceil_div(m, bm) * ceil_div(N, bn); };
-  const auto large = [&](long long m) { return ceil_div(tiles(m, 256, 256), kCus) * (5 + 1.72 * steps); };
+  const auto large = [&](long long m) { return ceil_div(tiles(m, 256, 128), kCus) * (5.5 + 1.75 * steps); };
   MmPlan best{MM_64, 1e30, 0, 1, steps};
   const auto consider = [&](MmKind kind, int bm, int bn, int slots, double fix, double each) {
     const long long t = tiles(M, bm, bn);
@@ -1245,12 +1241,11 @@ MmPlan mm_plan(long long M, long long N, int steps, bool f32, bool whole = false
       if (us < best.us) best = {kind, us, 0, int(ceil_div(steps, per)), per};
     }
   };
-  const double slow = f32 ? 1.6 : 1;
-  consider(MM_64X2, 64, 64, kCus, 3, 0.28 * slow);
-  consider(MM_64, 64, 64, 2 * kCus, 2, 0.5 * slow);
-  consider(MM_128, 128, 128, kCus, f32 ? 2.5 : 5.7, f32 ? 0.8 * slow : 0.53);
+  consider(MM_64X2, 64, 64, kCus, f32 ? 3 : 3.9, f32 ? 0.448 : 0.36);
+  consider(MM_64, 64, 64, 2 * kCus, f32 ? 2 : 3.9, f32 ? 0.8 : 0.73);
+  consider(MM_128, 128, 128, kCus, f32 ? 2.5 : 6, f32 ? 1.28 : 0.92);
   if (f32) return best;
-  consider(MM_96, 96, 128, kCus, 4.9, 0.52);
+  consider(MM_96, 96, 128, kCus, 5.3, 0.76);
   if (large(M) < best.us) best = {MM_LARGE, large(M), 0, 1, steps};
   const int rest = int(M % 256);
   if (M > 256 && rest > 0 && rest <= 64) {
@@ -1280,7 +1275,7 @@ int launch_mm(const MmArgs& a, const MmPlan& plan, bool b_tile, bool f32, float*
       case MM_96: return launch_mm_large<LargeTile<3, 2, 2, 2>>(p, b_tile, s);
       case MM_LARGE: break;
     }
-    return launch_mm_large<LargeTile<8, 2, 4, 1>>(p, b_tile, s);
+    return launch_mm_large<LargeTile<4, 4, 2, 1>>(p, b_tile, s);
   };
   if (plan.peel > 0) {
     MmArgs rest = p;
