@@ -433,7 +433,8 @@ typedef struct moe_block_mm_desc {
  * dW = dy^T x (a, b: the codes_t of dy and x, b_scale MOE_SCALE_TILE, K tokens).
  * A run of 128 products is summed by the matrix core, multiplied by both scales
  * and added over the runs in fp32: the products are exact, every sum is fp32's, and
- * C is rounded once.  With a_type F32 or BF16
+ * C is rounded once.  Scales may be any finite numbers: their product alone may lie outside
+ * fp32's range where the run's result does not.  With a_type F32 or BF16
  * `a` holds the values, a_scales is NULL and the call quantises them as
  * moe_block_quant would, with the same result.  Codes behind column K are not
  * used.  Padding of C's rows (ldc > N) is left as it was.

@@ -360,13 +360,28 @@ __device__ __forceinline__ int take_part(MmArgs& p, int l) {
   return l - s * tiles;
 }
 
-// Eight of the fragment's codes as bf16 (exact), the eighth part s of its 32.
-__device__ __forceinline__ bf16x8 widen(const i32x8& f, int s) {
+// A scale as m 2^e: the power goes into the operand when its codes are widened, which costs nothing
+// (the conversion takes the exponent of `power`), and m stays for the promotion.  The product of two
+// scales may lie far outside fp32's range where the result does not.  With 2^e in [2^-50, 2^66] widened
+// codes and their products' sums are normal numbers or 0 unless the result is past the range, and
+// the product of two m (each below 2^62, and from 2^-99 on) is finite, and subnormal only where the
+// run adds less than 2^-200.
+struct Scale {
+  float power, m;
+  __device__ __forceinline__ Scale() = default;
+  __device__ __forceinline__ explicit Scale(float s) {
+    power = __builtin_amdgcn_fmed3f(fabsf(s), 0x1p-50f, 0x1p66f);
+    m = s * __uint_as_float(0x7f000000u - (__float_as_uint(power) & 0x7f800000u));
+  }
+};
+
+// Eight of the fragment's codes, times the power of two in `power`, as bf16 (exact): the part s of its 32.
+__device__ __forceinline__ bf16x8 widen(const i32x8& f, int s, float power) {
   bf16x8 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + i], 1.f, false);
-    const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + i], 1.f, true);
+    const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + i], power, false);
+    const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * s + i], power, true);
     r[4 * i] = lo[0]; r[4 * i + 1] = lo[1]; r[4 * i + 2] = hi[0]; r[4 * i + 3] = hi[1];
   }
   return r;
@@ -476,25 +491,33 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   auto scale_b = [&](int st, int j) __attribute__((always_inline)) {
     return *reinterpret_cast<const SB_*>(sbp + st + j * 64);
   };
+  // the scale of the lane's row of B in a fragment
+  const char* sbr = smem + A_BYTES + B_BYTES + QA * 256 + (wn * 16 * NB + l16) * 4;
+  auto row_scale_b = [&](int st, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<const float*>(sbr + st + j * 64);
+  };
   // A step goes over its MB blocks of 16 rows of A against the NB blocks of B, two of those at a time.
   // A block's codes are widened while the one before it is multiplied, and a pair's run sums are promoted
   // during the next pair's products: a wave that promotes right behind its own product stalls on it.
   bf16x8 wb[NB][4], wa[4];
-  i32x8 rb[2];        // the last pair of B, widened during the step's first products
+  i32x8 rb[2];        // the last pair of B, widened during the step's first products, and its scales
+  float rs2[2];
   SB_ sbv[NS] = {};
-  float sav = 0.f, sp = 0.f;  // scales of the current block of A and of the one before it
+  float sav = 0.f, sp = 0.f;  // m of the current block of A and of the one before it
   f32x4 R[2] = {};    // run sums of the last pair
-  auto widen_all = [&](const i32x8& f, bf16x8 (&w)[4]) __attribute__((always_inline)) {
+  auto widen_all = [&](const i32x8& f, float scale, bf16x8 (&w)[4]) __attribute__((always_inline)) {
+    const Scale s(scale);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = widen(f, e);
+    for (int e = 0; e < 4; ++e) w[e] = widen(f, e, s.power);
+    return s.m;
   };
   auto open = [&](int st) __attribute__((always_inline)) {
-    widen_all(frag_a(st, 0), wa);
-    sav = scale_a(st, 0);
+    sav = widen_all(frag_a(st, 0), scale_a(st, 0), wa);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      widen_all(frag_b(st, j), wb[j]);
+      widen_all(frag_b(st, j), row_scale_b(st, j), wb[j]);
       rb[j] = frag_b(st, j + 2);
+      rs2[j] = row_scale_b(st, j + 2);
     }
   };
   auto products = [&](int j0, f32x4 (&q)[2]) __attribute__((always_inline)) {
@@ -517,14 +540,17 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   auto row = [&](auto next, int st, int i, int sn, auto loads) __attribute__((always_inline)) {
     constexpr int NEXT = decltype(next)::value;
     i32x8 an, bn[2];
-    float san = 0.f;
+    float san = 0.f, sbn[2];
     if constexpr (NEXT < 2) {
       an = NEXT ? frag_a(sn, 0) : frag_a(st, i + 1);
       san = NEXT ? scale_a(sn, 0) : scale_a(st, i + 1);
     }
     if constexpr (NEXT == 1) {
-      bn[0] = frag_b(sn, 0);
-      bn[1] = frag_b(sn, 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        bn[j] = frag_b(sn, j);
+        sbn[j] = row_scale_b(sn, j);
+      }
     }
     f32x4 Q[2];
     loads(0);
@@ -534,13 +560,24 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     for (int j = 0; j < 2; ++j) promote(i > 0 ? i - 1 : MB - 1, j + 2, R[j], sp);
     if (i == 0) {
 #pragma unroll
-      for (int j = 0; j < NS; ++j) sbv[j] = scale_b(st, j);
+      for (int j = 0; j < NS; ++j) {
+        sbv[j] = scale_b(st, j);
+        if constexpr (B_TILE) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) widen_all(rb[j], wb[j + 2]);
+          for (int e = 0; e < 4; ++e) sbv[j][e] = Scale(sbv[j][e]).m;
+        } else {
+          sbv[j] = Scale(sbv[j]).m;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) widen_all(rb[j], rs2[j], wb[j + 2]);
     }
     if constexpr (NEXT == 1) {
-      rb[0] = frag_b(sn, 2);
-      rb[1] = frag_b(sn, 3);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        rb[j] = frag_b(sn, j + 2);
+        rs2[j] = row_scale_b(sn, j + 2);
+      }
     }
     loads(2);
     products(2, R);
@@ -548,13 +585,10 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
 #pragma unroll
     for (int j = 0; j < 2; ++j) promote(i, j, Q[j], sav);
     sp = sav;
-    if constexpr (NEXT < 2) {
-      widen_all(an, wa);
-      sav = san;
-    }
+    if constexpr (NEXT < 2) sav = widen_all(an, san, wa);
     if constexpr (NEXT == 1) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) widen_all(bn[j], wb[j]);
+      for (int j = 0; j < 2; ++j) widen_all(bn[j], sbn[j], wb[j]);
     }
     if constexpr (NEXT == 0) {
       __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
@@ -786,8 +820,8 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
   using SB_ = typename std::conditional<B_TILE, f32x4, float>::type;
   struct Step {
     i32x8 a[MB], b[NB];
-    float sa[MB];
-    SB_ sb[NB];
+    float sa[MB], sr[NB];  // scales of the lane's rows of A and B
+    SB_ sb[NB];            // and of its results' columns
   };
   auto read = [&](int i, Step& x) __attribute__((always_inline)) {
     const char* st = ring + (i % S) * STAGE;
@@ -806,6 +840,7 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
     for (int q = 0; q < NB; ++q) {
       const int r = (wn * NB + q) * 16;
       x.b[q] = frag(st + A_BYTES + r * 128);
+      x.sr[q] = sc[BM + r + l16];
       x.sb[q] = *reinterpret_cast<const SB_*>(sc + BM + r + (B_TILE ? 4 * g4 : 0));
     }
   };
@@ -828,23 +863,35 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
   };
   auto multiply = [&](const Step& x) __attribute__((always_inline)) {
     promote_all();
+    Scale ra[MB], rb[NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) ra[i] = Scale(x.sa[i]);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) rb[j] = Scale(x.sr[j]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       bf16x8 wb[NB];
 #pragma unroll
-      for (int j = 0; j < NB; ++j) wb[j] = widen(x.b[j], e);
+      for (int j = 0; j < NB; ++j) wb[j] = widen(x.b[j], e, rb[j].power);
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
-        const bf16x8 wa = widen(x.a[i], e);
+        const bf16x8 wa = widen(x.a[i], e, ra[i].power);
 #pragma unroll
         for (int j = 0; j < NB; ++j)
           P[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa, e ? P[i][j] : f32x4{}, 0, 0, 0);
       }
     }
 #pragma unroll
-    for (int i = 0; i < MB; ++i) psa[i] = x.sa[i];
+    for (int i = 0; i < MB; ++i) psa[i] = ra[i].m;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) psb[j] = x.sb[j];
+    for (int j = 0; j < NB; ++j) {
+      if constexpr (B_TILE) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) psb[j][e] = Scale(x.sb[j][e]).m;
+      } else {
+        psb[j] = Scale(x.sb[j]).m;
+      }
+    }
   };
   const int n = (p.ksteps + KG - 1) / KG;  // steps a group
   const bool tail = p.K % 128 != 0;
@@ -1042,7 +1089,7 @@ __global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectA
   const int nb = min(nt * 16, q.N - 1) >> 7;
   struct Run {
     RunPart a, b;
-    float sa, sb[B_TILE ? 4 : 1];
+    float sa, sr, sb[B_TILE ? 4 : 1];  // scales of the lane's row of A, of B and of its results' columns
   };
   auto load = [&](int kt, Run& r) __attribute__((always_inline)) {
     const int k = kt * 128 + 32 * g;
@@ -1055,8 +1102,9 @@ __global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectA
     if constexpr (B_TILE) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.sb[e] = nc + e < q.N && run ? q.SB[int64_t(kt) * q.N + nc + e] : 0.f;
+      r.sr = n < q.N && run ? q.SB[int64_t(kt) * q.N + n] : 0.f;
     } else {
-      r.sb[0] = q.SB[int64_t(nb) * q.ksteps + min(kt, q.ksteps - 1)];
+      r.sr = r.sb[0] = q.SB[int64_t(nb) * q.ksteps + min(kt, q.ksteps - 1)];
     }
   };
   Run cur;
@@ -1117,12 +1165,13 @@ __global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectA
       sa = cur.sa;
     }
     const i32x8 b = cur.b.codes();
+    const Scale ra(sa), rb(cur.sr);
     f32x4 part = {};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b, e), widen(a, e), part, 0, 0, 0);
+      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b, e, rb.power), widen(a, e, ra.power), part, 0, 0, 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], sa * cur.sb[B_TILE ? e : 0], acc[e]);
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], ra.m * Scale(cur.sb[B_TILE ? e : 0]).m, acc[e]);
     cur = next;
   }
   using O = typename std::conditional<OUT_F32, float, uint16_t>::type;
