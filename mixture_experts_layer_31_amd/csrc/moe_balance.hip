@@ -14,9 +14,10 @@
 // adds p to per-lane sums over the block's tokens, joined at the end over the
 // wave's tokens and the block's waves in a fixed order, and counts the block's ids
 // with LDS atomics (integers: their order does not show).  Up to kBalOneBlock tokens
-// one block does it all; past that a second launch adds the blocks' partial sums, in 64
-// bits, 64 experts a block, and its last block the loss.  Sums over one block's
-// tokens are fp32: T / 16384 p <= 1 a lane past 16384 tokens, T / 4096 past 256 experts.
+// one block does it all; past that a second launch adds the blocks' partial sums, 64
+// experts a block, and its last block the loss.  Every sum over tokens is 64 bits wide: equal
+// numbers added in fp32 are rounded the same way each time (2^22 tokens of 3 experts: 11 u off).  A wave's sum
+// and a block's are rounded to fp32 where they are handed on, which adds u each.
 // Partial sums in global atomics would be one launch fewer and another result with
 // each run.  256 tokens of 128 experts take 9.2 us in one launch and 7.7 in two, whose
 // second costs the host 4; 512 tokens 14.8 against 7.6.
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
   constexpr int GROUPS = kBalThreads / LPT, WAVES = kBalThreads / 64, COLS = LPT * VPL;
   __shared__ int32_t hist[COLS];
   __shared__ float red[WAVES][COLS];
-  __shared__ float zred[WAVES];
+  __shared__ double zred[WAVES];
   __shared__ int32_t nred[WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = tid & (LPT - 1);
   // token numbers in 64 bits: a step past the last of 2^31 - 1 tokens must not wrap
@@ -184,10 +185,10 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
       if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
     }
   }
-  float acc[VPL], zsum = 0.f;
+  double acc[VPL], zsum = 0.;
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) acc[i] = 0.f;
+  for (int i = 0; i < VPL; ++i) acc[i] = 0.;
   for (int64_t t = t0 + tid / LPT; t < t1; t += GROUPS) {
     float p[VPL];
     const bool kept = keep;
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
     if (!kept) continue;
     const float lse = softmax_row<LPT>(p, E, l);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) acc[i] += p[i];
-    zsum = __builtin_fmaf(lse, lse, zsum);
+    for (int i = 0; i < VPL; ++i) acc[i] += double(p[i]);
+    zsum = __builtin_fma(double(lse), double(lse), zsum);
     n += 1;
   }
   if constexpr (LPT == 16) {  // the wave's four tokens
@@ -216,18 +217,18 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
 #pragma unroll
     for (int q = 0; q < VPL / 4; ++q)
       *reinterpret_cast<float4*>(&red[wv][expert_of<LPT>(l, 4 * q)]) =
-          make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+          make_float4(float(acc[4 * q]), float(acc[4 * q + 1]), float(acc[4 * q + 2]), float(acc[4 * q + 3]));
   }
   if (lane == 0) {
     zred[wv] = zsum;
     nred[wv] = n;
   }
   __syncthreads();
-  float p = 0.f, z = 0.f;  // thread e: expert e's sum
+  double p = 0., z = 0.;  // thread e: expert e's sum
   int all = 0;
   if (tid < E) {
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) p += red[w][tid];
+    for (int w = 0; w < WAVES; ++w) p += double(red[w][tid]);
   }
   for (int w = 0; w < WAVES; ++w) {
     z += zred[w];
@@ -235,11 +236,11 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
   }
   if (gridDim.x > 1) {
     if (tid < E) {
-      out.p[size_t(blockIdx.x) * E + tid] = p;
+      out.p[size_t(blockIdx.x) * E + tid] = float(p);
       out.c[size_t(blockIdx.x) * E + tid] = hist[tid];
     }
     if (tid == 0) {
-      out.z[blockIdx.x] = z;
+      out.z[blockIdx.x] = float(z);
       out.n[blockIdx.x] = all;
       if (blockIdx.x == 0) *out.done = 0;
     }
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
   }
   double dot = 0.;
   if (tid < E) {
-    const double mp = all > 0 ? double(p) / all : 0.;
+    const double mp = all > 0 ? p / all : 0.;
     res.counts[tid] = hist[tid];
     res.mean_p[tid] = float(mp);
     dot = all > 0 ? mp * (double(hist[tid]) / (double(all) * K)) : 0.;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kBalThreads) balance_fwd_kernel(
   if (tid == 0) {
     res.counts[E] = all;
     res.losses[0] = float(E * dot);
-    res.losses[1] = all > 0 ? float(double(z) / all) : 0.f;
+    res.losses[1] = all > 0 ? float(z / all) : 0.f;
   }
 }
 
