@@ -5,9 +5,10 @@
 // e4m3(x / s) of the fp32 quotient.  The quotient must be the correctly rounded one
 // (it decides between two codes when it lies next to their border), without the
 // eight-odd instructions of a division: q0 = x r with r = 1 / s, then two steps
-// q <- q + r (x - q s), each with an exact residual in one FMA; the first leaves q
+// q <- q - r (q s - x), each with an exact residual in one FMA; the first leaves q
 // within an ulp, and from there the second rounds correctly (Markstein's theorem:
-// r is the correctly rounded reciprocal).  Residuals and r stay in range because
+// r is the correctly rounded reciprocal).  Where x is -0 the residual is +0, so that q stays
+// -0 (x - q s would be +0 too, and q + 0 = +0).  Residuals and r stay in range because
 // a run with a small amax is first scaled by a power of two, which the quotient does
 // not see.
 //
@@ -52,8 +53,8 @@ struct Quant {
   __device__ __forceinline__ float quotient(float x) const {
     x *= up;
     float q = x * r;
-    q = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
-    return __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
+    q = __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
+    return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
   }
   __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
     return pack_e4m3x4(quotient(a), quotient(b), quotient(c), quotient(d));
