@@ -435,9 +435,9 @@ typedef struct moe_block_mm_desc {
  * and added over the runs in fp32: the products are exact, every sum is fp32's, and
  * C is rounded once.  Scales may be any finite numbers: their product alone may lie outside
  * fp32's range where the run's result does not.  With a_type F32 or BF16
- * `a` holds the values, a_scales is NULL and the call quantises them as
- * moe_block_quant would, with the same result.  Codes behind column K are not
- * used.  Padding of C's rows (ldc > N) is left as it was.
+ * `a` holds the values, a_scales is NULL and the call quantises them to the codes
+ * that moe_block_quant gives; its sums may have another order than the product of those
+ * codes has, within the same bounds.  Codes behind column K are not used.  Padding of C's rows (ldc > N) is left as it was.
  * K = 0 gives C = 0 (or C as it was, with MOE_MM_ACCUMULATE); M = 0 or N = 0 is
  * MOE_OK and touches nothing.  a, b (codes) 16-byte aligned; values, C and
  * scales aligned to their element (MOE_EALIGN); scratch 16-byte aligned, of
