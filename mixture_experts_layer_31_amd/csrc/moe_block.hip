@@ -1011,7 +1011,7 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
   }
 }
 
-template <class TL>
+template <class TL, bool BF16 = true>  // BF16: bf16 results take these tiles too
 int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
   MmArgs p = a;
   p.ntm = int(ceil_div(p.M, TL::BM));
@@ -1019,11 +1019,11 @@ int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
   const long long tiles = (long long)p.ntm * p.ntn * (p.part ? ceil_div(p.ksteps, p.per) : 1);
   const unsigned grid = unsigned(tiles);
   prof_begin("block_mm_mid", s);
-  if (b_tile) {
-    if (f32) block_mm_mid_kernel<TL, true, true><<<grid, TL::THREADS, 0, s>>>(p);
-    else block_mm_mid_kernel<TL, true, false><<<grid, TL::THREADS, 0, s>>>(p);
-  } else {
-    if (f32) block_mm_mid_kernel<TL, false, true><<<grid, TL::THREADS, 0, s>>>(p);
+  if (f32) {
+    if (b_tile) block_mm_mid_kernel<TL, true, true><<<grid, TL::THREADS, 0, s>>>(p);
+    else block_mm_mid_kernel<TL, false, true><<<grid, TL::THREADS, 0, s>>>(p);
+  } else if constexpr (BF16) {
+    if (b_tile) block_mm_mid_kernel<TL, true, false><<<grid, TL::THREADS, 0, s>>>(p);
     else block_mm_mid_kernel<TL, false, false><<<grid, TL::THREADS, 0, s>>>(p);
   }
   prof_end(s);
@@ -1321,7 +1321,7 @@ int launch_mm(const MmArgs& a, const MmPlan& plan, bool b_tile, bool f32, float*
       case MM_64: return launch_mm_mid<MidTile<64, 64, 2, 2, 1>>(p, b_tile, f32, s);
       case MM_128:
         if (!f32) return launch_mm_large<LargeTile<4, 2, 2, 2>>(p, b_tile, s);
-        return launch_mm_mid<MidTile<128, 128, 2, 4, 1>>(p, b_tile, f32, s);
+        return launch_mm_mid<MidTile<128, 128, 2, 4, 1>, false>(p, b_tile, true, s);
       case MM_96: return launch_mm_large<LargeTile<3, 2, 2, 2>>(p, b_tile, s);
       case MM_LARGE: break;
     }
