@@ -377,8 +377,8 @@ enum moe_scale { MOE_SCALE_TILE = 0, MOE_SCALE_BLOCK = 1 };
 /* Dense e4m3 operands with one fp32 scale for each block of 128: the layer's
  * blockwise FP8 recipe (Prime Mega MoE news item, "How does the fused kernel
  * work?") for the linear layers beside the experts.  A matrix [R, C] is stored
- * as codes [R, ld] (ld >= C, a multiple of 16; multiples of 128 are up to a
- * quarter faster where a product's contraction is long) and
+ * as codes [R, ld] (ld >= C, a multiple of 16; multiples of 128 are a twentieth
+ * faster where a product's contraction is long) and
  *   MOE_SCALE_TILE   a scale for each 1 x 128 run of a row: [ceil(C/128), R]
  *                    (one row of scales per step of 128 columns);
  *   MOE_SCALE_BLOCK  a scale for each 128 x 128 block: [ceil(R/128), ceil(C/128)].

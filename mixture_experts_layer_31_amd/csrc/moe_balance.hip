@@ -9,8 +9,9 @@
 // Both passes read each logit once into registers.  LPT lanes share a token (16 up
 // to 256 experts, so a wave holds four tokens and a row reduction is four DPP
 // moves; 64 above, where 16 would hold 32 logits a lane), each with VPL logits of it in
-// runs of four: 65536 tokens, forward + backward in us, 16 lanes against 64: 64 experts
-// 21.8, 47; 128 experts 29.9, 50; 256 experts 47.4, 52; 512 experts 112, 82.  The forward
+// runs of four: 65536 tokens, forward + backward in us (with fp32 sums, one to two less),
+// 16 lanes against 64: 64 experts 21.8, 47; 128 experts 29.9, 50; 256 experts 47.4, 52; 512
+// experts 112, 82.  The forward
 // adds p to per-lane sums over the block's tokens, joined at the end over the
 // wave's tokens and the block's waves in a fixed order, and counts the block's ids
 // with LDS atomics (integers: their order does not show).  Up to kBalOneBlock tokens
@@ -19,12 +20,14 @@
 // numbers added in fp32 are rounded the same way each time (2^22 tokens of 3 experts: 11 u off).  A wave's sum
 // and a block's are rounded to fp32 where they are handed on, which adds u each.
 // Partial sums in global atomics would be one launch fewer and another result with
-// each run.  256 tokens of 128 experts take 9.2 us in one launch and 7.7 in two, whose
-// second costs the host 4; 512 tokens 14.8 against 7.6.
+// each run.  256 tokens of 128 experts take 10.1 us in one launch and 8.4 in two, whose
+// second costs the host 4; 128 tokens 7.0 and 8.3.  The limit is on tokens alone and was set there: with
+// more experts two launches win earlier (256 tokens of 256 experts 15.1 and 11.7, of 512 29.8 and 14.6, of
+// 1024 46.8 and 20.1; 128 tokens of 512 16.6 and 14.6).
 //
-// Bound by launches up to some 16384 x 128 (9.8 us forward, 6.7 backward), by memory from
-// 65536 x 256 on: 65536 x 512 (134 MB) 33.9 forward, 4 TB/s read, and 48.5 backward, 5.5 TB/s
-// read and written.
+// Bound by launches up to some 16384 x 128 (10.5 us forward, 6.7 backward).  65536 x 512 (134 MB): forward 36.5,
+// 3.7 TB/s read, bound by the loads in flight (a workgroup a CU, a token ahead a wave; 1024 experts,
+// with twice the bytes ahead, 56.6 and 4.7); backward 48.5, 5.5 TB/s read and written, by memory.
 #include <type_traits>
 
 #include "moe_args.h"

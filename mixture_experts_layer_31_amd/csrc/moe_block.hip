@@ -399,9 +399,9 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
 // Large products with bf16 results: 256 x 128 tiles of eight waves, 64 x 64 each, or, where those
 // are too few, 128 x 128 (96 x 128) tiles of two groups of four waves, 64 x 64 (48 x 64) each, that
 // share the runs and are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
-// 16384 x 4096 x 4096: 490 us, 1.12 PFLOP/s, 2048 x 2048 x 8192: 63 us, 1.08 (a library's bf16 product on
-// values of the same sizes 425 us, 1.29 PFLOP/s).  Bound by the matrix instructions at the clock that the power
-// allows: without the widening, or without the promotion, the same product takes 489 to 504 us.  256 x 256
+// 16384 x 4096 x 4096: 490 us, 1.12 PFLOP/s, with tile scales 547; 4096 x 4096 x 4096 124 and 138 (a library's
+// bf16 product on values 425 and 95).  Bound by the matrix instructions at the clock that the power
+// allows: without the widening, or without the promotion, the same product takes as long.  256 x 256
 // tiles took 476, and 637 with tile scales: their sums and operands do not fit the registers.
 template <int MB_, int WGM_, int WGN_, int KG_>
 struct LargeTile {
@@ -759,7 +759,7 @@ int launch_mm_large(const MmArgs& a, bool b_tile, hipStream_t s) {
 // waves in 16 x 16 blocks, KG such groups a workgroup that share the runs of the contraction and
 // are joined at the end.  Where tiles or steps are few, a step's latency is what it costs: a
 // ring of four stages is filled four steps ahead, a step's fragments are read one step before
-// their products, and a product's sums are promoted one step behind it (256 x 4096 x 4096 bf16 12.7 us, fp32 17.7).
+// their products, and a product's sums are promoted one step behind it (256 x 4096 x 4096 16.7 us, fp32 17).
 template <int BM_, int BN_, int WGM_, int WGN_, int KG_>
 struct MidTile {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, KG = KG_;
@@ -1037,8 +1037,8 @@ int launch_mm_mid(const MmArgs& a, bool b_tile, bool f32, hipStream_t s) {
 // fragment holds row l & 15 and bytes 32 (l >> 4) .. + 31 of a run, for A and B alike; with B as
 // the first operand a lane's results are row l & 15 of C and columns 4 (l >> 4) .. + 3.
 // Every workgroup of a row of tiles quantises its A again, which costs less than a second launch
-// up to the size in use_direct.  1 x 4096 x 2048 from bf16: 4.6 us in a graph, 8.4 MB of codes, of it 3 a
-// launch's; 33 x 1000 x 1363 from fp32: 7.6, of it 2 the quotients.
+// up to the size in use_direct.  1 x 4096 x 2048 from bf16: 4.8 us in a graph, 8.4 MB of codes, of it 3 a
+// launch's; 33 x 1000 x 1363 from fp32: 7.7, of it 2 the quotients.
 enum AKind { A_CODES = 0, A_BF16 = 1, A_F32 = 2 };
 constexpr int kDirectWaves = 16, kDirectK = 4096;
 
@@ -1264,9 +1264,10 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 //   64 x 64, two a CU     2   + 0.8  steps  (2048 x 1024 x 2048 16.1)
 //   64 x 64, two groups   3   + 0.45 steps  (1024 x 1024 x 2048 10)
 // The sizes' best is the least of these.  Where a few rows past a multiple of 256 cost a further round, they
-// go to a launch of 64 x 64 tiles.
+// go to a launch of 64 x 64 tiles (8197 x 2048 x 1536: 64.4, in one launch 75.9; 4128 x 4096 x 2048: 79.3, 93.4).
 // With too few tiles for the chip the contraction is cut into parts, whose sums take a second launch:
-// 4 us and their bytes at 3 TB/s, written and read.
+// 4 us and their bytes at 3 TB/s, written and read (256 x 256 x 16384 13.0, whole 50; 512 x 512 x 8192 15.2, whole
+// 27.3; 64 x 64 x 16384 10.6, whole 50).
 enum MmKind { MM_LARGE, MM_128, MM_96, MM_64, MM_64X2 };
 struct MmPlan {
   MmKind kind;
@@ -1349,12 +1350,12 @@ int launch_mm(const MmArgs& a, const MmPlan& plan, bool b_tile, bool f32, float*
 }
 
 // Whether the one-launch kernel takes the product: for values, up to the work of quantising A again
-// in every workgroup (in runs of 128 values: 64 x 1024 x 1024, 32768 runs, takes 5.8 us against 7.1
-// in two launches, 128 x 1024 x 1024, 65536, 7.9 against 7.2 and a launch's host time, 16 x 4096 x 4096, 131072,
-// 13.9 against 12.1); for codes, up to 4096 runs of tiles (128 x 1024 x 1024: 4.5 us against 4.9; 256 x
-// 1024 x 1024: 7.6 against 5.0), and with one row of tiles up to 16384 (16 x 4096 x 4096: 7.3 against 9.8),
-// as long as a wave has four runs at most (16 x 512 x 8192: 11.1 against 8.3 in parts and a launch's
-// host time; 16 x 512 x 16384: 19.5 against 9.8).
+// in every workgroup (in runs of 128 values: 64 x 1024 x 1024, 32768 runs, takes 6.1 us against 8.9
+// in two launches, 128 x 1024 x 1024, 65536, 8.3 against 8.9, 16 x 4096 x 4096, 131072, 14.6 against
+// 12.2); for codes, up to 4096 runs of tiles (128 x 1024 x 1024: 4.6 us against 6.5; 256 x
+// 1024 x 1024: 7.9 against 6.6), and with one row of tiles up to 16384 (16 x 4096 x 4096: 7.5 against 10.0),
+// as long as a wave has four runs at most (16 x 512 x 8192: 10.9 against 9.1 in parts and a launch's
+// host time; 16 x 512 x 16384: 18.3 against 10.9).
 bool use_direct(long long M, long long N, long long K, bool values) {
   const long long steps = ceil_div(K, 128), tm = ceil_div(M, 16), tn = ceil_div(N, 16);
   if (!values) return steps <= 4 * kDirectWaves && tm * tn * steps <= (M <= 16 ? 16384 : 4096);

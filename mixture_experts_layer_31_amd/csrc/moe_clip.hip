@@ -17,7 +17,7 @@
 // of 1.2 GB took 264 us, so 241), and a workgroup's sum goes to its own slot: the
 // result does not depend on the order in which they run.
 //
-// Lists past kStreamChunks go by with nontemporal loads and stores (1.2 GB: norm 241 -> 187
+// Launches past kStreamChunks (of up to kMaxList tensors each) go by with nontemporal loads and stores (1.2 GB: norm 241 -> 187
 // us, 6.5 TB/s; clip 429 -> 417 us, 5.8 TB/s); below, the clip finds part of the list in the
 // memory-side cache (256 MB), which they would cost it (104 MB: 58 us for both calls, 64
 // nontemporal).  Loading the end of a long list plainly and clipping from there lost
