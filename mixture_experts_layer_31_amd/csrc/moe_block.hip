@@ -362,19 +362,28 @@ __device__ __forceinline__ int take_part(MmArgs& p, int l) {
 }
 
 // A scale as m 2^e: the power goes into the operand when its codes are widened, which costs nothing
-// (the conversion takes the exponent of `power`), and m stays for the promotion.  The product of two
-// scales may lie far outside fp32's range where the result does not.  With 2^e in [2^-50, 2^66] widened
-// codes and their products' sums are normal numbers or 0 unless the result is past the range, and
-// the product of two m (each below 2^62, and from 2^-99 on) is finite, and subnormal only where the
-// run adds less than 2^-200.
+// (the conversion takes the exponent of `power`), and m stays for the promotion.  The product of two scales
+// may lie far outside fp32's range where the result does not.  With 2^e in [2^-50, 2^51] no sum of a
+// run's products passes 2^127 or is below 2^-118 unless it is 0.  m is in [1, 2) but for scales past that
+// range: below 2^-50 it is smaller, from 2^52 on larger, and then the other scale's power (or the result's
+// own range) leaves room for it, so that a run's sum times A's m and then B's m is infinite or subnormal
+// only where the run's result is.
 struct Scale {
   float power, m;
   __device__ __forceinline__ Scale() = default;
   __device__ __forceinline__ explicit Scale(float s) {
-    power = __builtin_amdgcn_fmed3f(fabsf(s), 0x1p-50f, 0x1p66f);
+    power = __builtin_amdgcn_fmed3f(fabsf(s), 0x1p-50f, 0x1p51f);
     m = s * __uint_as_float(0x7f000000u - (__float_as_uint(power) & 0x7f800000u));
   }
 };
+
+// Both m of a run at once, where B has one for all columns (16384 x 4096 x 4096: 495 us, 539 with a
+// multiplication more for each value).  Two finite ones past the range count as its end: a sum of 0 stays 0, another one is
+// past the range by its power alone.
+__device__ __forceinline__ float both(float a, float b) {
+  const float p = a * b, end = copysignf(3.402823466e38f, p);
+  return isinf(p) && !isinf(a) && !isinf(b) ? end : p;
+}
 
 // Eight of the fragment's codes, times the power of two in `power`, as bf16 (exact): the part s of its 32.
 __device__ __forceinline__ bf16x8 widen(const i32x8& f, int s, float power) {
@@ -504,7 +513,7 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
   i32x8 rb[2];        // the last pair of B, widened during the step's first products, and its scales
   float rs2[2];
   SB_ sbv[NS] = {};
-  float sav = 0.f, sp = 0.f;  // m of the current block of A and of the one before it
+  float sav = 0.f, sp = 0.f;  // m of the current block of A; of the one promoted last, with block scales times B's
   f32x4 R[2] = {};    // run sums of the last pair
   auto widen_all = [&](const i32x8& f, float scale, bf16x8 (&w)[4]) __attribute__((always_inline)) {
     const Scale s(scale);
@@ -528,12 +537,11 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
       for (int j = 0; j < 2; ++j)
         q[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j0 + j][e], wa[e], e ? q[j] : f32x4{}, 0, 0, 0);
   };
-  auto promote = [&](int i, int j, const f32x4& part, float sr_) __attribute__((always_inline)) {
+  auto promote = [&](int i, int j, const f32x4& part, float m) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float sc;
-      if constexpr (B_TILE) sc = sr_ * sbv[j][e]; else sc = sr_ * sbv[0];
-      acc[i][j][e] = __builtin_fmaf(part[e], sc, acc[i][j][e]);
+      if constexpr (B_TILE) acc[i][j][e] = __builtin_fmaf(part[e] * m, sbv[j][e], acc[i][j][e]);
+      else acc[i][j][e] = __builtin_fmaf(part[e], m, acc[i][j][e]);
     }
   };
   // Block i of stage st; `next` is what follows: 0 its next block, 1 the first one of stage sn, 2 nothing
@@ -583,9 +591,9 @@ __global__ void __launch_bounds__(TL::THREADS, 2) block_mm_large_kernel(MmArgs p
     loads(2);
     products(2, R);
     loads(3);
+    if constexpr (B_TILE) sp = sav; else sp = both(sav, sbv[0]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) promote(i, j, Q[j], sav);
-    sp = sav;
+    for (int j = 0; j < 2; ++j) promote(i, j, Q[j], sp);
     if constexpr (NEXT < 2) sav = widen_all(an, san, wa);
     if constexpr (NEXT == 1) {
 #pragma unroll
@@ -851,9 +859,8 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
   auto promote = [&](int i, int j) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float s;
-      if constexpr (B_TILE) s = psa[i] * psb[j][e]; else s = psa[i] * psb[j];
-      acc[i][j][e] = __builtin_fmaf(P[i][j][e], s, acc[i][j][e]);
+      if constexpr (B_TILE) acc[i][j][e] = __builtin_fmaf(P[i][j][e] * psa[i], psb[j][e], acc[i][j][e]);
+      else acc[i][j][e] = __builtin_fmaf(P[i][j][e], psa[i], acc[i][j][e]);
     }
   };
   auto promote_all = [&]() __attribute__((always_inline)) {
@@ -883,15 +890,15 @@ __global__ void __launch_bounds__(TL::THREADS) block_mm_mid_kernel(MmArgs p) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < MB; ++i) psa[i] = ra[i].m;
+    for (int i = 0; i < MB; ++i) {
+      // the tile is in one block of B
+      if constexpr (B_TILE) psa[i] = ra[i].m; else psa[i] = both(ra[i].m, Scale(x.sb[0]).m);
+    }
+    if constexpr (B_TILE) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      if constexpr (B_TILE) {
+      for (int j = 0; j < NB; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) psb[j][e] = Scale(x.sb[j][e]).m;
-      } else {
-        psb[j] = Scale(x.sb[j]).m;
-      }
     }
   };
   const int n = (p.ksteps + KG - 1) / KG;  // steps a group
@@ -1172,7 +1179,10 @@ __global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectA
     for (int e = 0; e < 4; ++e)
       part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(b, e, rb.power), widen(a, e, ra.power), part, 0, 0, 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e], ra.m * Scale(cur.sb[B_TILE ? e : 0]).m, acc[e]);
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (B_TILE) acc[e] = __builtin_fmaf(part[e] * ra.m, Scale(cur.sb[e]).m, acc[e]);
+      else acc[e] = __builtin_fmaf(part[e], both(ra.m, rb.m), acc[e]);
+    }
     cur = next;
   }
   using O = typename std::conditional<OUT_F32, float, uint16_t>::type;

@@ -137,3 +137,34 @@ def test_values_and_weights_of_any_size(t):
             va = q8.e4m3_decode(xq.cpu().numpy()[:, :K]) * _wide(xs.cpu().numpy().T, K, 1)
             vb = q8.e4m3_decode(wq.cpu().numpy()[:, :K]) * _wide(_wide(ws.cpu().numpy(), N, 0), K, 1)
             _check(c, va, vb, K, F32, "values")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 300), (2000, 900, 300), (700, 256, 520), (1500, 1900, 300), (2040, 2000, 520),
+                                   (2890, 2900, 300)])
+@pytest.mark.parametrize("b_scale", [TILE, BLOCK])
+def test_large_products_that_cancel(M, N, K, b_scale):
+    """A run's products may pass fp32's range once scaled where their sum does not: 448^2 and -448^2 beside
+    terms of 1, which leave their number, under scales whose product is up to 2^119 (448^2 2^119 = 2^136)."""
+    kb, ld = (K + 127) // 128, (K + 15) // 16 * 16
+    av, bv = np.ones((M, K)), np.ones((N, K))
+    av[:, ::16], bv[:, ::16] = 448, 448
+    av[:, 1::16], bv[:, 1::16] = 448, -448
+    if K % 16 == 1:
+        av[:, K - 1] = bv[:, K - 1] = 1
+    pad = lambda c: np.pad(q8.e4m3_encode(c), ((0, 0), (0, ld - K)))  # noqa: E731
+    for ea, eb in ((60, 59), (119, -3), (110, 9), (-20, 119), (100, -140), (52, 51)):
+        sa = np.full((kb, M), 2.0 ** ea, np.float32)
+        sb = np.full((kb, N) if b_scale == TILE else ((N + 127) // 128, kb), 2.0 ** eb, np.float32)
+        ref = np.float64((av[:1] @ bv[:1].T).item()) * 2.0 ** (ea + eb)
+        assert ref < 2.0 ** 128
+        for ct in (BF, F32):
+            print(f"[case] cancel {M}x{N}x{K} 2^{ea} 2^{eb} b_scale={b_scale} c={ct}", flush=True)
+            c = torch.full((M, N), np.nan, dtype=DT[ct], device="cuda")
+            d = moe.make_block_mm_desc(M, N, K, b_scale=b_scale, c_type=ct)
+            scratch = torch.full((max(1, moe.moe_block_mm_scratch_bytes(d)),), 0xA5, dtype=torch.uint8, device="cuda")
+            dev = [torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in (pad(av), sa, pad(bv), sb)]
+            assert moe.moe_block_mm(d, *dev, c, scratch) == moe.MOE_OK
+            torch.cuda.synchronize()
+            # every partial sum is a whole number below 2^24 times a power of two: exact but for the result's rounding
+            got = c.cpu().double().numpy()
+            assert np.all(np.abs(got - ref) <= (2.0 ** -8 if ct == BF else U) * ref), (got.min(), got.max(), ref)
