@@ -20,7 +20,7 @@
 // twice that rate and is not used: it adds eight products at a time, each cut at 13 bits below
 // the largest one's leading bit (beside products of +-2^16 one of 2^3 survives and one of 2^2
 // does not), so where large terms cancel the rest of the sum is lost.  Its results are 1.5e-5 off on normal
-// data, and 16384 x 4096 x 4096 took 232 us with it against 490.
+// data, and 16384 x 4096 x 4096 took 232 us with it against 495.
 #include <type_traits>
 
 #include "moe_args.h"
@@ -408,7 +408,7 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds, int voff) {
 // Large products with bf16 results: 256 x 128 tiles of eight waves, 64 x 64 each, or, where those
 // are too few, 128 x 128 (96 x 128) tiles of two groups of four waves, 64 x 64 (48 x 64) each, that
 // share the runs and are joined at the end.  Two stages of a run each; a wave goes over its rows of 16 x 16 blocks.
-// 16384 x 4096 x 4096: 490 us, 1.12 PFLOP/s, with tile scales 547; 4096 x 4096 x 4096 124 and 138 (a library's
+// 16384 x 4096 x 4096: 495 us, 1.11 PFLOP/s, with tile scales 552; 4096 x 4096 x 4096 121 and 140 (a library's
 // bf16 product on values 425 and 95).  Bound by the matrix instructions at the clock that the power
 // allows: without the widening, or without the promotion, the same product takes as long.  256 x 256
 // tiles took 476, and 637 with tile scales: their sums and operands do not fit the registers.
@@ -1264,7 +1264,7 @@ __global__ void __launch_bounds__(256) block_zero_kernel(T* C, int64_t ldc, int 
 
 // Which kernel a product takes.  Measured on an MI355X (256 CUs, one workgroup of 256 x 128 or 128 x
 // 128, or two of 64 x 64, a CU), in us a round of workgroups with `steps` runs:
-//   256 x 128             5.5 + 1.75 steps  (4096 x 4096 x 4096 122 in two rounds, 8192 x 2048 x 1536 52)
+//   256 x 128             5.5 + 1.75 steps  (4096 x 4096 x 4096 121 in two rounds, 8192 x 2048 x 1536 53)
 //   128 x 128             6   + 0.92 steps  (2048 x 2048 x 2048 20.8, 2048 x 2048 x 8192 63 to 73)
 //   96 x 128              5.3 + 0.76 steps  (1536 x 2048 x 2048 17.1, 1536 x 2048 x 8192 54.5)
 //   64 x 64, two a CU     3.9 + 0.73 steps  (2048 x 1024 x 2048 15.4, 2048 x 1024 x 8192 51)
