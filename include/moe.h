@@ -370,9 +370,69 @@ int moe_balance_bwd(const moe_desc* d, const float* logits, const uint8_t* valid
                     const int32_t* counts, const float* dlosses, const int32_t* topk_idx,
                     const float* topk_w, const float* dtopk_w, float* dlogits, void* stream);
 
-/* Element types and scale layouts of the block-scaled calls below. */
+/* Element types and scale layouts of the calls below. */
 enum moe_type { MOE_TYPE_F32 = 0, MOE_TYPE_BF16 = 1, MOE_TYPE_E4M3 = 2 };
 enum moe_scale { MOE_SCALE_TILE = 0, MOE_SCALE_BLOCK = 1 };
+
+/* Gate: the router's choice by scores of either kind with a bias for balance and groups
+ * of experts, beside moe_router_fwd's plain softmax (the routing decision that the layer
+ * consumes: Prime Mega MoE news item, "Why is MoE training communication-bound?", each
+ * token goes to a small subset of experts).  Per token, with logits z[0..E-1]:
+ *   s = sigmoid(z), or softmax(z) (0 for a row of only -inf);
+ *   c_e = s_e + bias_e, computed in 64 bits and rounded to fp32: what the choice
+ *   goes by.  An expert whose z is -inf or whose c is NaN or -inf has c = -FLT_MAX (the
+ *   lowest choice);
+ *   with top_groups < groups, a group (E / groups experts in a row) scores the fp32
+ *   sum of its group_best largest c (of its one, where it has one), and only the experts of the top_groups
+ *   best groups (ties to the lower group) can be chosen;
+ *   topk_idx: the K largest c in descending order, ties to the lower expert;
+ *   topk_w[t,k] = scale s_k, or with MOE_GATE_RENORM scale s_k / sum_k' s_k' (0 where
+ *   that sum is 0), of the scores without the bias.
+ * A +inf or NaN logit gives its scores as the formulas do (ids stay distinct and in range). */
+enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+#define MOE_GATE_RENORM 0x1     /* weights of a token sum to scale */
+#define MOE_GATE_ACCUMULATE 0x2 /* moe_gate_bwd adds to dlogits (in_type MOE_TYPE_F32 only) */
+
+typedef struct moe_gate_desc {
+  int32_t T, E, K;
+  int32_t groups, top_groups; /* 1, 1: no groups */
+  int32_t group_best;         /* 1 or 2 */
+  int32_t score;              /* enum moe_score */
+  int32_t in_type;            /* logits and dlogits: MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  int32_t flags;              /* MOE_GATE_* */
+  float scale;                /* finite */
+  int64_t ld_logits, ld_dlogits; /* elements between rows, >= E */
+} moe_gate_desc;
+
+/* Requires T >= 0, T*K < 2^31, groups >= 1 with E % groups == 0, 1 <= top_groups <= groups, 1 <= K
+ * <= top_groups (E / groups), and the values above (else MOE_EINVAL); E <= 1024, K <= 64,
+ * groups <= 64, T < 2^26 and row strides below 2^40 (else MOE_EUNSUPPORTED).  logits: device [T, E] of in_type, aligned to
+ * its element; bias: device float32 [E] or NULL (0); topk_idx: device int32 [T, K]
+ * and topk_w: device float32 [T, K], written (the layout moe_fwd reads); 4-byte
+ * aligned (MOE_EALIGN).  T = 0 is MOE_OK and touches nothing.  Asynchronous on
+ * `stream`; allocates nothing. */
+int moe_gate_fwd(const moe_gate_desc* d, const void* logits, const float* bias,
+                 int32_t* topk_idx, float* topk_w, void* stream);
+
+/* dlogits = dL/dlogits for the upstream gradient dtopk_w = dL/dtopk_w [T, K] (moe_bwd's)
+ * with topk_idx fixed (moe_gate_fwd's): the bias and the groups do not enter.  With
+ * a_k = scale dtopk_w_k and v_k = s_k / sum s (MOE_GATE_RENORM), A = sum_k v_k a_k:
+ *   sigmoid:  dz_k = s_k (1 - s_k) a_k, or renormalised v_k (1 - s_k) (a_k - A);
+ *   softmax:  dz_j = s_j (a_j [j chosen] - sum_k s_k a_k), or renormalised v_k (a_k - A)
+ * and 0 elsewhere.  An id outside [0, E) takes no part; one that a token holds twice gets both
+ * slots' gradients.  dlogits: device [T, E] of in_type, every entry written (its rows'
+ * padding is left as it was), apart from every input (MOE_EINVAL); after
+ * moe_balance_bwd, MOE_GATE_ACCUMULATE adds to that gradient.  The sums are fp32 or wider, rounded once.  Other
+ * requirements as moe_gate_fwd. */
+int moe_gate_bwd(const moe_gate_desc* d, const void* logits, const int32_t* topk_idx,
+                 const float* dtopk_w, void* dlogits, void* stream);
+
+/* Moves the bias towards balance: bias[e] += step where counts[e] is below the mean of
+ * counts[0..E-1], -= step where it is above, and stays where they are equal (compared as
+ * integers).  counts: device int32 [E], not negative (moe_balance_fwd's, or moe_routing_view's;
+ * summed over the ranks of a job); bias: device float32 [E], apart from counts.
+ * E >= 1, step finite (MOE_EINVAL); 4-byte aligned (MOE_EALIGN). */
+int moe_gate_bias(int32_t E, const int32_t* counts, float step, float* bias, void* stream);
 
 /* Dense e4m3 operands with one fp32 scale for each block of 128: the layer's
  * blockwise FP8 recipe (Prime Mega MoE news item, "How does the fused kernel
@@ -453,6 +513,53 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
                  const uint8_t* b, const float* b_scales, void* c, void* scratch,
                  size_t scratch_bytes, void* stream);
 
+/* What lies between two blocks: the end of one (its output b, normed and gated, added to the
+ * residual) and the norm ahead of the next, in one pass.  Per row t of D values:
+ *   u = b, or with w_post  b / sqrt(mean(b^2) + eps) * w_post;
+ *   h = r + scale u, or with gate  r + scale sigmoid(gate_t) u, rounded to fp32 and
+ *   then to res_type (exact before that rounding but for some 2^-50 of its terms);
+ *   y = h / sqrt(mean(h^2) + eps) * w of the h that is stored, in fp32, rounded once.
+ * b may be NULL (then gate and w_post are too, h = r and `h` may be NULL: a norm by
+ * itself), and so may w and y together (the residual sum by itself; then b is not). */
+typedef struct moe_norm_desc {
+  int32_t T, D;
+  int32_t io_type;  /* b, y and their gradients: MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  int32_t res_type; /* r, h and their gradients: the same two */
+  int32_t w_type;   /* w and w_post: the same two */
+  float eps, scale; /* eps >= 0; both finite */
+  int64_t ld_b, ld_r, ld_h, ld_y; /* elements between the rows of b and db, of r and dr, of h and dh, of y and dy */
+} moe_norm_desc;
+
+/* b, r, h, y: device [T, D]; gate: device float32 [T] or NULL; w, w_post: device [D]
+ * (w_post or NULL); all aligned to their element (MOE_EALIGN).  h may be r (with ld_h =
+ * ld_r); no other written buffer may overlap another buffer (MOE_EINVAL, as are null pointers but for those
+ * above, T < 0, D < 1, bad types and row strides below D).  D <= 16384 and strides below
+ * 2^40 (MOE_EUNSUPPORTED).  Padding of rows is left as it was.  T = 0 is MOE_OK and touches nothing.
+ * Asynchronous on `stream`; allocates nothing. */
+int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const float* gate,
+                 const void* w_post, const void* w, void* h, void* y, void* stream);
+
+/* The whole backward from dy = dL/dy and dh = dL/dh (what reaches h besides y; either may
+ * be NULL: 0), with the forward's b, h (r where b was NULL), gate and weights:
+ *   e = w dy, q = 1 / sqrt(mean(h^2) + eps), g = dh + q (e - h q^2 mean(e h));
+ *   dr = g;  dw = sum_t dy h q;
+ *   f = scale g, or scale sigmoid(gate_t) g;  dgate_t = (1 - sigmoid(gate_t)) sum(f u);
+ *   db = f, or with w_post  p (w_post f - b p^2 mean(w_post f b)), p = 1 / sqrt(mean(b^2) + eps);
+ *   dw_post = sum_t f b p.
+ * dr: device [T, D] of res_type, may be dh (with ld_r = ld_h); db: [T, D] of io_type (NULL with b NULL);
+ * dgate: float32 [T], NULL exactly where gate is; dw, dw_post: float32 [D], NULL exactly
+ * where w, w_post are.  With w NULL dy is NULL.  b is read only with gate or w_post (else it may be NULL where
+ * db is not); h only with w.  Row sums are fp32; sums over rows are 64 bits wide over a workgroup's rows and over the
+ * workgroups, rounded to fp32 between the two and at the end, in an order that
+ * depends on the sizes alone.  scratch: device, 16-byte aligned, of
+ * moe_norm_scratch_bytes(d) (MOE_ESCRATCH), used only during the call.  With T = 0 dw and
+ * dw_post are written 0.  Other requirements as moe_norm_fwd. */
+size_t moe_norm_scratch_bytes(const moe_norm_desc* d);
+int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const float* gate,
+                 const void* w_post, const void* w, const void* dy, const void* dh, void* db,
+                 void* dr, float* dgate, float* dw_post, float* dw, void* scratch,
+                 size_t scratch_bytes, void* stream);
+
 /* One gradient of a list: n elements at src (device, aligned to its element),
  * and where moe_grad_clip writes them, dst (src itself, or memory that no src
  * and no other dst of the list overlaps).  moe_grad_norm does not use dst. */
@@ -488,6 +595,54 @@ int moe_grad_norm(const moe_grad* g, int32_t count, float* norm, void* scratch,
  * norm inside a dst, are MOE_EINVAL.  Other requirements as moe_grad_norm. */
 int moe_grad_clip(const moe_grad* g, int32_t count, const float* norm, float max_norm,
                   void* stream);
+
+/* One tensor of an optimizer step: n elements of each buffer, all device memory. */
+typedef struct moe_adamw_param {
+  void* param;        /* param_type; updated */
+  float* master;      /* or NULL; with param_type MOE_TYPE_BF16: what param is rounded from */
+  const void* grad;   /* grad_type */
+  void* m;            /* first moment: float32, or e4m3 codes */
+  void* v;            /* second moment: float32, or e4m3 codes of its square root */
+  float* m_scale;     /* [ceil(n / 128)] with codes, else NULL */
+  float* v_scale;
+  int64_t n;
+  int32_t param_type, grad_type; /* MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  float weight_decay; /* finite */
+  int32_t reserved;   /* 0 */
+} moe_adamw_param;
+
+typedef struct moe_adamw_desc {
+  double beta1, beta2; /* in [0, 1) */
+  double eps;          /* >= 0, finite */
+  int32_t state_type;  /* MOE_TYPE_F32 or MOE_TYPE_E4M3 */
+  int32_t reserved;    /* 0 */
+} moe_adamw_desc;
+
+/* One AdamW step over a list of tensors, what follows moe_grad_norm in a training step:
+ *   g = grad c;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   p = p (1 - lr decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps),
+ * with p the master where there is one (param is then its rounding), else param, and c = 1
+ * without `norm`, min(1, max_norm / norm[0]) with it: moe_grad_clip folded in, without
+ * its pass over the gradients (max_norm >= 0 and finite, else MOE_EINVAL).  A norm that is
+ * not finite, or a step below 1, leaves every buffer as it was.  m and v are computed
+ * in 64 bits and rounded to fp32; p is computed from those in fp32 and rounded once to its type.
+ * With state_type MOE_TYPE_E4M3 the states are kept as codes of runs of 128 elements
+ * from the tensor's first, with moe_block_quant's scales and codes (scale = amax / 448, 1
+ * where that is 0; code = e4m3 of the fp32 quotient): m, and sqrt(v), whose code is at least 1 (2^-9) where
+ * v > 0, so that no update divides by eps alone where a gradient has been seen; p
+ * is computed from m and v as they are before that.  All zeros is the state before the first step
+ * (scales too: 0 stands for itself).  lr: device float32 [1]; step: device int32
+ * [1], this step's number, 1 for the first (both are read on the GPU when the call runs, so a
+ * captured graph follows them; the call does not advance it); norm: device float32 [1] or NULL.
+ * `p` is a host array of `count` entries, read during the call only.
+ * param, grad aligned to their element, fp32 states and scales 4-byte, codes 16-byte,
+ * lr, step and norm 4-byte (MOE_EALIGN).  MOE_EINVAL for null pointers (an entry with n = 0 may have
+ * them), count < 0, n < 0, bad types, a master beside an fp32 param, scales beside fp32 states,
+ * reserved != 0, beta, eps or weight_decay out of range, and a buffer that the call writes
+ * overlapping another of the list's (a tensor that is listed twice) or lr, step or norm; MOE_EUNSUPPORTED for n >= 2^34.
+ * Asynchronous on `stream`; allocates no device memory. */
+int moe_adamw(const moe_adamw_desc* d, const moe_adamw_param* p, int32_t count, const float* lr,
+              const int32_t* step, const float* norm, float max_norm, void* stream);
 
 /* Synchronizes `stream`, returns the latched device error (MOE_OK, MOE_EINDEX
  * or MOE_ETIMEOUT) of `scratch` and clears it.  Error reporting of this

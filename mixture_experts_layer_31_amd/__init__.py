@@ -5,8 +5,8 @@ libmoe_mi355x.so built in-tree by ``mixture_experts_layer_31_amd.build``.  The
 functions below carry the C names; tensors are torch tensors on the GPU (or
 None for optional pointers) and `stream` defaults to torch's current stream.
 Loading fails loudly when the library has not been built: there is no fallback.
-The calls of the operators beside the layer (moe_balance_*, moe_block_*, moe_grad_*)
-also look at their tensors: one of another type, device or stride than the call takes,
+The calls of the operators beside the layer (moe_balance_*, moe_gate_*, moe_block_*,
+moe_norm_*, moe_grad_*, moe_adamw) also look at their tensors: one of another type, device or stride than the call takes,
 or with too few elements, is MOE_EINVAL.
 """
 from __future__ import annotations
@@ -33,20 +33,29 @@ MOE_NOALLOC_SCRATCH_BYTES = 256 << 20
 MOE_TYPE_F32, MOE_TYPE_BF16, MOE_TYPE_E4M3 = range(3)
 MOE_SCALE_TILE, MOE_SCALE_BLOCK = range(2)
 MOE_MM_ACCUMULATE = 0x1
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = range(2)
+MOE_GATE_RENORM, MOE_GATE_ACCUMULATE = 0x1, 0x2
 
 # Exported symbols, in the order include/moe.h declares them.
 EXPORTS = (
     "moe_scratch_bytes", "moe_wprep_bytes", "moe_prepare_weights", "moe_route",
     "moe_routing_view", "moe_scratch_view", "moe_fwd", "moe_bwd", "moe_fwd_noalloc", "moe_router_fwd",
-    "moe_router_bwd", "moe_balance_scratch_bytes", "moe_balance_fwd", "moe_balance_bwd", "moe_block_quant",
-    "moe_block_mm_scratch_bytes", "moe_block_mm", "moe_grad_scratch_bytes", "moe_grad_norm", "moe_grad_clip",
-    "moe_check", "moe_strerror", "moe_abi_version", "moe_profile_enable", "moe_profile_collect",
+    "moe_router_bwd", "moe_balance_scratch_bytes", "moe_balance_fwd", "moe_balance_bwd", "moe_gate_fwd", "moe_gate_bwd",
+    "moe_gate_bias", "moe_block_quant", "moe_block_mm_scratch_bytes", "moe_block_mm", "moe_norm_fwd",
+    "moe_norm_scratch_bytes", "moe_norm_bwd", "moe_grad_scratch_bytes", "moe_grad_norm", "moe_grad_clip",
+    "moe_adamw", "moe_check", "moe_strerror", "moe_abi_version", "moe_profile_enable", "moe_profile_collect",
     "moe_profile_get", "moe_profile_reset",
 )
 
 
 class moe_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "F", "E", "K", "mode", "flags")]
+
+
+class moe_gate_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "K", "groups", "top_groups", "group_best", "score", "in_type",
+                                              "flags")] + \
+               [("scale", ctypes.c_float)] + [(n, ctypes.c_int64) for n in ("ld_logits", "ld_dlogits")]
 
 
 class moe_block_quant_desc(ctypes.Structure):
@@ -59,9 +68,26 @@ class moe_block_mm_desc(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("lda", "ldb", "ldc")]
 
 
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "io_type", "res_type", "w_type")] + \
+               [(n, ctypes.c_float) for n in ("eps", "scale")] + \
+               [(n, ctypes.c_int64) for n in ("ld_b", "ld_r", "ld_h", "ld_y")]
+
+
 class moe_grad(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_param(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+               [("n", ctypes.c_int64), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("beta1", "beta2", "eps")] + \
+               [("state_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -97,12 +123,20 @@ def lib() -> ctypes.CDLL:
             "moe_balance_scratch_bytes": (_sz, [_dp]),
             "moe_balance_fwd": (_i32, [_dp] + [_vp] * 7 + [_sz, _vp]),
             "moe_balance_bwd": (_i32, [_dp] + [_vp] * 9),
+            "moe_gate_fwd": (_i32, [ctypes.POINTER(moe_gate_desc)] + [_vp] * 5),
+            "moe_gate_bwd": (_i32, [ctypes.POINTER(moe_gate_desc)] + [_vp] * 5),
+            "moe_gate_bias": (_i32, [_i32, _vp, ctypes.c_float, _vp, _vp]),
             "moe_block_quant": (_i32, [ctypes.POINTER(moe_block_quant_desc)] + [_vp] * 6),
             "moe_block_mm_scratch_bytes": (_sz, [ctypes.POINTER(moe_block_mm_desc)]),
             "moe_block_mm": (_i32, [ctypes.POINTER(moe_block_mm_desc)] + [_vp] * 6 + [_sz, _vp]),
+            "moe_norm_fwd": (_i32, [ctypes.POINTER(moe_norm_desc)] + [_vp] * 8),
+            "moe_norm_scratch_bytes": (_sz, [ctypes.POINTER(moe_norm_desc)]),
+            "moe_norm_bwd": (_i32, [ctypes.POINTER(moe_norm_desc)] + [_vp] * 13 + [_sz, _vp]),
             "moe_grad_scratch_bytes": (_sz, [_i32]),
             "moe_grad_norm": (_i32, [ctypes.POINTER(moe_grad), _i32, _vp, _vp, _sz, _vp]),
             "moe_grad_clip": (_i32, [ctypes.POINTER(moe_grad), _i32, _vp, ctypes.c_float, _vp]),
+            "moe_adamw": (_i32, [ctypes.POINTER(moe_adamw_desc), ctypes.POINTER(moe_adamw_param), _i32] + [_vp] * 3
+                          + [ctypes.c_float, _vp]),
             "moe_check": (_i32, [_dp, _vp, _sz, _vp]),
             "moe_strerror": (ctypes.c_char_p, [_i32]),
             "moe_abi_version": (_i32, []),
@@ -256,6 +290,52 @@ def moe_balance_bwd(desc, logits, valid, counts, dlosses, topk_idx, topk_w, dtop
     return lib().moe_balance_bwd(ctypes.byref(desc), *at, raw(dev) if stream is None else _stream(stream))
 
 
+def make_gate_desc(T, E, K, score=MOE_SCORE_SIGMOID, groups=1, top_groups=1, group_best=2, in_type=MOE_TYPE_F32,
+                   flags=MOE_GATE_RENORM, scale=1.0, ld_logits=None, ld_dlogits=None) -> moe_gate_desc:
+    """Row strides default to the experts."""
+    return moe_gate_desc(T, E, K, groups, top_groups, group_best, score, in_type, flags, scale,
+                         E if ld_logits is None else ld_logits, E if ld_dlogits is None else ld_dlogits)
+
+
+def moe_gate_fwd(desc, logits, bias, topk_idx, topk_w, stream=None) -> int:
+    T, E, K = desc.T, desc.E, desc.K
+    device, raw, f32, i32, _, _, io = _look or _lookups()
+    dev = device()
+    if not _rows_fit(logits, T, E, desc.ld_logits):
+        return MOE_EINVAL
+    at = _addresses(dev, (logits, io.get(desc.in_type, ()), None), (bias, f32, E), (topk_idx, i32, T * K),
+                    (topk_w, f32, T * K))
+    if at is None:
+        return MOE_EINVAL
+    return lib().moe_gate_fwd(ctypes.byref(desc), *at, raw(dev) if stream is None else _stream(stream))
+
+
+def moe_gate_bwd(desc, logits, topk_idx, dtopk_w, dlogits, stream=None) -> int:
+    T, E, K = desc.T, desc.E, desc.K
+    device, raw, f32, i32, _, _, io = _look or _lookups()
+    dev = device()
+    if not (_rows_fit(logits, T, E, desc.ld_logits) and _rows_fit(dlogits, T, E, desc.ld_dlogits)):
+        return MOE_EINVAL
+    t = io.get(desc.in_type, ())
+    at = _addresses(dev, (logits, t, None), (topk_idx, i32, T * K), (dtopk_w, f32, T * K), (dlogits, t, None))
+    if at is None:
+        return MOE_EINVAL
+    return lib().moe_gate_bwd(ctypes.byref(desc), *at, raw(dev) if stream is None else _stream(stream))
+
+
+def moe_gate_bias(counts, step: float, bias, stream=None) -> int:
+    """One step of the bias [E]; counts [E] or longer (moe_balance_fwd's [E + 1])."""
+    device, raw, f32, i32, *_ = _look or _lookups()
+    dev = device()
+    if bias is None:
+        return MOE_EINVAL
+    E = bias.numel()
+    at = _addresses(dev, (counts, i32, E), (bias, f32, E))
+    if at is None:
+        return MOE_EINVAL
+    return lib().moe_gate_bias(E, at[0], step, at[1], raw(dev) if stream is None else _stream(stream))
+
+
 def _code_ld(n: int) -> int:
     return (n + 15) // 16 * 16
 
@@ -317,6 +397,48 @@ def moe_block_mm(desc, a, a_scales, b, b_scales, c, scratch=None, stream=None) -
                               raw(dev) if stream is None else _stream(stream))
 
 
+def make_norm_desc(T, D, io_type=MOE_TYPE_BF16, res_type=MOE_TYPE_BF16, w_type=MOE_TYPE_F32, eps=1e-6, scale=1.0,
+                   ld_b=None, ld_r=None, ld_h=None, ld_y=None) -> moe_norm_desc:
+    """Row strides default to the columns."""
+    return moe_norm_desc(T, D, io_type, res_type, w_type, eps, scale, *[D if v is None else v
+                                                                       for v in (ld_b, ld_r, ld_h, ld_y)])
+
+
+def moe_norm_fwd(desc, b, r, gate, w_post, w, h, y, stream=None) -> int:
+    T, D = desc.T, desc.D
+    device, raw, f32, _, _, _, types = _look or _lookups()
+    dev = device()
+    if not (_rows_fit(b, T, D, desc.ld_b) and _rows_fit(r, T, D, desc.ld_r) and _rows_fit(h, T, D, desc.ld_h)
+            and _rows_fit(y, T, D, desc.ld_y)):
+        return MOE_EINVAL
+    io, res, wt = types.get(desc.io_type, ()), types.get(desc.res_type, ()), types.get(desc.w_type, ())
+    at = _addresses(dev, (b, io, None), (r, res, None), (gate, f32, T), (w_post, wt, D), (w, wt, D), (h, res, None),
+                    (y, io, None))
+    if at is None:
+        return MOE_EINVAL
+    return lib().moe_norm_fwd(ctypes.byref(desc), *at, raw(dev) if stream is None else _stream(stream))
+
+
+def moe_norm_scratch_bytes(desc: moe_norm_desc) -> int:
+    return lib().moe_norm_scratch_bytes(ctypes.byref(desc))
+
+
+def moe_norm_bwd(desc, b, h, gate, w_post, w, dy, dh, db, dr, dgate, dw_post, dw, scratch, stream=None) -> int:
+    T, D = desc.T, desc.D
+    device, raw, f32, _, _, _, types = _look or _lookups()
+    dev = device()
+    if not (_rows_fit(b, T, D, desc.ld_b) and _rows_fit(h, T, D, desc.ld_h) and _rows_fit(dy, T, D, desc.ld_y)
+            and _rows_fit(dh, T, D, desc.ld_h) and _rows_fit(db, T, D, desc.ld_b) and _rows_fit(dr, T, D, desc.ld_r)):
+        return MOE_EINVAL
+    io, res, wt = types.get(desc.io_type, ()), types.get(desc.res_type, ()), types.get(desc.w_type, ())
+    at = _addresses(dev, (b, io, None), (h, res, None), (gate, f32, T), (w_post, wt, D), (w, wt, D), (dy, io, None),
+                    (dh, res, None), (db, io, None), (dr, res, None), (dgate, f32, T), (dw_post, f32, D), (dw, f32, D))
+    if at is None:
+        return MOE_EINVAL
+    return lib().moe_norm_bwd(ctypes.byref(desc), *at, *_scratch(scratch, dev),
+                              raw(dev) if stream is None else _stream(stream))
+
+
 def make_grad_list(src, dst=None):
     """The moe_grad array of contiguous GPU tensors (float32 or bfloat16) and of where their clipped
     values go (default: in place).  It holds addresses: keep the tensors alive, and make it anew when
@@ -359,6 +481,56 @@ def moe_grad_clip(grads, norm, max_norm: float, stream=None) -> int:
     if at is None or getattr(grads, "device", dev) not in (dev, None):
         return MOE_EINVAL
     return lib().moe_grad_clip(grads, len(grads), *at, max_norm, raw(dev) if stream is None else _stream(stream))
+
+
+def make_adamw_desc(beta1=0.9, beta2=0.95, eps=1e-8, state_type=MOE_TYPE_F32) -> moe_adamw_desc:
+    return moe_adamw_desc(beta1, beta2, eps, state_type, 0)
+
+
+def make_adamw_list(params, grads, m, v, masters=None, m_scales=None, v_scales=None, weight_decay=0.0):
+    """The moe_adamw_param array of contiguous GPU tensors: params and grads float32 or bfloat16, the states
+    float32, or uint8 or float8_e4m3fn codes with float32 scales ([ceil(n / 128)] each), masters float32 or None
+    each, weight_decay a number or one a tensor.  It holds addresses: keep the tensors alive, and make it
+    anew when they move.  The call refuses it with another GPU current than the tensors'."""
+    import torch
+    types = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
+    params, count = list(params), len(params)
+    e4m3 = m_scales is not None
+    lists = [list(x) if x is not None else [None] * count for x in (masters, grads, m, v, m_scales, v_scales)]
+    decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    if any(len(x) != count for x in (*lists, decay)) or (v_scales is not None) != e4m3:
+        raise ValueError("as many of each as parameters; scales for both states or for none")
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    rows = []
+    for p, w, g, a, b, sa, sb, wd in zip(params, *lists, decay):
+        n = p.numel()
+        if p.dtype not in types or g.dtype not in types or g.numel() != n:
+            raise ValueError("parameters and gradients are float32 or bfloat16, of one length")
+        if w is not None and (p.dtype != torch.bfloat16 or w.dtype != torch.float32 or w.numel() != n):
+            raise ValueError("a master is float32, beside a bfloat16 parameter of its length")
+        if any(x.numel() < n or x.dtype not in (codes if e4m3 else (torch.float32,)) for x in (a, b)):
+            raise ValueError("states have an element for each of the parameter's, float32 or codes")
+        if e4m3 and any(x.dtype != torch.float32 or x.numel() < (n + 127) // 128 for x in (sa, sb)):
+            raise ValueError("codes have a float32 scale for each 128")
+        own = [x for x in (p, w, g, a, b, sa, sb) if x is not None]
+        if not all(x.is_cuda and x.device == params[0].device and x.is_contiguous() for x in own):
+            raise ValueError("contiguous tensors on one GPU")
+        rows.append(moe_adamw_param(*[_p(x) for x in (p, w, g, a, b, sa, sb)], n, types[p.dtype], types[g.dtype], wd, 0))
+    out = (moe_adamw_param * count)(*rows)
+    out.device = params[0].get_device() if params else None
+    out.state_type = MOE_TYPE_E4M3 if e4m3 else MOE_TYPE_F32
+    return out
+
+
+def moe_adamw(desc, params, lr, step, norm=None, max_norm: float = 0.0, stream=None) -> int:
+    device, raw, f32, i32, *_ = _look or _lookups()
+    dev = device()
+    at = _addresses(dev, (lr, f32, 1), (step, i32, 1), (norm, f32, 1))
+    if at is None or getattr(params, "device", dev) not in (dev, None) or \
+            getattr(params, "state_type", desc.state_type) != desc.state_type:
+        return MOE_EINVAL
+    return lib().moe_adamw(ctypes.byref(desc), params, len(params), *at, max_norm,
+                           raw(dev) if stream is None else _stream(stream))
 
 
 def moe_routing_view(desc, scratch) -> tuple:

@@ -1,0 +1,354 @@
+"""AdamW on the GPU (through the C ABI) against the float64 oracle, step by step from the states that are stored.
+
+Tolerances, u = 2^-24:
+* m, v in fp32: computed in 64 bits, rounded once: u relative, 2^-45 of their terms' sizes for the 64-bit sums' sake;
+* p: 1 - lr decay rounds by 2 u, the update (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps) lr by m, v and its root,
+  its factor, eps and their sum, the quotient, lr's factor and the product u each (v's halves): 10 u; then u for the sum, and half a step
+  of the type (2^-8 in bf16): 2 u |p| + 10 u |update| + (u + half) |p'|;
+* codes and scales are equal to those of the oracle's moments in fp32: both sides round the same 64-bit numbers, so
+  that they differ with a chance of some 2^-28 an element.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_31_amd as moe
+from oracle import adamw_oracle as ao
+
+pytestmark = pytest.mark.gpu
+U, TINY = 2.0 ** -24, 2.0 ** -140
+F, B = torch.float32, torch.bfloat16
+BETA, EPS = (0.9, 0.95), 1e-8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    moe.lib()
+
+
+class Param:
+    """A tensor with everything that belongs to it, each in a buffer with neighbours."""
+
+    def __init__(self, g, n, t=F, gt=F, master=False, codes=False, off=0, decay=0.0, fresh=False, gstd=None):
+        self.n, self.decay, self.codes, self.bufs = n, decay, codes, []
+        gstd = 2.0 ** float(torch.randint(-12, 2, (1,), generator=g)) if gstd is None else gstd
+
+        def put(x, t, off):
+            buf = torch.full((n_of(x) + off + 20,), 55, dtype=t, device="cuda") if t != torch.uint8 else \
+                torch.full((n_of(x) + off + 20,), 0x55, dtype=t, device="cuda")
+            buf[off:off + n_of(x)] = torch.as_tensor(x).to(t).cuda() if t != torch.uint8 else torch.from_numpy(x).cuda()
+            self.bufs.append((buf, off, n_of(x)))
+            return buf[off:off + n_of(x)]
+
+        def n_of(x):
+            return len(x)
+
+        p = torch.randn(n, generator=g) * 0.1
+        self.master = put(p, F, off % 3) if master else None
+        self.p = put(p, t, off)
+        self.g = put(torch.randn(n, generator=g) * gstd, gt, (off + 1) % 8)
+        m = torch.zeros(n) if fresh else torch.randn(n, generator=g) * gstd * 0.3
+        s = torch.zeros(n) if fresh else torch.rand(n, generator=g) * gstd + 0.1 * gstd
+        if codes:
+            (cm, sm), (cv, sv) = ao.encode(m.numpy()), ao.encode(s.numpy(), least=True)
+            if fresh:
+                sm, sv = sm * 0, sv * 0
+            self.m, self.v = put(cm, torch.uint8, 0), put(cv, torch.uint8, 0)
+            self.ms, self.vs = put(torch.from_numpy(sm), F, off % 5), put(torch.from_numpy(sv), F, off % 2)
+        else:
+            self.m, self.v, self.ms, self.vs = put(m, F, off % 5), put(s * s, F, off % 7), None, None
+
+    def new_gradient(self, g, std):
+        self.g.copy_(torch.randn(self.n, generator=g) * std)
+
+    def values(self):
+        """(p, g, m, v) in float64 as they are stored."""
+        f = lambda t: t.double().cpu().numpy()  # noqa: E731
+        p = f(self.p if self.master is None else self.master)
+        if self.codes:
+            m = ao.decode(self.m.cpu().numpy(), self.ms.cpu().numpy())
+            v = ao.decode(self.v.cpu().numpy(), self.vs.cpu().numpy()) ** 2
+        else:
+            m, v = f(self.m), f(self.v)
+        return p, f(self.g), m, v
+
+    def check(self, before, lr, t, norm=None, max_norm=0.0, beta=BETA, eps=EPS):
+        p0, g0, m0, v0 = before
+        p, m, v = ao.step(p0, g0, m0, v0, lr, t, *beta, eps, self.decay, norm, max_norm)
+        done = t >= 1 and (norm is None or np.isfinite(norm))
+        update = p - p0 * (1 - lr * self.decay) if done else np.zeros_like(p)
+        f = lambda t: t.double().cpu().numpy()  # noqa: E731
+        bound = 2 * U * np.abs(p0) + 10 * U * np.abs(update) + U * np.abs(p) + TINY
+        if self.master is not None:
+            w = f(self.master)
+            assert np.all(np.abs(w - p) <= bound)
+            assert torch.equal(self.p, self.master.to(self.p.dtype))
+        else:
+            half = 2.0 ** -8 if self.p.dtype == B else 0.0
+            assert np.all(np.abs(f(self.p) - p) <= bound * (1 + half) + half * np.abs(p))
+        if self.codes:
+            if done:
+                cm, sm = ao.encode(m.astype(np.float32))
+                cv, sv = ao.encode(np.sqrt(v.astype(np.float32)), least=True)
+                assert np.array_equal(self.ms.cpu().numpy(), sm) and np.array_equal(self.vs.cpu().numpy(), sv)
+                assert np.array_equal(self.m.cpu().numpy(), cm) and np.array_equal(self.v.cpu().numpy(), cv)
+        else:
+            assert np.all(np.abs(f(self.m) - m) <= U * np.abs(m) + 2.0 ** -45 * (np.abs(m0) + np.abs(g0)) + TINY)
+            assert np.all(np.abs(f(self.v) - v) <= U * np.abs(v) + 2.0 ** -45 * (np.abs(v0) + g0 * g0) + TINY)
+        for buf, off, n in self.bufs:
+            edge = 0x55 if buf.dtype == torch.uint8 else 55
+            assert (buf[:off] == edge).all() and (buf[off + n:] == edge).all()
+
+
+def _list(ps):
+    codes = ps[0].codes if ps else False
+    pick = lambda k: [getattr(p, k) for p in ps]  # noqa: E731
+    return moe.make_adamw_list(pick("p"), pick("g"), pick("m"), pick("v"), masters=pick("master"),
+                               m_scales=pick("ms") if codes else None, v_scales=pick("vs") if codes else None,
+                               weight_decay=pick("decay"))
+
+
+def _scalars(lr, t, norm=None):
+    return (torch.tensor([lr], device="cuda"), torch.tensor([t], dtype=torch.int32, device="cuda"),
+            None if norm is None else torch.tensor([norm], device="cuda"))
+
+
+def _run(ps, lr=1e-2, t=3, norm=None, max_norm=0.0, beta=BETA, eps=EPS, name=""):
+    print(f"[case] adamw {name} {len(ps)} tensors, {sum(p.n for p in ps)} values, codes={ps[0].codes} t={t} norm={norm}", flush=True)
+    codes = ps[0].codes
+    d = moe.make_adamw_desc(*beta, eps, moe.MOE_TYPE_E4M3 if codes else moe.MOE_TYPE_F32)
+    before = [p.values() for p in ps]
+    lrt, tt, nt = _scalars(lr, t, norm)
+    assert moe.moe_adamw(d, _list(ps), lrt, tt, nt, max_norm) == moe.MOE_OK
+    torch.cuda.synchronize()
+    for p, b in zip(ps, before):
+        p.check(b, float(np.float32(lr)), t, None if norm is None else float(np.float32(norm)), max_norm, beta, eps)
+
+
+KINDS = [(F, F, False), (B, B, False), (B, B, True), (F, B, False), (B, F, False), (B, F, True)]
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("t,gt,master", KINDS)
+def test_lengths_and_alignments(t, gt, master, codes):
+    g = torch.Generator().manual_seed(1)
+    for off in range(9):
+        _run([Param(g, n, t, gt, master, codes, off, 0.1) for n in (1, 2, 3, 5, 7, 8, 9, 16, 17, 127, 128, 129, 300)], name="short")
+    _run([Param(g, n, t, gt, master, codes, off, 0.1) for n, off in ((2047, 0), (2048, 1), (2049, 0), (4096, 3), (10007, 2))],
+         name="chunks")
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_mixed_lists(codes):
+    rng, g = np.random.default_rng(2), torch.Generator().manual_seed(2)
+    for count in (1, 7, 45, 46, 47, 100):
+        ps = [Param(g, int(np.exp(rng.uniform(0, 8))), *KINDS[int(rng.integers(6))], codes, int(rng.integers(9)),
+                    float(rng.random() < 0.5) * 0.1) for _ in range(count)]
+        ps.insert(count // 2, Param(g, 0, codes=codes))
+        _run(ps, name="mixed")
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_steps_from_nothing(codes):
+    """Five steps from states of zeros, each from what the one before left."""
+    g = torch.Generator().manual_seed(3)
+    ps = [Param(g, n, t, gt, master, codes, 1, 0.05, fresh=True) for (t, gt, master), n in zip(KINDS, (700, 129, 3000, 64, 1, 1000))]
+    ps[2].g[5::2] = 0  # some that see no gradient
+    for t in range(1, 6):
+        _run(ps, t=t, name="step")
+        for p in ps[:2]:
+            p.new_gradient(g, 0.1 * t)
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_steps_rates_and_clipping(codes):
+    g = torch.Generator().manual_seed(4)
+    new = lambda: [Param(g, 900, B, B, True, codes, 0, 0.1), Param(g, 333, F, F, False, codes, 1, 0.0)]  # noqa: E731
+    for t in (1, 2, 10, 1000, 100000, 2 ** 31 - 1):
+        _run(new(), t=t, name="step number")
+    for lr in (0.0, 1e-6, 1.0):
+        _run(new(), lr=lr, name="rate")
+    for norm, top in ((0.5, 1.0), (1.0, 1.0), (4.0, 1.0), (1e30, 1.0), (3.0, 0.0), (0.0, 1.0)):
+        _run(new(), norm=norm, max_norm=top, name="clipped")
+    for beta in ((0.0, 0.0), (0.0, 0.999), (0.9, 0.0), (0.99, 0.9999)):
+        _run(new(), beta=beta, name="betas")
+    _run(new(), eps=0.1, name="eps")
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_steps_that_change_nothing(codes):
+    g = torch.Generator().manual_seed(5)
+    for t, norm in ((0, None), (-5, None), (3, float("inf")), (3, float("nan"))):
+        ps = [Param(g, 500, B, B, True, codes, 1, 0.1), Param(g, 77, F, F, False, codes, 0, 0.1)]
+        old = [b.clone() for p in ps for b, _, _ in p.bufs]
+        _run(ps, t=t, norm=norm, max_norm=1.0, name="nothing")
+        assert all(torch.equal(a, b) for a, b in zip(old, [b for p in ps for b, _, _ in p.bufs]))
+
+
+def test_clipping_equals_the_clipped_gradients():
+    """The norm of a list, then a step with it, against the gradients clipped by a call of their own (whose rounding
+    to bf16 and fp32 is what differs)."""
+    g = torch.Generator().manual_seed(6)
+    ps = [Param(g, 5000, F, F, False, False, 0, 0.1, gstd=1.0), Param(g, 777, F, F, False, False, 1, 0.0, gstd=1.0)]
+    norm = torch.zeros(1, device="cuda")
+    grads = moe.make_grad_list([p.g for p in ps])
+    scratch = torch.zeros(moe.moe_grad_scratch_bytes(2), dtype=torch.uint8, device="cuda")
+    moe.check(moe.moe_grad_norm(grads, norm, scratch))
+    before = [p.values() for p in ps]
+    lr, t, _ = _scalars(1e-2, 3)
+    moe.check(moe.moe_adamw(moe.make_adamw_desc(), _list(ps), lr, t, norm, 2.0))
+    torch.cuda.synchronize()
+    for p, b in zip(ps, before):
+        p.check(b, float(np.float32(1e-2)), 3, float(norm), 2.0)
+
+
+def test_values_at_the_ends_of_fp32():
+    for codes in (False, True):
+        for std in (1e-38, 1e-22, 1e-19, 1e15, 1e18):
+            g = torch.Generator().manual_seed(7)
+            p = Param(g, 600, F, F, False, codes, 0, 0.0, gstd=std)
+            lr, t, _ = _scalars(1e-2, 3)
+            d = moe.make_adamw_desc(state_type=moe.MOE_TYPE_E4M3 if codes else moe.MOE_TYPE_F32)
+            before = p.values()
+            moe.check(moe.moe_adamw(d, _list([p]), lr, t))
+            torch.cuda.synchronize()
+            assert torch.isfinite(p.p).all(), std
+            if codes:  # the codes are those of the formats' definition here too
+                _, m, v = ao.step(*before, float(np.float32(1e-2)), 3, *BETA, EPS, 0.0)
+                cm, sm = ao.encode(m.astype(np.float32))
+                assert np.array_equal(p.ms.cpu().numpy(), sm) and np.array_equal(p.m.cpu().numpy(), cm), std
+                cv, sv = ao.encode(np.sqrt(v.astype(np.float32)), least=True)
+                assert np.array_equal(p.vs.cpu().numpy(), sv) and np.array_equal(p.v.cpu().numpy(), cv), std
+
+
+def test_a_value_that_is_none_stays_in_its_place():
+    for codes in (False, True):
+        g = torch.Generator().manual_seed(8)
+        p = Param(g, 400, F, F, False, codes, 0, 0.1)
+        p.g[200] = np.nan
+        lr, t, _ = _scalars(1e-2, 3)
+        moe.check(moe.moe_adamw(moe.make_adamw_desc(state_type=moe.MOE_TYPE_E4M3 if codes else moe.MOE_TYPE_F32), _list([p]), lr, t))
+        torch.cuda.synchronize()
+        assert torch.isnan(p.p[200]) and torch.isfinite(p.p[:200]).all() and torch.isfinite(p.p[201:]).all()
+        if codes:
+            assert int(p.m[200]) & 0x7F == 0x7F and torch.isfinite(p.ms).all() and torch.isfinite(p.vs).all()
+
+
+def test_a_small_second_moment_keeps_a_code():
+    """A run with one large gradient: the others' roots lie below half the smallest code, which they keep."""
+    g = torch.Generator().manual_seed(9)
+    p = Param(g, 128, F, F, False, True, 0, 0.0, fresh=True)
+    p.g.fill_(1e-6)
+    p.g[3], p.g[4] = 1e3, 0.0
+    _run([p], t=1, name="small")
+    codes = p.v.cpu().numpy()
+    assert codes[3] == 0x7E and codes[4] == 0 and (np.delete(codes, [3, 4]) == 1).all()
+
+
+def test_empty_list():
+    lr, t, _ = _scalars(1e-2, 1)
+    assert moe.moe_adamw(moe.make_adamw_desc(), moe.make_adamw_list([], [], [], []), lr, t) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("codes", [False, True])
+def test_same_bits_streams_and_graph(codes):
+    """Two lists on two streams at once, then a captured step whose number and rate move on, replayed between eager
+    steps, against the same steps one by one."""
+    def make(seed):
+        g = torch.Generator().manual_seed(seed)
+        ps = [Param(g, 40000, B, B, True, codes, 1, 0.1), Param(g, 513, F, F, False, codes, 3, 0.0), Param(g, 20000, B, B, False, codes, 0, 0.1)]
+        return ps, _list(ps)
+
+    d = moe.make_adamw_desc(state_type=moe.MOE_TYPE_E4M3 if codes else moe.MOE_TYPE_F32)
+    state = lambda ps: [b.clone() for p in ps for b, _, _ in p.bufs]  # noqa: E731
+    steps = 6
+
+    def reference(seed):
+        ps, lst = make(seed)
+        for t in range(1, steps + 1):
+            lr, tt, nt = _scalars(1e-2 / t, t, 2.0)
+            moe.check(moe.moe_adamw(d, lst, lr, tt, nt, 1.0))
+        torch.cuda.synchronize()
+        return state(ps)
+
+    want = [reference(1), reference(2)]
+    jobs = [make(1), make(2)]
+    sides = [torch.cuda.Stream() for _ in jobs]
+    scal = [_scalars(1e-2 / t, t, 2.0) for t in range(1, steps + 1)]
+    torch.cuda.synchronize()
+    for lr, tt, nt in scal:
+        for (ps, lst), side in zip(jobs, sides):
+            with torch.cuda.stream(side):
+                moe.check(moe.moe_adamw(d, lst, lr, tt, nt, 1.0))
+    torch.cuda.synchronize()
+    for (ps, _), w in zip(jobs, want):
+        assert all(torch.equal(a, b) for a, b in zip(state(ps), w))
+
+    ps, lst = make(1)
+    lr, tt, nt = _scalars(1e-2, 1, 2.0)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        moe.check(moe.moe_adamw(d, lst, lr, tt, nt, 1.0))
+    for t in range(1, steps + 1):
+        lr.fill_(float(scal[t - 1][0]))
+        tt.fill_(t)
+        if t % 3 == 0:
+            moe.check(moe.moe_adamw(d, lst, lr, tt, nt, 1.0))
+        else:
+            g.replay()
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(state(ps), want[0]))
+
+
+def test_list_refuses_what_does_not_fit():
+    z = lambda n=256, t=F, dev="cuda": torch.zeros(n, dtype=t, device=dev)  # noqa: E731
+    u8 = torch.uint8
+    good = dict(params=[z()], grads=[z()], m=[z()], v=[z()])
+    moe.make_adamw_list(**good)
+    for k, bad in (("params", z(dev="cpu")), ("params", z(t=torch.float16)), ("grads", z(255)), ("grads", z(dev="cpu")), ("m", z(255)),
+                   ("m", z(t=B)), ("v", z(512)[::2]), ("v", z(t=u8)), ("params", z(512)[::2])):
+        with pytest.raises(ValueError):
+            moe.make_adamw_list(**{**good, k: [bad]})
+    with pytest.raises(ValueError):
+        moe.make_adamw_list(**good, masters=[z()])  # beside an fp32 parameter
+    coded = dict(params=[z(t=B)], grads=[z(t=B)], m=[z(t=u8)], v=[z(t=u8)], m_scales=[z(2)], v_scales=[z(2)])
+    lst = moe.make_adamw_list(**coded)
+    for k, bad in (("m_scales", z(1)), ("v_scales", z(2, t=B)), ("m", z())):
+        with pytest.raises(ValueError):
+            moe.make_adamw_list(**{**coded, k: [bad]})
+    lr, t, nt = _scalars(1e-2, 1, 1.0)
+    e4m3 = moe.make_adamw_desc(state_type=moe.MOE_TYPE_E4M3)
+    assert moe.moe_adamw(e4m3, lst, lr, t) == moe.MOE_OK
+    assert moe.moe_adamw(moe.make_adamw_desc(), lst, lr, t) == moe.MOE_EINVAL  # codes as fp32 states
+    for args in ((lr.cpu(), t, None), (lr, t.long(), None), (lr.double(), t, None), (lr, t, nt.cpu()), (lr, None, None)):
+        assert moe.moe_adamw(e4m3, lst, *args, 1.0) == moe.MOE_EINVAL
+    lst.device = 1
+    assert moe.moe_adamw(e4m3, lst, lr, t) == moe.MOE_EINVAL
+    p = z()
+    with_itself = moe.make_adamw_list([p, p], [z(), z()], [z(), z()], [z(), z()])
+    assert moe.moe_adamw(moe.make_adamw_desc(), with_itself, lr, t) == moe.MOE_EINVAL
+    one = moe.make_adamw_list(**good)
+    assert moe.moe_adamw(moe.make_adamw_desc(), one, good["params"][0], t) == moe.MOE_EINVAL  # the rate inside a parameter
+
+
+def test_offsets_past_2_31_elements():
+    n = 2 ** 31 + 1003
+    print(f"[case] adamw large n={n}", flush=True)
+    p, g = torch.full((n,), 0.5, dtype=B, device="cuda"), torch.full((n,), 0.25, dtype=B, device="cuda")
+    m, v = torch.zeros(n, dtype=torch.uint8, device="cuda"), torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ms, vs = torch.zeros((n + 127) // 128, device="cuda"), torch.zeros((n + 127) // 128, device="cuda")
+    g[-1000:] = -0.25
+    lr, t, _ = _scalars(0.125, 1)
+    moe.check(moe.moe_adamw(moe.make_adamw_desc(state_type=moe.MOE_TYPE_E4M3),
+                            moe.make_adamw_list([p], [g], [m], [v], m_scales=[ms], v_scales=[vs]), lr, t))
+    torch.cuda.synchronize()
+    # the first step moves by lr: 0.375, and 0.625 at the end (to a step of bf16)
+    assert (p[:-1000].float() - 0.375).abs().max() <= 2.0 ** -9 and (p[-1000:].float() - 0.625).abs().max() <= 2.0 ** -8
+    assert bool((m[:-1000] == 0x7E).all()) and bool((m[-1000:] == 0xFE).all()) and bool((v == 0x7E).all())
+    assert torch.allclose(ms, torch.full_like(ms, 0.1 * 0.25 / 448), rtol=1e-6)
+    assert torch.allclose(vs, torch.full_like(vs, 0.05 ** 0.5 * 0.25 / 448), rtol=1e-6)
