@@ -624,11 +624,14 @@ typedef struct moe_adamw_desc {
  * with p the master where there is one (param is then its rounding), else param, and c = 1
  * without `norm`, min(1, max_norm / norm[0]) with it: moe_grad_clip folded in, without
  * its pass over the gradients (max_norm >= 0 and finite, else MOE_EINVAL).  A norm that is
- * not finite, or a step below 1, leaves every buffer as it was.  m and v are computed
- * in 64 bits and rounded to fp32; p is computed from those in fp32 and rounded once to its type.
+ * not finite, or a step below 1, leaves every buffer as it was.  c, g, m and v are computed in fp32, with
+ * beta and 1 - beta rounded to fp32 and each quotient, product and sum rounded (no fused multiply-adds): m =
+ * (beta1 m) + ((1 - beta1) g), v = (beta2 v) + ((1 - beta2) (g g)).  p is computed from those in fp32 and
+ * rounded once to its type.
  * With state_type MOE_TYPE_E4M3 the states are kept as codes of runs of 128 elements
  * from the tensor's first, with moe_block_quant's scales and codes (scale = amax / 448, 1
- * where that is 0; code = e4m3 of the fp32 quotient): m, and sqrt(v), whose code is at least 1 (2^-9) where
+ * where that is 0; code = e4m3 of the fp32 quotient; a value is code * scale rounded to fp32): m, and
+ * sqrt(v), whose code is at least 1 (2^-9) where
  * v > 0, so that no update divides by eps alone where a gradient has been seen; p
  * is computed from m and v as they are before that.  All zeros is the state before the first step
  * (scales too: 0 stands for itself).  lr: device float32 [1]; step: device int32

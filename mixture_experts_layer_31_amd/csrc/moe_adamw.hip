@@ -2,20 +2,17 @@
 // run of 128 (moe_adamw in moe.h).
 //
 // Bound by memory: a bf16 parameter with its master, an fp32 state and a bf16 gradient
-// move 28 bytes an element, a bf16 parameter with e4m3 states 10.  The moments are
-// computed in 64 bits and rounded once to fp32 (the vector ALU takes 64-bit multiply-adds at
-// the rate of 32-bit ones), so that a code next to a border does not depend on an order
-// of roundings.
+// move 28 bytes an element, a bf16 parameter with e4m3 states 10.
 //
 // The list travels in the kernel arguments (kMaxAdam entries a launch), so nothing is
 // copied to the device and a captured graph holds its own list.  A tensor is cut into chunks
-// of kChunk elements from its first, eight neighbouring ones a thread, so that sixteen lanes
-// hold a run: its largest value is four lane moves away.  Loads take 16 bytes at any
-// element's address.  The step's coefficients are computed by every thread for itself: a launch
+// of kChunk elements from its first.  With codes a thread has eight neighbouring elements, so that sixteen
+// lanes hold a run: its largest value is four lane moves away.  Loads take 16 bytes at any element's address.  The step's coefficients are computed by every thread for itself: a launch
 // to compute them once costs more.
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "moe_args.h"
 #include "moe_fp8_codec.h"
@@ -26,8 +23,14 @@ namespace {
 constexpr int kMaxAdam = 46;  // entries a launch
 constexpr int kAdamThreads = 256;
 constexpr int kChunk = 8 * kAdamThreads;
-constexpr int kMaxAdamBlocks = 4096;
-constexpr uint64_t kStreamBytes = 256ull << 20;  // what the memory-side cache holds
+constexpr uint32_t kMaxAdamBlocks = (1u << 24) - 1;  // HIP counts a launch's threads in 32 bits
+// Lists past this go by with nontemporal loads and stores: 2.1 GB of fp32 states 425 -> 398 us, 6 GB with codes 1464 ->
+// 1334 (either alone gains nothing), 300 MB in two launches 111 -> 106; below, the gradients and the parameters may be
+// in the memory-side cache (256 MB) for this call and the next forward.
+constexpr uint64_t kStreamBytes = 64ull << 20;
+// With codes a workgroup takes two chunks of such a list (6 GB: 1054 -> 1016 us; four 1073): its coefficients
+// cost a tenth of a chunk's instructions.  With fp32 states one (359 us; two 368), and never a few workgroups that
+// step through the list (4096: 1334 and 398 us), which drift apart.
 
 struct AdamList {
   void* param[kMaxAdam];
@@ -45,33 +48,53 @@ struct AdamList {
 struct AdamStep {
   const float *lr, *norm;
   const int32_t* step;
-  double b1, b2, log_b1, log_b2;
-  float eps, max_norm;
+  double log_b1, log_b2;
+  float b1, b2, a1, a2, eps, max_norm;
 };
 static_assert(sizeof(AdamList) + sizeof(AdamStep) <= 3584, "kernel arguments hold the list");
 
+// 1 - e^x for x <= 0: e^x by its series on half an octave, in 64 bits, for the difference from 1.
+__device__ __forceinline__ float left_over(double x) {
+  x = x > -700. ? x : -700.;
+  const double n = __builtin_rint(x * 1.4426950408889634074);  // log2(e)
+  const double r = __builtin_fma(n, -0.69314718055994530942, x);
+  double y = 1. / 39916800.;
+  y = __builtin_fma(y, r, 1. / 3628800.);
+  y = __builtin_fma(y, r, 1. / 362880.);
+  y = __builtin_fma(y, r, 1. / 40320.);
+  y = __builtin_fma(y, r, 1. / 5040.);
+  y = __builtin_fma(y, r, 1. / 720.);
+  y = __builtin_fma(y, r, 1. / 120.);
+  y = __builtin_fma(y, r, 1. / 24.);
+  y = __builtin_fma(y, r, 1. / 6.);
+  y = __builtin_fma(y, r, 0.5);
+  y = __builtin_fma(y, r, 1.);
+  y = __builtin_fma(y, r, 1.);
+  return float(1. - __builtin_ldexp(y, int(n)));
+}
+
 // The step's numbers, the same in every thread.
 struct Coef {
-  double c, b1, b2, a1, a2;  // clipping factor, betas and 1 - betas
-  float lr, rate, root, eps;  // lr, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  float c, b1, b2, a1, a2;    // clipping factor, betas and 1 - betas
+  float lr, rate, root, eps;  // lr, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   bool none;                  // nothing to do
 };
 __device__ __forceinline__ Coef coefficients(const AdamStep& s) {
   Coef k;
   const float lr = *s.lr;
   const int t = *s.step;
-  k.c = 1.;
+  k.c = 1.f;
   k.none = t < 1;
   if (s.norm != nullptr) {
     const float nm = *s.norm;
     k.none |= !(fabsf(nm) < INFINITY);
-    if (!(nm <= s.max_norm)) k.c = double(s.max_norm) / double(nm);
+    if (!(nm <= s.max_norm)) k.c = s.max_norm / nm;
   }
   k.b1 = s.b1; k.b2 = s.b2;
-  k.a1 = 1. - s.b1; k.a2 = 1. - s.b2;
+  k.a1 = s.a1; k.a2 = s.a2;
   k.lr = lr;
-  k.rate = float(double(lr) / -expm1(double(t) * s.log_b1));
-  k.root = float(1. / sqrt(-expm1(double(t) * s.log_b2)));
+  k.rate = lr / left_over(double(t) * s.log_b1);
+  k.root = 1.f / sqrtf(left_over(double(t) * s.log_b2));
   k.eps = s.eps;
   return k;
 }
@@ -87,6 +110,21 @@ __device__ __forceinline__ uint4 fetch16(const void* p) {
   }
 }
 template <bool STREAM>
+__device__ __forceinline__ uint2 fetch8(const void* p) {
+  typedef uint32_t any_u32x2 __attribute__((ext_vector_type(2), aligned(2)));
+  any_u32x2 v;
+  if constexpr (STREAM) v = __builtin_nontemporal_load(static_cast<const any_u32x2*>(p));
+  else v = *static_cast<const any_u32x2*>(p);
+  return make_uint2(v.x, v.y);
+}
+template <bool STREAM>
+__device__ __forceinline__ void keep8(void* p, const uint2& a) {
+  typedef uint32_t any_u32x2 __attribute__((ext_vector_type(2), aligned(2)));
+  const any_u32x2 v = {a.x, a.y};
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<any_u32x2*>(p));
+  else *static_cast<any_u32x2*>(p) = v;
+}
+template <bool STREAM>
 __device__ __forceinline__ void keep16(void* p, const uint4& a) {
   typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
   if constexpr (STREAM) {
@@ -97,79 +135,80 @@ __device__ __forceinline__ void keep16(void* p, const uint4& a) {
   }
 }
 
-// Eight elements from p, `n` of which are there (zeros behind them), as they are stored.
-template <class T> struct Eight;
-template <> struct Eight<float> {
-  uint4 a, b;
+// N neighbouring elements (4 or 8) from p, `n` of which are there (zeros behind them).
+template <class T, int N>
+struct Piece {
+  static constexpr int WORDS = N * int(sizeof(T)) / 4;
+  uint32_t w[WORDS];
   template <bool STREAM>
-  __device__ __forceinline__ void get(const float* p, int n) {
-    if (n >= 8) {
-      a = fetch16<STREAM>(p);
-      b = fetch16<STREAM>(p + 4);
-    } else {
-      uint32_t w[8];
+  __device__ __forceinline__ void get(const T* p, int n) {
+    if (n >= N) {
+      if constexpr (WORDS == 2) {
+        const uint2 v = fetch8<STREAM>(p);
+        w[0] = v.x; w[1] = v.y;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
-      a = make_uint4(w[0], w[1], w[2], w[3]);
-      b = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-  }
-  template <bool STREAM>
-  static __device__ __forceinline__ void put(float* p, int n, const float (&f)[8]) {
-    if (n >= 8) {
-      keep16<STREAM>(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-      keep16<STREAM>(p + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+        for (int k = 0; k < WORDS / 4; ++k) {
+          const uint4 v = fetch16<STREAM>(p + k * 16 / sizeof(T));
+          w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+        }
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = f[i];
+      for (int k = 0; k < WORDS; ++k) w[k] = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < n) {
+          if constexpr (sizeof(T) == 2) w[i / 2] |= uint32_t(p[i]) << (16 * (i & 1));
+          else w[i] = __float_as_uint(p[i]);
+        }
     }
   }
-};
-template <> struct Eight<uint16_t> {
-  uint4 a;
-  template <bool STREAM>
-  __device__ __forceinline__ void get(const uint16_t* p, int n) {
-    if (n >= 8) {
-      a = fetch16<STREAM>(p);
+  __device__ __forceinline__ void values(float (&f)[N]) const {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
     } else {
-      uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) w[i / 2] |= uint32_t(p[i]) << (16 * (i & 1));
-      a = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  __device__ __forceinline__ void values(float (&f)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      for (int k = 0; k < WORDS; ++k) f[k] = __uint_as_float(w[k]);
     }
   }
   template <bool STREAM>
-  static __device__ __forceinline__ void put(uint16_t* p, int n, const float (&f)[8]) {
-    if (n >= 8) {
-      keep16<STREAM>(p, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                   pack_bf16x2(f[6], f[7])));
+  static __device__ __forceinline__ void put(T* p, int n, const float (&f)[N]) {
+    uint32_t o[WORDS];
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) {
+      if constexpr (sizeof(T) == 2) o[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+      else o[k] = __float_as_uint(f[k]);
+    }
+    if (n >= N) {
+      if constexpr (WORDS == 2) {
+        keep8<STREAM>(p, make_uint2(o[0], o[1]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < WORDS / 4; ++k)
+          keep16<STREAM>(p + k * 16 / sizeof(T), make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = uint16_t(pack_bf16x2(f[i], 0.f));
+      for (int i = 0; i < N; ++i)
+        if (i < n) {
+          if constexpr (sizeof(T) == 2) p[i] = uint16_t(o[i / 2] >> (16 * (i & 1)));
+          else p[i] = f[i];
+        }
     }
   }
 };
 // Eight e4m3 codes.
 struct Codes {
   uint2 a;
+  template <bool STREAM>
   __device__ __forceinline__ void get(const uint8_t* p, int n) {
     if (n >= 8) {
-      a = *reinterpret_cast<const uint2*>(p);
+      a = fetch8<STREAM>(p);
     } else {
       uint32_t w[2] = {0, 0};
 #pragma unroll
@@ -186,9 +225,10 @@ struct Codes {
       f[4 * k] = lo[0]; f[4 * k + 1] = lo[1]; f[4 * k + 2] = hi[0]; f[4 * k + 3] = hi[1];
     }
   }
+  template <bool STREAM>
   static __device__ __forceinline__ void put(uint8_t* p, int n, const uint2& c) {
     if (n >= 8) {
-      *reinterpret_cast<uint2*>(p) = c;
+      keep8<STREAM>(p, c);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -197,104 +237,148 @@ struct Codes {
   }
 };
 
-// Codes of a run's eight values in each of its sixteen lanes; LEAST: what is positive has a
-// positive code.  Returns the scale.
-template <bool LEAST>
+// The moments, each product and sum rounded to fp32 (no fused multiply-add: the codes of the next
+// step are those of these numbers, and a definition that names each rounding can be computed elsewhere).
+__device__ __forceinline__ void moments(float g, float& m, float& v, const Coef& k) {
+#pragma clang fp contract(off)
+  m = k.b1 * m + k.a1 * g;
+  v = k.b2 * v + k.a2 * (g * g);
+}
+
+// Codes of x[i] / s, the quotient rounded to fp32, of eight values a lane.  Both x rc (1 - d) and x rc (1 + d) are
+// coded, with rc an approximation of 1 / s: the conversion is monotone, so where the codes are equal they are the
+// quotient's.  Elsewhere (a border between codes lies within some ulps: one wave in a hundred) `exact` gives the
+// quotients.  d covers the reciprocal's ulp (2 u), a rounding each of rc (1 +- d), of the product and of the
+// quotient, and the error that x itself has (2 u more and a rounding, for a root): 5 u, or 8 u.
+template <class F>
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float s, float d, F&& exact) {
+  const float rc = __builtin_amdgcn_rcpf(s), lo = rc * (1.f - d), hi = rc * (1.f + d);
+  uint2 c = make_uint2(pack_e4m3x4(x[0] * lo, x[1] * lo, x[2] * lo, x[3] * lo),
+                       pack_e4m3x4(x[4] * lo, x[5] * lo, x[6] * lo, x[7] * lo));
+  const uint2 h = make_uint2(pack_e4m3x4(x[0] * hi, x[1] * hi, x[2] * hi, x[3] * hi),
+                             pack_e4m3x4(x[4] * hi, x[5] * hi, x[6] * hi, x[7] * hi));
+  if (((c.x ^ h.x) | (c.y ^ h.y)) != 0 || !(s >= 0x1p-120f)) {  // below, the reciprocal may be infinite
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = exact(i);
+    c = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+  }
+  return c;
+}
+// A run's eight values in each of its sixteen lanes; returns the scale.
 __device__ __forceinline__ float code8(const float (&x)[8], uint2& codes) {
   float am = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
   am = max16(am);
   const float s = am == 0.f ? 1.f : am / 448.f;
-  float y[8];
-  if (s >= 0x1p-120f) {
-    block_quotients(x, s, 1.f / s, y);
-  } else {  // the reciprocal may be infinite
+  codes = codes_of(x, s, 0x1p-21f, [&](int i) { return x[i] / s; });
+  return s;
+}
+// The same of the square roots of v, r their approximations within an ulp; what is positive has a positive code.
+__device__ __forceinline__ float code8_root(const float (&v)[8], const float (&r)[8], uint2& codes) {
+  float am = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] / s;
-  }
-  if constexpr (LEAST) {
+  for (int i = 0; i < 8; ++i) am = fmaxf(am, v[i]);
+  am = max16(am);
+  const float s = am == 0.f ? 1.f : sqrtf(am) / 448.f;
+  codes = codes_of(r, s, 0x1p-20f, [&](int i) { return sqrtf(v[i]) / s; });
+  // codes are below 0x80: a byte + 0x7f has its top bit clear where the code is 0
+  if ((((codes.x + 0x7f7f7f7fu) & (codes.y + 0x7f7f7f7fu)) & 0x80808080u) != 0x80808080u) {
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i] > 0.f ? fmaxf(y[i], 0x1p-9f) : y[i];
+    for (int i = 0; i < 8; ++i) y[i] = v[i] > 0.f ? fmaxf(sqrtf(v[i]) / s, 0x1p-9f) : v[i];
+    codes = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
   }
-  codes.x = pack_e4m3x4(y[0], y[1], y[2], y[3]);
-  codes.y = pack_e4m3x4(y[4], y[5], y[6], y[7]);
   return s;
 }
 
-// This thread's eight elements of chunk c of entry i.
-template <bool E4M3, bool STREAM, class P, class G>
+// This thread's elements of chunk c of entry i: with codes eight neighbouring ones (sixteen lanes a run), with fp32
+// states two pieces of four, so that a wave's loads of 16 bytes lie side by side.  WHOLE: the chunk ends inside
+// the tensor.
+template <bool E4M3, bool STREAM, bool WHOLE, class P, class G>
 __device__ __forceinline__ void step_chunk(const AdamList& L, int i, uint32_t c, const Coef& k) {
-  const int64_t e = int64_t(c) * kChunk + threadIdx.x * 8, left = L.n[i] - e;
-  const int n = left > 8 ? 8 : int(left);  // may be negative
-  P* param = static_cast<P*>(L.param[i]) + e;
-  float* master = L.master[i];
+  constexpr int N = E4M3 ? 8 : 4, PIECES = 8 / N;
+  const int64_t base = int64_t(c) * kChunk;
+  const G* const grad = static_cast<const G*>(L.grad[i]) + base;
+  P* const param = static_cast<P*>(L.param[i]) + base;
+  float* const master = L.master[i] == nullptr ? nullptr : L.master[i] + base;
   const bool own = master == nullptr;
-  Eight<G> g8;
-  Eight<P> p8;
-  Eight<float> w8, m8, v8;
+  const float shrink = 1.f - k.lr * L.decay[i];
+  const int64_t rest = L.n[i] - base;
+  const int there = WHOLE || rest > kChunk ? kChunk : int(rest);
+  Piece<G, N> g8[PIECES];
+  Piece<P, N> p8[PIECES];
+  Piece<float, N> w8[PIECES], m8[PIECES], v8[PIECES];
   Codes mc, vc;
   float ms = 0.f, vs = 0.f;
-  g8.template get<STREAM>(static_cast<const G*>(L.grad[i]) + e, n);
-  if (own) p8.template get<STREAM>(param, n);
-  else w8.template get<STREAM>(master + e, n);
-  if constexpr (E4M3) {
-    mc.get(static_cast<const uint8_t*>(L.m[i]) + e, n);
-    vc.get(static_cast<const uint8_t*>(L.v[i]) + e, n);
-    if (n > 0) {
-      ms = L.ms[i][e >> 7];
-      vs = L.vs[i][e >> 7];
-    }
-  } else {
-    m8.template get<STREAM>(static_cast<const float*>(L.m[i]) + e, n);
-    v8.template get<STREAM>(static_cast<const float*>(L.v[i]) + e, n);
-  }
-  float g[8], p[8], m[8], v[8];
-  g8.values(g);
-  if (own) p8.values(p);
-  else w8.values(p);
-  if constexpr (E4M3) {
-    mc.values(m);
-    vc.values(v);
-  } else {
-    m8.values(m);
-    v8.values(v);
-  }
-  const float shrink = 1.f - k.lr * L.decay[i];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const double gd = double(g[j]) * k.c;
-    double md = double(m[j]), vd = double(v[j]);
+  for (int q = 0; q < PIECES; ++q) {
+    const uint32_t e = (q * kAdamThreads + threadIdx.x) * N;
+    const int n = WHOLE ? N : there - int(e);
+    g8[q].template get<STREAM>(grad + e, n);
+    if (own) p8[q].template get<STREAM>(param + e, n);
+    else w8[q].template get<STREAM>(master + e, n);
     if constexpr (E4M3) {
-      md *= double(ms);
-      vd *= double(vs);  // exact
-      vd *= vd;
+      mc.get<STREAM>(static_cast<const uint8_t*>(L.m[i]) + base + e, n);
+      vc.get<STREAM>(static_cast<const uint8_t*>(L.v[i]) + base + e, n);
+      if (n > 0) {
+        ms = (L.ms[i] + (base >> 7))[e >> 7];
+        vs = (L.vs[i] + (base >> 7))[e >> 7];
+      }
+    } else {
+      m8[q].template get<STREAM>(static_cast<const float*>(L.m[i]) + base + e, n);
+      v8[q].template get<STREAM>(static_cast<const float*>(L.v[i]) + base + e, n);
     }
-    m[j] = float(__builtin_fma(k.a1, gd, k.b1 * md));
-    const float v32 = float(__builtin_fma(k.a2 * gd, gd, k.b2 * vd));
-    const float sq = sqrtf(v32);
-    p[j] = __builtin_fmaf(p[j], shrink, -k.rate * (m[j] / __builtin_fmaf(sq, k.root, k.eps)));
-    v[j] = E4M3 ? sq : v32;
   }
-  if (own) {
-    Eight<P>::template put<STREAM>(param, n, p);
-  } else {
-    Eight<float>::template put<STREAM>(master + e, n, p);
-    Eight<P>::template put<STREAM>(param, n, p);
-  }
-  if constexpr (E4M3) {
-    uint2 codes;
-    ms = code8<false>(m, codes);
-    Codes::put(static_cast<uint8_t*>(L.m[i]) + e, n, codes);
-    vs = code8<true>(v, codes);
-    Codes::put(static_cast<uint8_t*>(L.v[i]) + e, n, codes);
-    if ((threadIdx.x & 15) == 0 && n > 0) {
-      L.ms[i][e >> 7] = ms;
-      L.vs[i][e >> 7] = vs;
+#pragma unroll
+  for (int q = 0; q < PIECES; ++q) {
+    const uint32_t e = (q * kAdamThreads + threadIdx.x) * N;
+    const int n = WHOLE ? N : there - int(e);
+    float g[N], p[N], m[N], v[N], r[N];
+    g8[q].values(g);
+    if (own) p8[q].values(p);
+    else w8[q].values(p);
+    if constexpr (E4M3) {
+      mc.values(m);
+      vc.values(v);
+    } else {
+      m8[q].values(m);
+      v8[q].values(v);
     }
-  } else {
-    Eight<float>::template put<STREAM>(static_cast<float*>(L.m[i]) + e, n, m);
-    Eight<float>::template put<STREAM>(static_cast<float*>(L.v[i]) + e, n, v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if constexpr (E4M3) {
+        m[j] *= ms;
+        v[j] *= vs;
+        v[j] *= v[j];
+      }
+      moments(g[j] * k.c, m[j], v[j], k);
+      r[j] = __builtin_amdgcn_sqrtf(v[j]);  // within an ulp; 0 for what is below the normal numbers
+    }
+    if (k.eps < 0x1p-30f) {  // where such a root (below 2^-63) would count beside eps
+#pragma unroll
+      for (int j = 0; j < N; ++j) r[j] = v[j] < 0x1p-126f ? sqrtf(v[j]) : r[j];
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      p[j] = __builtin_fmaf(p[j], shrink, -k.rate * (m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], k.root, k.eps))));
+    if (!own) Piece<float, N>::template put<STREAM>(master + e, n, p);
+    Piece<P, N>::template put<STREAM>(param + e, n, p);
+    if constexpr (E4M3) {
+      uint2 codes;
+      ms = code8(m, codes);
+      Codes::put<STREAM>(static_cast<uint8_t*>(L.m[i]) + base + e, n, codes);
+      vs = code8_root(v, r, codes);
+      Codes::put<STREAM>(static_cast<uint8_t*>(L.v[i]) + base + e, n, codes);
+      if ((threadIdx.x & 15) == 0 && n > 0) {
+        (L.ms[i] + (base >> 7))[e >> 7] = ms;
+        (L.vs[i] + (base >> 7))[e >> 7] = vs;
+      }
+    } else {
+      Piece<float, N>::template put<STREAM>(static_cast<float*>(L.m[i]) + base + e, n, m);
+      Piece<float, N>::template put<STREAM>(static_cast<float*>(L.v[i]) + base + e, n, v);
+    }
   }
 }
 
@@ -307,10 +391,15 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(AdamList L, AdamSte
   for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
     while (c >= L.first[i + 1]) ++i;
     const uint32_t at = c - L.first[i];
-    if (L.kind[i] == 3) step_chunk<E4M3, STREAM, float, float>(L, i, at, k);
-    else if (L.kind[i] == 2) step_chunk<E4M3, STREAM, uint16_t, float>(L, i, at, k);
-    else if (L.kind[i] == 1) step_chunk<E4M3, STREAM, float, uint16_t>(L, i, at, k);
-    else step_chunk<E4M3, STREAM, uint16_t, uint16_t>(L, i, at, k);
+    auto go = [&](auto whole) __attribute__((always_inline)) {
+      constexpr bool W = decltype(whole)::value;
+      if (L.kind[i] == 3) step_chunk<E4M3, STREAM, W, float, float>(L, i, at, k);
+      else if (L.kind[i] == 2) step_chunk<E4M3, STREAM, W, uint16_t, float>(L, i, at, k);
+      else if (L.kind[i] == 1) step_chunk<E4M3, STREAM, W, float, uint16_t>(L, i, at, k);
+      else step_chunk<E4M3, STREAM, W, uint16_t, uint16_t>(L, i, at, k);
+    };
+    if (c + 1 < L.first[i + 1]) go(std::true_type{});
+    else go(std::false_type{});
   }
 }
 
@@ -402,7 +491,8 @@ extern "C" int moe_adamw(const moe_adamw_desc* d, const moe_adamw_param* p, int3
   if (const int bad = check_apart(p, count, e4m3, lr, step, norm)) return bad;
   AdamStep st{};
   st.lr = lr; st.norm = norm; st.step = step;
-  st.b1 = d->beta1; st.b2 = d->beta2;
+  st.b1 = float(d->beta1); st.b2 = float(d->beta2);
+  st.a1 = float(1. - d->beta1); st.a2 = float(1. - d->beta2);
   st.log_b1 = std::log(d->beta1); st.log_b2 = std::log(d->beta2);
   st.eps = float(d->eps); st.max_norm = max_norm;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -412,8 +502,9 @@ extern "C" int moe_adamw(const moe_adamw_desc* d, const moe_adamw_param* p, int3
   uint64_t bytes = 0;
   auto flush = [&]() {
     if (L.count == 0) return int(MOE_OK);
-    const unsigned grid = std::min<uint32_t>(L.first[L.count], kMaxAdamBlocks);
     const bool stream_it = bytes > kStreamBytes;
+    const uint32_t chunks = L.first[L.count];
+    const unsigned grid = std::min(e4m3 && stream_it ? (chunks + 1) / 2 : chunks, kMaxAdamBlocks);
     prof_begin("adamw", s);
     if (e4m3) {
       if (stream_it) adamw_kernel<true, true><<<grid, kAdamThreads, 0, s>>>(L, st);

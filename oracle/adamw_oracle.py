@@ -19,6 +19,16 @@ def step(p, g, m, v, lr, t, beta1, beta2, eps, decay, norm=None, max_norm=0.0):
     return p, m, v
 
 
+def moments32(g, m, v, beta1, beta2, norm=None, max_norm=0.0):
+    """(m, v) in float32 as they are defined: each quotient, product and sum rounded."""
+    f = np.float32
+    g, m, v = (np.asarray(x, f) for x in (g, m, v))
+    with np.errstate(over="ignore", under="ignore", invalid="ignore"):
+        if norm is not None and f(norm) > f(max_norm):
+            g = g * (f(max_norm) / f(norm))
+        return (f(beta1) * m + f(1 - beta1) * g, f(beta2) * v + f(1 - beta2) * (g * g))
+
+
 def encode(x, least=False):
     """(codes uint8, scales fp32) of x, fp32 values, in runs of 128; least: what is positive has a code of 1 at least."""
     x = np.asarray(x, np.float32)
@@ -33,6 +43,6 @@ def encode(x, least=False):
 
 
 def decode(codes, scales):
-    """The values in float64."""
+    """The values: code * scale in float32."""
     codes = np.asarray(codes, np.uint8)
-    return q8.e4m3_decode(codes).astype(np.float64) * np.repeat(np.asarray(scales, np.float64), 128)[:codes.size]
+    return q8.e4m3_decode(codes).astype(np.float32) * np.repeat(np.asarray(scales, np.float32), 128)[:codes.size]

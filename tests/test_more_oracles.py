@@ -137,6 +137,21 @@ def test_adamw_against_torch():
     assert np.array_equal(ao.step(p0, g[0], m, v, 1e-2, 4, 0.9, 0.95, 1e-8, 0.1, norm=np.inf, max_norm=2.0)[0], p0)
 
 
+def test_moments_in_fp32():
+    rng = np.random.default_rng(5)
+    g, m, v = (rng.standard_normal(300).astype(np.float32) for _ in range(3))
+    v = v * v
+    for norm, top in ((None, 0.0), (0.5, 1.0), (3.0, 1.0)):
+        a, b = ao.moments32(g, m, v, 0.9, 0.95, norm, top)
+        assert a.dtype == b.dtype == np.float32
+        _, ra, rb = ao.step(np.zeros(300), g, m, v, 0.1, 3, 0.9, 0.95, 1e-8, 0.0, norm, top)
+        # a beta, a product and the sum, g's factor: 5 and (squared) 7 roundings of the terms
+        assert np.all(np.abs(a - ra) <= 5 * 2.0 ** -24 * (np.abs(0.9 * m) + np.abs(0.1 * g)))
+        assert np.all(np.abs(b - rb) <= 7 * 2.0 ** -24 * rb)
+    a, b = ao.moments32(np.float32([3.0]), np.float32([1.0]), np.float32([2.0]), 0.5, 0.25)
+    assert a[0] == 2.0 and b[0] == 0.5 + 0.75 * 9
+
+
 def test_state_codes():
     x = np.zeros(300, np.float32)
     x[:5] = [448.0, -1.0, 1e-5, 0.3, -448.0]
@@ -145,6 +160,6 @@ def test_state_codes():
     assert s.tolist() == [1.0, 7.0 / 448, 1.0] and codes[0] == 0x7E and codes[4] == 0xFE and codes[2] == 0
     assert codes[130] == 0x7E and not codes[256:].any()
     got = ao.decode(codes, s)
-    assert got[0] == 448 and got[1] == -1 and abs(got[3] - 0.3) <= 0.3 / 16 and got[130] == 448 * np.float64(s[1])
+    assert got[0] == 448 and got[1] == -1 and abs(got[3] - 0.3) <= 0.3 / 16 and got[130] == np.float32(448) * s[1]
     codes, s = ao.encode(np.abs(x), least=True)
     assert codes[2] == 1 and codes[1] != 0 and codes[5] == 0
