@@ -2,18 +2,21 @@
 // experts, the gradient of its weights into the logits, and the bias's step
 // (moe_gate_fwd, moe_gate_bwd, moe_gate_bias in moe.h).
 //
-// The choice goes by c = fl32(s + bias).  The scores are computed in 64 bits, so that
-// the rounding to fp32 decides which of two neighbours comes first and not the error of
-// an fp32 exp (a sequence of 16384 tokens has some five rows where that would show).
+// The choice goes by c = fl32(s + bias) of scores in 64 bits, so that the rounding to fp32 decides which
+// of two neighbours comes first and not the error of an fp32 exp.  64-bit scores of every logit cost more than
+// the memory does (65536 tokens of 256 experts: 63 us, where the logits take 11), so a wave first chooses by fp32
+// scores in fixed point and then looks whether any two choices that matter lie within their error bound of
+// each other: the K chosen ones and the next, and the groups at the border.  Only then (a row in a few hundred, rows
+// with equal scores, masked groups, scores past the numbers) it chooses again by 64-bit ones.
 //
 // LPT lanes share a token, each with VPL of its experts in runs of four; with groups, each
 // group has LPT / GP of the lanes (GP the power of two from the number of groups).
-// A choice is a 64-bit key: fp32's bits in their order, then the expert from the
-// highest down, below a fixed exponent, so that the 64-bit floating maximum (one
-// instruction) orders keys and breaks ties.  A lane sorts its keys with a merging network
-// (a maximum and a minimum a comparator); a group's score is the sum of its lanes'
-// two largest; then K times the largest head of a lane is the next expert, and
-// its lane moves on by one.
+// * A fixed-point key is c in units of 2^-22 (2^-20 past 256 experts) of the row's largest score or choice, then
+//   the expert from the highest down, so that an integer maximum orders keys.  A lane sorts its keys by merging
+//   networks (a maximum and a minimum a comparator) and keeps eight; K + 1 times the largest head of a lane is
+//   the next expert, and its lane moves on by one.
+// * A 64-bit key is fp32's bits of c in their order, then the expert, below a fixed exponent, so that the 64-bit
+//   floating maximum (one instruction) orders keys and breaks ties.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -69,6 +72,8 @@ __device__ __forceinline__ int cross(int v) {
   else return __shfl_xor(v, STEP, 64);
 }
 template <int STEP>
+__device__ __forceinline__ uint32_t cross(uint32_t v) { return uint32_t(cross<STEP>(int(v))); }
+template <int STEP>
 __device__ __forceinline__ double cross(double v) {
   const long long b = __double_as_longlong(v);
   const uint32_t lo = uint32_t(cross<STEP>(int(b))), hi = uint32_t(cross<STEP>(int(b >> 32)));
@@ -103,26 +108,6 @@ __device__ __forceinline__ double key_max(double v) {
   return v;
 }
 
-// Descending, by Batcher's odd-even merging network.
-template <int N>
-__device__ __forceinline__ void sort_keys(double (&k)[N]) {
-#pragma unroll
-  for (int p = 1; p < N; p *= 2)
-#pragma unroll
-    for (int q = p; q >= 1; q /= 2)
-#pragma unroll
-      for (int j = q % p; j + q < N; j += 2 * q)
-#pragma unroll
-        for (int i = 0; i < q; ++i) {
-          const int a = i + j, b = i + j + q;
-          if (b < N && a / (2 * p) == b / (2 * p)) {
-            const double hi = __builtin_fmax(k[a], k[b]), lo = __builtin_fmin(k[a], k[b]);
-            k[a] = hi;
-            k[b] = lo;
-          }
-        }
-}
-
 __device__ __forceinline__ float element(const float* p) { return *p; }
 __device__ __forceinline__ float element(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
 struct __attribute__((packed, aligned(4))) Four32 { float v[4]; };
@@ -153,54 +138,284 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ double sigmoid64(float z) { return 1. / (1. + exp(-double(z))); }
+// e^x in 64 bits (2^-45 relative): its series on half an octave.  0 below -700, infinite above 709.
+__device__ __forceinline__ double exp64(double x) {
+  const double c = x < -745. ? -745. : x > 745. ? 745. : x;  // a NaN stays
+  const double n = __builtin_rint(c * 1.4426950408889634074);
+  double r = __builtin_fma(n, -0.693147180559945286, c);
+  r = __builtin_fma(n, -2.3190468138462996e-17, r);
+  double y = 1. / 39916800.;
+  y = __builtin_fma(y, r, 1. / 3628800.);
+  y = __builtin_fma(y, r, 1. / 362880.);
+  y = __builtin_fma(y, r, 1. / 40320.);
+  y = __builtin_fma(y, r, 1. / 5040.);
+  y = __builtin_fma(y, r, 1. / 720.);
+  y = __builtin_fma(y, r, 1. / 120.);
+  y = __builtin_fma(y, r, 1. / 24.);
+  y = __builtin_fma(y, r, 1. / 6.);
+  y = __builtin_fma(y, r, 0.5);
+  y = __builtin_fma(y, r, 1.);
+  y = __builtin_fma(y, r, 1.);
+  return __builtin_ldexp(y, int(n));
+}
+__device__ __forceinline__ double sigmoid64(float z) { return 1. / (1. + exp64(-double(z))); }
 
+// Descending, by Batcher's odd-even merging network.
+template <int N>
+__device__ __forceinline__ void sort8(uint32_t (&k)[N], int from) {
+#pragma unroll
+  for (int p = 1; p < 8; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < 8; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i) {
+          const int a = i + j, b = i + j + q;
+          if (b < 8 && a / (2 * p) == b / (2 * p) && from + b < N) {
+            const uint32_t x = k[from + a], y = k[from + b];
+            k[from + a] = max(x, y);
+            k[from + b] = min(x, y);
+          }
+        }
+}
+// The largest eight of a lane's keys, descending in its first eight (all of fewer).
+template <int VPL>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[VPL]) {
+  constexpr int N = VPL < 8 ? VPL : 8;
+#pragma unroll
+  for (int f = 0; f < VPL; f += 8) sort8(k, f);
+#pragma unroll
+  for (int f = 8; f < VPL; f += 8) {
+    // the larger of a descending and an ascending row: the eight largest, which rise and then fall
+#pragma unroll
+    for (int i = 0; i < N; ++i) k[i] = max(k[i], k[f + N - 1 - i]);
+#pragma unroll
+    for (int q = N / 2; q >= 1; q /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((i & q) == 0) {
+          const uint32_t x = k[i], y = k[i + q];
+          k[i] = max(x, y);
+          k[i + q] = min(x, y);
+        }
+  }
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t token_min(uint32_t v) {
+  each_step(LPT, [&](auto s) { v = min(v, cross<decltype(s)::value>(v)); });
+  return v;
+}
+// Lanes of this one's sixteen whose v is larger.
+template <int N = 1>
+__device__ __forceinline__ int lanes_ahead(uint32_t v) {
+  const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + N, 0xF, 0xF, true));  // row_ror:N
+  if constexpr (N < 15) return (o > v ? 1 : 0) + lanes_ahead<N + 1>(v);
+  else return o > v ? 1 : 0;
+}
+
+// A token's lanes and the experts of one of them.
+template <int LPT>
+struct Share {
+  int l, g, in;  // lane of the token, its group, its place in the group
+  bool mine;
+  __device__ __forceinline__ explicit Share(const GateArgs& a)
+      : l(threadIdx.x & (LPT - 1)), g(l / a.lanes), in(l & (a.lanes - 1)), mine(g < a.groups) {}
+  __device__ __forceinline__ int place(const GateArgs& a, int i) const {  // in its group, of the i-th value
+    return 4 * (in + a.lanes * (i >> 2)) + (i & 3);
+  }
+};
 template <class Z, int LPT, int VPL>
-__global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int32_t* __restrict__ topk_idx,
-                                                                float* __restrict__ topk_w) {
-  constexpr int TOKENS = kGateThreads / LPT;
-  __shared__ double s_group[TOKENS][kGateMaxGroups < LPT ? kGateMaxGroups : LPT];
-  const int l = threadIdx.x & (LPT - 1), tok = threadIdx.x / LPT;
-  const int64_t t = int64_t(blockIdx.x) * TOKENS + tok;
-  const bool there = t < a.T;  // lanes behind the last token go along with it
-  const Z* row = static_cast<const Z*>(a.z) + (there ? t : a.T - 1) * a.ld;
-  // the lane's experts: g * each + e for e in runs of four
-  const int g = l / a.lanes, in = l & (a.lanes - 1);
-  const bool mine = g < a.groups;
+__device__ __forceinline__ void load_logits(const GateArgs& a, const Share<LPT>& s, const Z* row, float (&z)[VPL]) {
   const bool fours = (a.each & 3) == 0;
-  float z[VPL];
 #pragma unroll
   for (int q = 0; q < VPL / 4; ++q) {
-    const int e = 4 * (in + a.lanes * q);
+    const int e = s.place(a, 4 * q);
     float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (mine) {
+    if (s.mine) {
       if (fours) {
-        if (e < a.each) four(row + g * a.each + e, f);
+        if (e < a.each) four(row + s.g * a.each + e, f);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (e + r < a.each) f[r] = element(row + g * a.each + e + r);
+          if (e + r < a.each) f[r] = element(row + s.g * a.each + e + r);
       }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) z[4 * q + r] = f[r];
   }
-  float m = 0.f;
-  double inv = 1.;
-  double key[VPL];
+}
+
+// Sum by halves: log2 VPL roundings.
+template <int N>
+__device__ __forceinline__ float half_sum(const float* v) {
+  if constexpr (N == 1) return v[0];
+  else return half_sum<N / 2>(v) + half_sum<N / 2>(v + N / 2);
+}
+
+// The choice by fixed-point keys: lane k's expert of slot k in `at`, its logit in x; false where this wave's tokens have to
+// be chosen by 64-bit keys.  m, inv: the largest logit and 1 / sum exp(z - m) for softmax scores.
+//
+// Errors, u = 2^-24: of a sigmoid's e^-z 3 u (its exponent is formed in two parts), 1 + e u, the reciprocal 2 u; of a
+// softmax's score 2 u + 0.6 u of the row's largest for the exp, 11 u for the sum by halves over VPL values and
+// the lanes, 3 u for the reciprocal and the product; 1 u each for the sum with the bias and the product with the unit's
+// reciprocal: below 20 u of M, the largest score or choice.  A unit of 2^-22 M is 4 u, so that keys
+// are off by 5 units and half a one for their rounding, the fp32 rounding of c a quarter: a difference of 13 units is
+// one of c's.  With units of 2^-20 M (16 u) one of 5 is.  The sums of two of a group twice that and an fp32 rounding.
+template <class Z, int LPT, int VPL>
+__device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>& sh, const Z* row, int& at, float& x,
+                                             float& m, float& inv) {
+  constexpr int PB = LPT == 16 ? 8 : 10, GAP = LPT == 16 ? 13 : 5;
+  constexpr uint32_t PLACES = (1u << PB) - 1;
+  constexpr float TOP = LPT == 16 ? 4194304.f : 1048576.f;  // units of M
+  constexpr float MAGIC = LPT == 16 ? 12582912.f : 13631488.f;  // 1.5 * 2^23 (+ TOP): an integer's bits are the low ones
+  float z[VPL], c[VPL];
+  load_logits(a, sh, row, z);
   if (a.softmax) {
     m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, z[i]);
+    m = fmaxf(token_max<LPT>(m), -FLT_MAX);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)  // with a NaN or +inf the sum is a NaN, with only -inf it is 0
+      c[i] = __builtin_amdgcn_exp2f((z[i] - m) * 1.44269504f);
+    inv = __builtin_amdgcn_rcpf(token_sum<LPT>(half_sum<VPL>(c)));
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] *= inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float y = __builtin_amdgcn_fmed3f(z[i], -88.f, 88.f);
+      const float hi = y * -1.44269504f;
+      const float lo = __builtin_fmaf(y, -1.92596299e-8f, __builtin_fmaf(y, -1.44269504f, -hi));
+      const float e = __builtin_amdgcn_exp2f(hi);
+      c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_fmaf(e, lo * 0.693147181f, e));
+    }
+  }
+  // M, and c in the place of the scores (0 where an expert cannot be chosen)
+  float M = 0.f;
+  bool odd = false;  // a NaN score
+#pragma unroll
+  for (int q = 0; q < VPL / 4; ++q) {
+    const int e = sh.place(a, 4 * q);
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.bias != nullptr && sh.mine) {
+      const float* p = a.bias + sh.g * a.each + e;
+      if ((a.each & 3) == 0) {
+        if (e < a.each) four(p, b);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (e + r < a.each) b[r] = p[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float s = c[4 * q + r], v = s + b[r];
+      odd |= !(s >= 0.f);
+      c[4 * q + r] = z[4 * q + r] > -INFINITY ? v : 0.f;
+      M = fmaxf(fmaxf(M, s), fabsf(c[4 * q + r]));
+    }
+  }
+  M = token_max<LPT>(M);
+  bool bad = odd || !(M >= 0x1p-60f && M < 0x1p100f);
+  const float unit = __builtin_amdgcn_rcpf(M) * (TOP - 2048.f);
+  uint32_t key[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = sh.place(a, i);
+    const uint32_t last = PLACES - uint32_t(sh.g * a.each + e);
+    const uint32_t k = (__float_as_uint(__builtin_fmaf(c[i], unit, MAGIC)) << PB) + last;
+    // one that cannot be chosen before any other: a unit of 1, under all others' 2000
+    key[i] = sh.mine && e < a.each ? (z[i] > -INFINITY ? k : (1u << PB) + last) : 0u;
+  }
+  sort_keys(key);
+  constexpr int N = VPL < 8 ? VPL : 8;
+  const bool full = VPL > 8 && key[N - 1] != 0;
+  bool kept = true;
+  if (a.top_groups < a.groups) {
+    uint32_t k0 = key[0], k1 = key[1];
+    each_step(a.lanes, [&](auto s) {
+      const uint32_t o0 = cross<decltype(s)::value>(k0), o1 = cross<decltype(s)::value>(k1);
+      k1 = max(min(k0, o0), max(k1, o1));
+      k0 = max(k0, o0);
+    });
+    uint32_t score = k0 >> PB;
+    // a group that holds too few: its sum is another number
+    bad |= sh.mine && score < 2;
+    if (a.best == 2 && a.each > 1) {
+      bad |= sh.mine && (k1 >> PB) < 2;
+      score += k1 >> PB;
+    }
+    int ahead;  // lanes of better groups
+    if constexpr (LPT == 16) {
+      ahead = lanes_ahead(score);
+    } else {
+      ahead = 0;
+      for (int j = 0; j < a.groups; ++j) ahead += uint32_t(__shfl(int(score), j * a.lanes, 64)) > score ? a.lanes : 0;
+    }
+    const bool in = ahead < a.top_groups * a.lanes;
+    const uint32_t worst = token_min<LPT>(in ? score : 0xffffffffu), next = token_max<LPT>(in ? 0u : score);
+    bad |= worst < next + (2 * GAP + 2);
+    // groups with equal sums are all ahead of the next
+    const uint64_t lanes = LPT == 64 ? ~0ull : 0xffffull << (threadIdx.x & 48);
+    bad |= __popcll(__ballot(in) & lanes) != a.top_groups * a.lanes;
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = in ? key[i] : 0u;
+    kept = in;
+  }
+  uint32_t won = 0, loser = 0;
+  for (int k = 0; k <= a.K; ++k) {
+    loser = token_max<LPT>(key[0]);
+    if (sh.l == k) won = loser;
+    // one bit-field insert a key; a select of two of them becomes a search through the array
+    const uint32_t next = key[0] == loser ? ~0u : 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = ((i + 1 < N ? key[i + 1] : 0u) & next) | (key[i] & ~next);
+  }
+  bad |= full && kept && key[0] == 0;  // more than eight of one lane's: the others are not known
+  at = int(PLACES - (won & PLACES));
+  at = at < a.E ? at : 0;
+  x = element(row + at);
+  uint32_t behind;
+  float x_behind;
+  if constexpr (LPT == 16) {  // the next lane's
+    behind = uint32_t(__builtin_amdgcn_update_dpp(0, int(won), 0x101, 0xF, 0xF, false));  // row_shl:1
+    x_behind = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xF, 0xF, false));
+  } else {
+    behind = __shfl_down(won, 1, 64);
+    x_behind = __shfl_down(x, 1, 64);
+  }
+  if (sh.l == a.K - 1) {
+    behind = loser;
+    const int other = int(PLACES - (loser & PLACES));
+    x_behind = element(row + (other < a.E ? other : 0));
+  }
+  // equal logits without a bias have equal choices, whose places decide
+  const bool near = behind != 0 && (won >> PB) < (behind >> PB) + GAP && !(a.bias == nullptr && x == x_behind);
+  bad |= sh.l < a.K && near;
+  return __ballot(bad) == 0;
+}
+
+// The choice by 64-bit keys, one maximum over the lane's values a slot.
+template <class Z, int LPT, int VPL>
+__device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LPT>& sh, const Z* row, int& at, float& x) {
+  float z[VPL];
+  load_logits(a, sh, row, z);
+  double key[VPL];
+  if (a.softmax) {
+    float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) m = fmaxf(m, z[i]);
     m = token_max<LPT>(m);
     double sum = 0.;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      key[i] = z[i] == -INFINITY ? 0. : exp(double(z[i]) - double(m));
+      key[i] = z[i] == -INFINITY ? 0. : exp64(double(z[i]) - double(m));
       sum += key[i];
     }
     sum = token_sum<LPT>(sum);
-    inv = sum == 0. ? 0. : 1. / sum;
+    const double inv = sum == 0. ? 0. : 1. / sum;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] *= inv;
   } else {
@@ -209,28 +424,33 @@ __global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int3
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = 4 * (in + a.lanes * (i >> 2)) + (i & 3), at = g * a.each + e;
-    const bool is = mine && e < a.each;
+    const int e = sh.place(a, i), to = sh.g * a.each + e;
+    const bool is = sh.mine && e < a.each;
     double s = key[i];
-    if (a.bias != nullptr && is) s += double(a.bias[at]);
+    if (a.bias != nullptr && is) s += double(a.bias[to]);
     const float c = z[i] == -INFINITY ? -FLT_MAX : fmaxf(float(s), -FLT_MAX);
-    key[i] = is ? make_key(c, at) : 0.;
+    key[i] = is ? make_key(c, to) : 0.;
   }
-  sort_keys(key);
   if (a.top_groups < a.groups) {
-    double k0 = key[0], k1 = key[1];
+    double k0 = 0., k1 = 0.;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      k1 = __builtin_fmax(k1, __builtin_fmin(k0, key[i]));
+      k0 = __builtin_fmax(k0, key[i]);
+    }
     each_step(a.lanes, [&](auto s) {
       const double o0 = cross<decltype(s)::value>(k0), o1 = cross<decltype(s)::value>(k1);
       k1 = __builtin_fmax(__builtin_fmin(k0, o0), __builtin_fmax(k1, o1));
       k0 = __builtin_fmax(k0, o0);
     });
-    float score = key_value(k0);
+    float score = sh.mine ? key_value(k0) : 0.f;
     if (a.best == 2 && k1 != 0.) score += key_value(k1);
-    const double own = mine ? make_key(score, g) : 0.;
-    if (in == 0) s_group[tok][g] = own;
-    wave_order();
+    const double own = sh.mine ? make_key(score, sh.g) : 0.;
     int ahead = 0;
-    for (int j = 0; j < a.groups; ++j) ahead += s_group[tok][j] > own ? 1 : 0;
+    for (int j = 0; j < a.groups; ++j) {
+      const int from = (int(threadIdx.x) & 63 & ~(LPT - 1)) + j * a.lanes;
+      ahead += __shfl(own, from, 64) > own ? 1 : 0;
+    }
     if (ahead >= a.top_groups) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) key[i] = 0.;
@@ -238,29 +458,39 @@ __global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int3
   }
   double won = 0.;
   for (int k = 0; k < a.K; ++k) {
-    const double top = key_max<LPT>(key[0]);
-    if (l == k) won = top;
-    const bool next = key[0] == top;
+    double top = key[0];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const double behind = i + 1 < VPL ? key[i + 1] : 0.;
-      key[i] = next ? behind : key[i];
-    }
+    for (int i = 1; i < VPL; ++i) top = __builtin_fmax(top, key[i]);
+    top = key_max<LPT>(top);
+    if (sh.l == k) won = top;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = key[i] == top ? 0. : key[i];
   }
+  at = sh.l < a.K ? key_place(won) : 0;
+  x = element(row + at);
+}
+
+template <class Z, int LPT, int VPL>
+__global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int32_t* __restrict__ topk_idx,
+                                                                float* __restrict__ topk_w) {
+  constexpr int TOKENS = kGateThreads / LPT;
+  const Share<LPT> sh(a);
+  const int64_t t = int64_t(blockIdx.x) * TOKENS + threadIdx.x / LPT;
+  const bool there = t < a.T;  // lanes behind the last token go along with it
+  const Z* row = static_cast<const Z*>(a.z) + (there ? t : a.T - 1) * a.ld;
+  int at;
+  float x, m = 0.f, inv = 1.f;
+  if (!choose_fixed<Z, LPT, VPL>(a, sh, row, at, x, m, inv)) choose_exactly<Z, LPT, VPL>(a, sh, row, at, x);
   double s = 0.;
-  int at = 0;
-  if (l < a.K) {
-    at = key_place(won);
-    const float x = element(row + at);
-    s = a.softmax ? (x == -INFINITY ? 0. : exp(double(x) - double(m))) * inv : sigmoid64(x);
-  }
+  if (sh.l < a.K) s = a.softmax ? (x == -INFINITY ? 0. : exp64(double(x) - double(m))) : sigmoid64(x);
+  if (a.softmax && (!a.renorm || !(inv < INFINITY))) s *= inv == INFINITY ? 0. : double(inv);  // a row of only -inf, a NaN
   if (a.renorm) {
     const double sum = token_sum<LPT>(s);
     s = sum == 0. ? 0. : s / sum;
   }
-  if (l < a.K && there) {
-    topk_idx[t * a.K + l] = at;
-    topk_w[t * a.K + l] = float(s * double(a.scale));
+  if (sh.l < a.K && there) {
+    topk_idx[t * a.K + sh.l] = at;
+    topk_w[t * a.K + sh.l] = float(s * double(a.scale));
   }
 }
 
