@@ -17,6 +17,7 @@
 //   the next expert, and its lane moves on by one.
 // * A 64-bit key is fp32's bits of c in their order, then the expert, below a fixed exponent, so that the 64-bit
 //   floating maximum (one instruction) orders keys and breaks ties.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -110,23 +111,23 @@ __device__ __forceinline__ double key_max(double v) {
 
 __device__ __forceinline__ float element(const float* p) { return *p; }
 __device__ __forceinline__ float element(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
-struct __attribute__((packed, aligned(4))) Four32 { float v[4]; };
-struct __attribute__((packed, aligned(2))) Four16 { uint32_t v[2]; };
+// Four elements at any element's address, in one access.
+typedef float four_f32 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t four_bf16 __attribute__((ext_vector_type(2), aligned(2)));
 __device__ __forceinline__ void four(const float* p, float (&f)[4]) {
-  const Four32 a = *reinterpret_cast<const Four32*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = a.v[i];
+  const four_f32 a = *reinterpret_cast<const four_f32*>(p);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
 }
 __device__ __forceinline__ void four(const uint16_t* p, float (&f)[4]) {
-  const Four16 a = *reinterpret_cast<const Four16*>(p);
-  f[0] = __uint_as_float(a.v[0] << 16); f[1] = __uint_as_float(a.v[0] & 0xffff0000u);
-  f[2] = __uint_as_float(a.v[1] << 16); f[3] = __uint_as_float(a.v[1] & 0xffff0000u);
+  const four_bf16 a = *reinterpret_cast<const four_bf16*>(p);
+  f[0] = __uint_as_float(a.x << 16); f[1] = __uint_as_float(a.x & 0xffff0000u);
+  f[2] = __uint_as_float(a.y << 16); f[3] = __uint_as_float(a.y & 0xffff0000u);
 }
 __device__ __forceinline__ void put_four(float* p, const float (&f)[4]) {
-  *reinterpret_cast<Four32*>(p) = Four32{{f[0], f[1], f[2], f[3]}};
+  *reinterpret_cast<four_f32*>(p) = four_f32{f[0], f[1], f[2], f[3]};
 }
 __device__ __forceinline__ void put_four(uint16_t* p, const float (&f)[4]) {
-  *reinterpret_cast<Four16*>(p) = Four16{{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])}};
+  *reinterpret_cast<four_bf16*>(p) = four_bf16{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
 }
 __device__ __forceinline__ void put_one(float* p, float f) { *p = f; }
 __device__ __forceinline__ void put_one(uint16_t* p, float f) { *p = uint16_t(pack_bf16x2(f, 0.f)); }
@@ -138,27 +139,42 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// e^x in 64 bits (2^-45 relative): its series on half an octave.  0 below -700, infinite above 709.
+// A constant of 64 bits in scalar registers where it is used: kept over a loop in vector registers, those of
+// exp64 take half of them.
+__device__ __forceinline__ double scalar(double c) {
+  asm volatile("" : "+s"(c));
+  return c;
+}
+// e^x in 64 bits (2^-45 relative): its series on half an octave.  0 below -745, infinite above 709.
 __device__ __forceinline__ double exp64(double x) {
   const double c = x < -745. ? -745. : x > 745. ? 745. : x;  // a NaN stays
-  const double n = __builtin_rint(c * 1.4426950408889634074);
-  double r = __builtin_fma(n, -0.693147180559945286, c);
-  r = __builtin_fma(n, -2.3190468138462996e-17, r);
-  double y = 1. / 39916800.;
-  y = __builtin_fma(y, r, 1. / 3628800.);
-  y = __builtin_fma(y, r, 1. / 362880.);
-  y = __builtin_fma(y, r, 1. / 40320.);
-  y = __builtin_fma(y, r, 1. / 5040.);
-  y = __builtin_fma(y, r, 1. / 720.);
-  y = __builtin_fma(y, r, 1. / 120.);
-  y = __builtin_fma(y, r, 1. / 24.);
-  y = __builtin_fma(y, r, 1. / 6.);
+  const double n = __builtin_rint(c * scalar(1.4426950408889634074));
+  double r = __builtin_fma(n, scalar(-0.693147180559945286), c);
+  r = __builtin_fma(n, scalar(-2.3190468138462996e-17), r);
+  double y = scalar(1. / 39916800.);
+  y = __builtin_fma(y, r, scalar(1. / 3628800.));
+  y = __builtin_fma(y, r, scalar(1. / 362880.));
+  y = __builtin_fma(y, r, scalar(1. / 40320.));
+  y = __builtin_fma(y, r, scalar(1. / 5040.));
+  y = __builtin_fma(y, r, scalar(1. / 720.));
+  y = __builtin_fma(y, r, scalar(1. / 120.));
+  y = __builtin_fma(y, r, scalar(1. / 24.));
+  y = __builtin_fma(y, r, scalar(1. / 6.));
   y = __builtin_fma(y, r, 0.5);
   y = __builtin_fma(y, r, 1.);
   y = __builtin_fma(y, r, 1.);
   return __builtin_ldexp(y, int(n));
 }
-__device__ __forceinline__ double sigmoid64(float z) { return 1. / (1. + exp64(-double(z))); }
+// 1 / y for y of normal size (2^-50 relative).
+__device__ __forceinline__ double inverse64(double y) {
+  double r = __builtin_amdgcn_rcp(y);
+  r = __builtin_fma(__builtin_fma(-y, r, 1.), r, r);
+  return __builtin_fma(__builtin_fma(-y, r, 1.), r, r);
+}
+__device__ __forceinline__ double sigmoid64(float z) {
+  const double e = exp64(-double(z));
+  return e < 1e300 ? inverse64(1. + e) : e != e ? e : 0.;
+}
 
 // Descending, by Batcher's odd-even merging network.
 template <int N>
@@ -206,12 +222,18 @@ __device__ __forceinline__ uint32_t token_min(uint32_t v) {
   each_step(LPT, [&](auto s) { v = min(v, cross<decltype(s)::value>(v)); });
   return v;
 }
-// Lanes of this one's sixteen whose v is larger.
-template <int N = 1>
-__device__ __forceinline__ int lanes_ahead(uint32_t v) {
+// Of the groups of `lanes` lanes in this one's sixteen, those whose v is larger.
+template <int N, int STEP>
+__device__ __forceinline__ int ahead_from(uint32_t v) {
   const uint32_t o = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + N, 0xF, 0xF, true));  // row_ror:N
-  if constexpr (N < 15) return (o > v ? 1 : 0) + lanes_ahead<N + 1>(v);
+  if constexpr (N + STEP < 16) return (o > v ? 1 : 0) + ahead_from<N + STEP, STEP>(v);
   else return o > v ? 1 : 0;
+}
+__device__ __forceinline__ int groups_ahead(uint32_t v, int lanes) {
+  if (lanes == 1) return ahead_from<1, 1>(v);
+  if (lanes == 2) return ahead_from<2, 2>(v);
+  if (lanes == 4) return ahead_from<4, 4>(v);
+  return ahead_from<8, 8>(v);
 }
 
 // A token's lanes and the experts of one of them.
@@ -225,14 +247,17 @@ struct Share {
     return 4 * (in + a.lanes * (i >> 2)) + (i & 3);
   }
 };
-template <class Z, int LPT, int VPL>
+// Its experts' values, -inf where it has fewer than VPL (RAGGED).
+template <bool RAGGED, class Z, int LPT, int VPL>
 __device__ __forceinline__ void load_logits(const GateArgs& a, const Share<LPT>& s, const Z* row, float (&z)[VPL]) {
   const bool fours = (a.each & 3) == 0;
 #pragma unroll
   for (int q = 0; q < VPL / 4; ++q) {
     const int e = s.place(a, 4 * q);
     float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (s.mine) {
+    if constexpr (!RAGGED) {
+      four(row + s.g * a.each + e, f);
+    } else if (s.mine) {
       if (fours) {
         if (e < a.each) four(row + s.g * a.each + e, f);
       } else {
@@ -253,8 +278,14 @@ __device__ __forceinline__ float half_sum(const float* v) {
   else return half_sum<N / 2>(v) + half_sum<N / 2>(v + N / 2);
 }
 
-// The choice by fixed-point keys: lane k's expert of slot k in `at`, its logit in x; false where this wave's tokens have to
-// be chosen by 64-bit keys.  m, inv: the largest logit and 1 / sum exp(z - m) for softmax scores.
+// What a lane ends up with: the expert `at`, its logit and its slot (K or more: none).
+struct Choice {
+  int at, slot;
+  float x;
+};
+
+// The choice by fixed-point keys; false where this wave's tokens have to be chosen by 64-bit keys.  m, inv: the largest logit and 1 / sum exp(z - m) for softmax scores.  RAGGED: some lane has
+// fewer than VPL experts.
 //
 // Errors, u = 2^-24: of a sigmoid's e^-z 3 u (its exponent is formed in two parts), 1 + e u, the reciprocal 2 u; of a
 // softmax's score 2 u + 0.6 u of the row's largest for the exp, 11 u for the sum by halves over VPL values and
@@ -262,15 +293,24 @@ __device__ __forceinline__ float half_sum(const float* v) {
 // reciprocal: below 20 u of M, the largest score or choice.  A unit of 2^-22 M is 4 u, so that keys
 // are off by 5 units and half a one for their rounding, the fp32 rounding of c a quarter: a difference of 13 units is
 // one of c's.  With units of 2^-20 M (16 u) one of 5 is.  The sums of two of a group twice that and an fp32 rounding.
-template <class Z, int LPT, int VPL>
-__device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>& sh, const Z* row, int& at, float& x,
+template <bool RAGGED, class Z, int LPT, int VPL>
+__device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>& sh, const Z* row, Choice& out,
                                              float& m, float& inv) {
-  constexpr int PB = LPT == 16 ? 8 : 10, GAP = LPT == 16 ? 13 : 5;
+  constexpr int PB = LPT == 16 ? 8 : 10, GAP = LPT == 16 ? 13 : 5, N = VPL < 8 ? VPL : 8;
   constexpr uint32_t PLACES = (1u << PB) - 1;
   constexpr float TOP = LPT == 16 ? 4194304.f : 1048576.f;  // units of M
   constexpr float MAGIC = LPT == 16 ? 12582912.f : 13631488.f;  // 1.5 * 2^23 (+ TOP): an integer's bits are the low ones
+  auto is = [&](int i) { return sh.mine && sh.place(a, i) < a.each; };
+  // -inf, NaN and +inf are left to the 64-bit keys
   float z[VPL], c[VPL];
-  load_logits(a, sh, row, z);
+  load_logits<RAGGED>(a, sh, row, z);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) c[i] = z[i];
+  if constexpr (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = is(i) ? c[i] : 0.f;
+  }
+  bool hard = !(fabsf(half_sum<VPL>(c)) < INFINITY);
   if (a.softmax) {
     m = -INFINITY;
 #pragma unroll
@@ -292,47 +332,35 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
       c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_fmaf(e, lo * 0.693147181f, e));
     }
   }
-  // M, and c in the place of the scores (0 where an expert cannot be chosen)
   float M = 0.f;
-  bool odd = false;  // a NaN score
 #pragma unroll
-  for (int q = 0; q < VPL / 4; ++q) {
-    const int e = sh.place(a, 4 * q);
-    float b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.bias != nullptr && sh.mine) {
-      const float* p = a.bias + sh.g * a.each + e;
-      if ((a.each & 3) == 0) {
-        if (e < a.each) four(p, b);
-      } else {
+  for (int i = 0; i < VPL; ++i) M = fmaxf(M, c[i]);
+  if (a.bias != nullptr) {
+    load_logits<RAGGED>(a, sh, a.bias, z);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (e + r < a.each) b[r] = p[r];
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float s = c[4 * q + r], v = s + b[r];
-      odd |= !(s >= 0.f);
-      c[4 * q + r] = z[4 * q + r] > -INFINITY ? v : 0.f;
-      M = fmaxf(fmaxf(M, s), fabsf(c[4 * q + r]));
+    for (int i = 0; i < VPL; ++i) {
+      c[i] += RAGGED && !is(i) ? 0.f : z[i];
+      M = fmaxf(M, fabsf(c[i]));
     }
   }
   M = token_max<LPT>(M);
-  bool bad = odd || !(M >= 0x1p-60f && M < 0x1p100f);
+  hard |= !(M >= 0x1p-60f && M < 0x1p100f);
   const float unit = __builtin_amdgcn_rcpf(M) * (TOP - 2048.f);
   uint32_t key[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = sh.place(a, i);
-    const uint32_t last = PLACES - uint32_t(sh.g * a.each + e);
-    const uint32_t k = (__float_as_uint(__builtin_fmaf(c[i], unit, MAGIC)) << PB) + last;
-    // one that cannot be chosen before any other: a unit of 1, under all others' 2000
-    key[i] = sh.mine && e < a.each ? (z[i] > -INFINITY ? k : (1u << PB) + last) : 0u;
+  for (int q = 0; q < VPL / 4; ++q) {
+    const uint32_t last = PLACES - uint32_t(sh.g * a.each + sh.place(a, 4 * q));
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      key[4 * q + r] = (__float_as_uint(__builtin_fmaf(c[4 * q + r], unit, MAGIC)) << PB) + (last - r);
+  }
+  if constexpr (RAGGED) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = is(i) ? key[i] : 0u;
   }
   sort_keys(key);
-  constexpr int N = VPL < 8 ? VPL : 8;
-  const bool full = VPL > 8 && key[N - 1] != 0;
-  bool kept = true;
+  bool full = VPL > 8 && key[N - 1] != 0;  // there may be more than the eight kept
+  auto place_of = [&](uint32_t k) { const int e = int(PLACES - (k & PLACES)); return e < a.E ? e : 0; };
   if (a.top_groups < a.groups) {
     uint32_t k0 = key[0], k1 = key[1];
     each_step(a.lanes, [&](auto s) {
@@ -340,68 +368,88 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
       k1 = max(min(k0, o0), max(k1, o1));
       k0 = max(k0, o0);
     });
-    uint32_t score = k0 >> PB;
-    // a group that holds too few: its sum is another number
-    bad |= sh.mine && score < 2;
-    if (a.best == 2 && a.each > 1) {
-      bad |= sh.mine && (k1 >> PB) < 2;
-      score += k1 >> PB;
-    }
-    int ahead;  // lanes of better groups
+    // a group's score in units; by its best alone the whole key, whose place orders equal ones
+    const bool two = a.best == 2 && a.each > 1;
+    const uint32_t score = two ? (k0 >> PB) + (k1 >> PB) : k0;
+    int ahead;
     if constexpr (LPT == 16) {
-      ahead = lanes_ahead(score);
+      ahead = groups_ahead(score, a.lanes);
     } else {
       ahead = 0;
-      for (int j = 0; j < a.groups; ++j) ahead += uint32_t(__shfl(int(score), j * a.lanes, 64)) > score ? a.lanes : 0;
+      for (int j = 0; j < a.groups; ++j) ahead += uint32_t(__shfl(int(score), j * a.lanes, 64)) > score ? 1 : 0;
     }
-    const bool in = ahead < a.top_groups * a.lanes;
+    const bool in = ahead < a.top_groups;
     const uint32_t worst = token_min<LPT>(in ? score : 0xffffffffu), next = token_max<LPT>(in ? 0u : score);
-    bad |= worst < next + (2 * GAP + 2);
-    // groups with equal sums are all ahead of the next
-    const uint64_t lanes = LPT == 64 ? ~0ull : 0xffffull << (threadIdx.x & 48);
-    bad |= __popcll(__ballot(in) & lanes) != a.top_groups * a.lanes;
+    if (two) {
+      hard |= worst < next + (2 * GAP + 2);  // also where equal ones are all in, which then are too many: worst >= next
+      const uint64_t lanes = LPT == 64 ? ~0ull : 0xffffull << (threadIdx.x & 48);
+      hard |= __popcll(__ballot(in) & lanes) != a.top_groups * a.lanes;
+    } else if (__ballot((worst >> PB) < (next >> PB) + GAP) != 0) {
+      // equal logits without a bias have equal choices: near the border all have to be
+      const int to_border = int(score >> PB) - int(worst >> PB);
+      const bool at_border = sh.mine && to_border < GAP && to_border > -GAP;
+      hard |= at_border && !(a.bias == nullptr && element(row + place_of(k0)) == element(row + place_of(worst)));
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) key[i] = in ? key[i] : 0u;
-    kept = in;
+    full &= in;
   }
   uint32_t won = 0, loser = 0;
-  for (int k = 0; k <= a.K; ++k) {
+  auto pop = [&](int k) __attribute__((always_inline)) {
     loser = token_max<LPT>(key[0]);
     if (sh.l == k) won = loser;
     // one bit-field insert a key; a select of two of them becomes a search through the array
     const uint32_t next = key[0] == loser ? ~0u : 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) key[i] = ((i + 1 < N ? key[i + 1] : 0u) & next) | (key[i] & ~next);
-  }
-  bad |= full && kept && key[0] == 0;  // more than eight of one lane's: the others are not known
-  at = int(PLACES - (won & PLACES));
-  at = at < a.E ? at : 0;
-  x = element(row + at);
-  uint32_t behind;
-  float x_behind;
-  if constexpr (LPT == 16) {  // the next lane's
-    behind = uint32_t(__builtin_amdgcn_update_dpp(0, int(won), 0x101, 0xF, 0xF, false));  // row_shl:1
-    x_behind = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x101, 0xF, 0xF, false));
-  } else {
-    behind = __shfl_down(won, 1, 64);
-    x_behind = __shfl_down(x, 1, 64);
-  }
-  if (sh.l == a.K - 1) {
-    behind = loser;
-    const int other = int(PLACES - (loser & PLACES));
-    x_behind = element(row + (other < a.E ? other : 0));
-  }
-  // equal logits without a bias have equal choices, whose places decide
-  const bool near = behind != 0 && (won >> PB) < (behind >> PB) + GAP && !(a.bias == nullptr && x == x_behind);
-  bad |= sh.l < a.K && near;
-  return __ballot(bad) == 0;
+  };
+  for (int k = 0; k <= a.K; ++k) pop(k);
+  out.at = place_of(won);
+  out.x = element(row + out.at);
+  out.slot = sh.l;
+  // Whether the candidate of a lane below n is near the next one (`loser` behind lane n - 1's); of equal logits without
+  // a bias the place decides.
+  auto near = [&](int n) {
+    uint32_t behind;
+    float x_behind;
+    if constexpr (LPT == 16) {
+      behind = uint32_t(__builtin_amdgcn_update_dpp(0, int(won), 0x101, 0xF, 0xF, true));  // row_shl:1: the next lane's
+      x_behind = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(out.x), 0x101, 0xF, 0xF, true));
+    } else {
+      behind = __shfl_down(won, 1, 64);
+      x_behind = __shfl_down(out.x, 1, 64);
+    }
+    if (sh.l == n - 1) {
+      behind = loser;
+      if (a.bias == nullptr) x_behind = element(row + place_of(loser));
+    }
+    return sh.l < n && behind != 0 && (won >> PB) < (behind >> PB) + GAP && !(a.bias == nullptr && out.x == x_behind);
+  };
+  const bool close = near(a.K);
+  hard |= full && key[0] == 0;
+  if (__ballot(hard) != 0 || (__ballot(close) != 0 && a.softmax)) return false;
+  if (__ballot(close) == 0) return true;
+  // Sigmoid scores: K and three more candidates, if the next one is clear of them, by 64-bit keys.
+  const int n = min(a.K + 3, LPT);
+  for (int k = a.K + 1; k <= n; ++k) pop(k);
+  out.at = place_of(won);
+  out.x = element(row + out.at);
+  const bool last = near(n) && sh.l == n - 1;
+  if (__ballot(last || (full && key[0] == 0)) != 0) return false;
+  double s = sigmoid64(out.x);
+  if (a.bias != nullptr) s += double(a.bias[out.at]);
+  const double own = sh.l < n && won != 0 ? make_key(float(s), out.at) : 0.;
+  out.slot = 0;
+  for (int j = 0; j < n; ++j) out.slot += __shfl(own, (int(threadIdx.x) & 63 & ~(LPT - 1)) + j, 64) > own ? 1 : 0;
+  if (own == 0.) out.slot = a.K;
+  return true;
 }
 
 // The choice by 64-bit keys, one maximum over the lane's values a slot.
-template <class Z, int LPT, int VPL>
-__device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LPT>& sh, const Z* row, int& at, float& x) {
+template <bool RAGGED, class Z, int LPT, int VPL>
+__device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LPT>& sh, const Z* row, Choice& out) {
   float z[VPL];
-  load_logits(a, sh, row, z);
+  load_logits<RAGGED>(a, sh, row, z);
   double key[VPL];
   if (a.softmax) {
     float m = -INFINITY;
@@ -425,7 +473,7 @@ __device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LP
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = sh.place(a, i), to = sh.g * a.each + e;
-    const bool is = sh.mine && e < a.each;
+    const bool is = !RAGGED || (sh.mine && e < a.each);
     double s = key[i];
     if (a.bias != nullptr && is) s += double(a.bias[to]);
     const float c = z[i] == -INFINITY ? -FLT_MAX : fmaxf(float(s), -FLT_MAX);
@@ -466,31 +514,33 @@ __device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LP
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = key[i] == top ? 0. : key[i];
   }
-  at = sh.l < a.K ? key_place(won) : 0;
-  x = element(row + at);
+  out.at = sh.l < a.K ? key_place(won) : 0;
+  out.x = element(row + out.at);
+  out.slot = sh.l;
 }
 
-template <class Z, int LPT, int VPL>
+template <class Z, int LPT, int VPL, bool RAGGED>
 __global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int32_t* __restrict__ topk_idx,
                                                                 float* __restrict__ topk_w) {
   constexpr int TOKENS = kGateThreads / LPT;
   const Share<LPT> sh(a);
   const int64_t t = int64_t(blockIdx.x) * TOKENS + threadIdx.x / LPT;
-  const bool there = t < a.T;  // lanes behind the last token go along with it
-  const Z* row = static_cast<const Z*>(a.z) + (there ? t : a.T - 1) * a.ld;
-  int at;
-  float x, m = 0.f, inv = 1.f;
-  if (!choose_fixed<Z, LPT, VPL>(a, sh, row, at, x, m, inv)) choose_exactly<Z, LPT, VPL>(a, sh, row, at, x);
+  // lanes behind the last token go along with it
+  const Z* row = static_cast<const Z*>(a.z) + (t < a.T ? t : a.T - 1) * a.ld;
+  Choice ch;
+  float m = 0.f, inv = 1.f;
+  if (!choose_fixed<RAGGED, Z, LPT, VPL>(a, sh, row, ch, m, inv)) choose_exactly<RAGGED, Z, LPT, VPL>(a, sh, row, ch);
+  const bool chosen = ch.slot < a.K;
   double s = 0.;
-  if (sh.l < a.K) s = a.softmax ? (x == -INFINITY ? 0. : exp64(double(x) - double(m))) : sigmoid64(x);
+  if (chosen) s = a.softmax ? (ch.x == -INFINITY ? 0. : exp64(double(ch.x) - double(m))) : sigmoid64(ch.x);
   if (a.softmax && (!a.renorm || !(inv < INFINITY))) s *= inv == INFINITY ? 0. : double(inv);  // a row of only -inf, a NaN
   if (a.renorm) {
     const double sum = token_sum<LPT>(s);
-    s = sum == 0. ? 0. : s / sum;
+    s = sum == 0. ? 0. : s * (sum > 1e-300 ? inverse64(sum) : 1. / sum);
   }
-  if (sh.l < a.K && there) {
-    topk_idx[t * a.K + sh.l] = at;
-    topk_w[t * a.K + sh.l] = float(s * double(a.scale));
+  if (chosen && t < a.T) {
+    topk_idx[t * a.K + ch.slot] = ch.at;
+    topk_w[t * a.K + ch.slot] = float(s * double(a.scale));
   }
 }
 
@@ -696,9 +746,13 @@ int moe_gate_fwd(const moe_gate_desc* d, const void* logits, const float* bias, 
   prof_begin("gate_fwd", s);
   with_lanes(lpt, values_a_lane(a.each, a.lanes), [&](auto l, auto v) {
     constexpr int LPT = decltype(l)::value, VPL = decltype(v)::value;
-    if (d->in_type == MOE_TYPE_F32) gate_fwd_kernel<float, LPT, VPL><<<grid, kGateThreads, 0, s>>>(a, topk_idx, topk_w);
-    else gate_fwd_kernel<uint16_t, LPT, VPL><<<grid, kGateThreads, 0, s>>>(a, topk_idx, topk_w);
-    return 0;
+    auto go = [&](auto z, auto ragged) {
+      gate_fwd_kernel<decltype(z), LPT, VPL, decltype(ragged)::value><<<grid, kGateThreads, 0, s>>>(a, topk_idx, topk_w);
+      return 0;
+    };
+    if (a.each == a.lanes * VPL && gp == a.groups)
+      return d->in_type == MOE_TYPE_F32 ? go(float(), std::false_type{}) : go(uint16_t(), std::false_type{});
+    return d->in_type == MOE_TYPE_F32 ? go(float(), std::true_type{}) : go(uint16_t(), std::true_type{});
   });
   prof_end(s);
   return launched();
