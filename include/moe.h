@@ -516,8 +516,9 @@ int moe_block_mm(const moe_block_mm_desc* m, const void* a, const float* a_scale
 /* What lies between two blocks: the end of one (its output b, normed and gated, added to the
  * residual) and the norm ahead of the next, in one pass.  Per row t of D values:
  *   u = b, or with w_post  b / sqrt(mean(b^2) + eps) * w_post;
- *   h = r + scale u, or with gate  r + scale sigmoid(gate_t) u, rounded to fp32 and
- *   then to res_type (exact before that rounding but for some 2^-50 of its terms);
+ *   h = r + scale u, or with gate  r + scale sigmoid(gate_t) u, rounded to fp32 and then to
+ *   res_type: exactly that without gate and w_post; with them it is computed in 64 bits for
+ *   res_type MOE_TYPE_BF16, in fp32 (row sums too) for MOE_TYPE_F32;
  *   y = h / sqrt(mean(h^2) + eps) * w of the h that is stored, in fp32, rounded once.
  * b may be NULL (then gate and w_post are too, h = r and `h` may be NULL: a norm by
  * itself), and so may w and y together (the residual sum by itself; then b is not). */

@@ -99,42 +99,6 @@ __device__ __forceinline__ Coef coefficients(const AdamStep& s) {
   return k;
 }
 
-template <bool STREAM>
-__device__ __forceinline__ uint4 fetch16(const void* p) {
-  typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
-  if constexpr (STREAM) {
-    const any_u32x4 v = __builtin_nontemporal_load(static_cast<const any_u32x4*>(p));
-    return make_uint4(v.x, v.y, v.z, v.w);
-  } else {
-    return load16(p);
-  }
-}
-template <bool STREAM>
-__device__ __forceinline__ uint2 fetch8(const void* p) {
-  typedef uint32_t any_u32x2 __attribute__((ext_vector_type(2), aligned(2)));
-  any_u32x2 v;
-  if constexpr (STREAM) v = __builtin_nontemporal_load(static_cast<const any_u32x2*>(p));
-  else v = *static_cast<const any_u32x2*>(p);
-  return make_uint2(v.x, v.y);
-}
-template <bool STREAM>
-__device__ __forceinline__ void keep8(void* p, const uint2& a) {
-  typedef uint32_t any_u32x2 __attribute__((ext_vector_type(2), aligned(2)));
-  const any_u32x2 v = {a.x, a.y};
-  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<any_u32x2*>(p));
-  else *static_cast<any_u32x2*>(p) = v;
-}
-template <bool STREAM>
-__device__ __forceinline__ void keep16(void* p, const uint4& a) {
-  typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
-  if constexpr (STREAM) {
-    const any_u32x4 v = {a.x, a.y, a.z, a.w};
-    __builtin_nontemporal_store(v, static_cast<any_u32x4*>(p));
-  } else {
-    store16(p, a);
-  }
-}
-
 // N neighbouring elements (4 or 8) from p, `n` of which are there (zeros behind them).
 template <class T, int N>
 struct Piece {

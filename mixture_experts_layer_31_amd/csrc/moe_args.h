@@ -1,5 +1,6 @@
 // Argument checks and small device helpers shared by the operators around the
-// layer (moe_balance.hip, moe_block.hip, moe_clip.hip).
+// layer (moe_balance.hip, moe_gate.hip, moe_block.hip, moe_norm.hip, moe_clip.hip,
+// moe_adamw.hip).
 #pragma once
 
 #include "moe_common.h"
@@ -70,6 +71,36 @@ struct RowPiece {
 };
 __device__ __forceinline__ void store16(void* p, const uint4& a) {
   *static_cast<Bytes16*>(p) = Bytes16{{a.x, a.y, a.z, a.w}};
+}
+// Sixteen and eight bytes at any element's address; STREAM: nontemporal, for data touched once
+// per pass that no cache holds until its next use.
+typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t any_u32x2 __attribute__((ext_vector_type(2), aligned(2)));
+template <bool STREAM>
+__device__ __forceinline__ uint4 fetch16(const void* p) {
+  any_u32x4 v;
+  if constexpr (STREAM) v = __builtin_nontemporal_load(static_cast<const any_u32x4*>(p));
+  else v = *static_cast<const any_u32x4*>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool STREAM>
+__device__ __forceinline__ uint2 fetch8(const void* p) {
+  any_u32x2 v;
+  if constexpr (STREAM) v = __builtin_nontemporal_load(static_cast<const any_u32x2*>(p));
+  else v = *static_cast<const any_u32x2*>(p);
+  return make_uint2(v.x, v.y);
+}
+template <bool STREAM>
+__device__ __forceinline__ void keep16(void* p, const uint4& a) {
+  const any_u32x4 v = {a.x, a.y, a.z, a.w};
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<any_u32x4*>(p));
+  else *static_cast<any_u32x4*>(p) = v;
+}
+template <bool STREAM>
+__device__ __forceinline__ void keep8(void* p, const uint2& a) {
+  const any_u32x2 v = {a.x, a.y};
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<any_u32x2*>(p));
+  else *static_cast<any_u32x2*>(p) = v;
 }
 
 }  // namespace moe

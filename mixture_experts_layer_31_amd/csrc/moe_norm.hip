@@ -3,7 +3,7 @@
 //
 // Both are bound by memory: four arrays of rows forward (b, r in, h, y out), six
 // backward (b, h, dy, dh in, db, dr out).  A row stays in the registers of its WAVES waves, eight
-// neighbouring values a lane and piece: it is read once, its sums are joined over the
+// or four neighbouring values a lane and piece: it is read once, its sums are joined over the
 // lanes and, past one wave, through LDS, and what depends on them is computed from the
 // registers.  The weights of a lane's columns stay in registers over the rows that a workgroup takes,
 // and so do its parts of dw and dw_post, which go to the scratch as one row a workgroup; a second launch
@@ -11,8 +11,9 @@
 //
 // Sums.  With e = w dy, q = 1 / rms(h): dh' = q (e - h q^2 mean(e h)), so sum h^2, sum e h and sum b^2 are
 // joined together; only sum g w_post b, of the finished gradient g, needs a second join.
-// h with a gate or w_post is computed in 64 bits: kept in bf16, a value next to a border
-// goes one way or the other, and an fp32 sum of squares decides that for one value in 2^15.
+// h with a gate or w_post is computed in 64 bits where it is kept in bf16: there a value next to a border goes one
+// way or the other, and an fp32 sum of squares would decide that for one value in 2^15.
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -23,7 +24,6 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxD = 16384;
-constexpr int kNormPartials = 1024;  // workgroups, so rows of the scratch, of a backward
 
 struct NormArgs {
   const void *b, *r, *w_post, *w;
@@ -38,8 +38,6 @@ struct NormArgs {
   bool w_f32;
 };
 
-__device__ __forceinline__ float one(const float* p) { return *p; }
-__device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float(uint32_t(*p) << 16); }
 __device__ __forceinline__ void put_one(float* p, float f) { *p = f; }
 __device__ __forceinline__ void put_one(uint16_t* p, float f) { *p = uint16_t(pack_bf16x2(f, 0.f)); }
 // A value as its type keeps it.
@@ -48,113 +46,187 @@ __device__ __forceinline__ float kept(const uint16_t*, float f) {
   return __uint_as_float(pack_bf16x2(f, 0.f) << 16);
 }
 
-__device__ __forceinline__ void whole8(const float* p, float (&f)[8]) {
-  const uint4 a = load16(p), b = load16(p + 4);
-  f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-  f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-}
-__device__ __forceinline__ void whole8(const uint16_t* p, float (&f)[8]) {
-  const uint4 v = load16(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// P values c .. c + P - 1 of a row of D (zeros behind its end) as they are stored, and their store.  Of fp32 rows P is
+// 4: pieces of 8 are two loads of 16 bytes that each touch half of every line (1363 x 1001 forward and backward 23.5 us,
+// so 22.7); beside bf16 rows, whose loads would have 8 bytes, it is 8 (16384 x 4096: 364 us, with 4 386).
+template <class T, int P>
+struct Piece {
+  static constexpr int W = P * int(sizeof(T)) / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void get(const T* row, int c, int D) {
+    if (c + P <= D) {
+      if constexpr (W == 2) {
+        const uint2 v = fetch8<false>(row + c);
+        w[0] = v.x; w[1] = v.y;
+      } else {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        for (int k = 0; k < W / 4; ++k) {
+          const uint4 v = load16(row + c + k * 16 / sizeof(T));
+          w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+        }
+      }
+    } else {
+      clear();
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (c + i < D) {
+          if constexpr (sizeof(T) == 2) w[i / 2] |= uint32_t(row[c + i]) << (16 * (i & 1));
+          else w[i] = __float_as_uint(row[c + i]);
+        }
+    }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = 0;
+  }
+  __device__ __forceinline__ void values(float (&f)[P]) const {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        f[2 * k] = __uint_as_float(w[k] << 16);
+        f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k) f[k] = __uint_as_float(w[k]);
+    }
+  }
+};
+template <class T, int P>
+__device__ __forceinline__ void get(const T* row, int c, int D, float (&f)[P]) {
+  Piece<T, P> e;
+  e.get(row, c, D);
+  e.values(f);
 }
-__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
-  store16(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
-  store16(p + 4, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
-}
-__device__ __forceinline__ void put8(uint16_t* p, const float (&f)[8]) {
-  store16(p, make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                        pack_bf16x2(f[6], f[7])));
-}
-
-// Values c .. c + 7 of a row of D (zeros behind its end), and their store.
-template <class T>
-__device__ __forceinline__ void get(const T* row, int c, int D, float (&f)[8]) {
-  if (c + 8 <= D) {
-    whole8(row + c, f);
+template <class T, int P>
+__device__ __forceinline__ void put(T* row, int c, int D, const float (&f)[P]) {
+  constexpr int W = P * int(sizeof(T)) / 4;
+  if (c + P <= D) {
+    uint32_t w[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if constexpr (sizeof(T) == 2) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+      else w[k] = __float_as_uint(f[k]);
+    }
+    if constexpr (W == 2) {
+      keep8<false>(row + c, make_uint2(w[0], w[1]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < W / 4; ++k)
+        store16(row + c + k * 16 / sizeof(T), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < D ? one(row + c + i) : 0.f;
-  }
-}
-template <class T>
-__device__ __forceinline__ void put(T* row, int c, int D, const float (&f)[8]) {
-  if (c + 8 <= D) {
-    put8(row + c, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < P; ++i)
       if (c + i < D) put_one(row + c + i, f[i]);
   }
 }
-__device__ __forceinline__ void get_weight(const void* w, bool f32, int c, int D, float (&f)[8]) {
+template <int P>
+__device__ __forceinline__ void get_weight(const void* w, bool f32, int c, int D, float (&f)[P]) {
   if (f32) get(static_cast<const float*>(w), c, D, f);
   else get(static_cast<const uint16_t*>(w), c, D, f);
 }
 
+// Sum over the wave by lane moves of the vector ALU (a shuffle through the LDS crossbar costs ten times as long, and
+// a row has two to six of them on its way): within sixteen lanes, then row by row into the last lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(b), CTRL, ROWS, 0xF, false));
+  const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(b >> 32), CTRL, ROWS, 0xF, false));
+  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(b), 63)), hi = uint32_t(__builtin_amdgcn_readlane(int(b >> 32), 63));
+  return __longlong_as_double((long long)((uint64_t(hi) << 32) | lo));
+}
 template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  v += moved<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
+  v += moved<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
+  v += moved<0x141, 0xF>(v);  // row_half_mirror
+  v += moved<0x140, 0xF>(v);  // row_mirror
+  v += moved<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v += moved<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+  return last_lane(v);
 }
 
-// Sums over a row's waves.  `red` is used by one join at a time: a join writes one half and
-// reads it behind one barrier, the next join of the workgroup uses the other half.
+// Sums over a row's waves; `row` is the workgroup's row that this wave belongs to.  A join writes one half of `red`
+// and reads it behind one barrier, the next join of the workgroup uses the other half.
 template <int WAVES, int N, class V>
-__device__ __forceinline__ void row_sums(V (&v)[N], double (*red)[WAVES][3], int& half) {
+__device__ __forceinline__ void row_sums(V (&v)[N], double (*red)[4 / WAVES + 1][WAVES][3], int row, int& half) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (WAVES > 1) {
-    const int wv = threadIdx.x >> 6;
+    const int wv = (threadIdx.x >> 6) % WAVES;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) red[half][wv][i] = double(v[i]);
+      for (int i = 0; i < N; ++i) red[half][row][wv][i] = double(v[i]);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       double s = 0.;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) s += red[half][w][i];
+      for (int w = 0; w < WAVES; ++w) s += red[half][row][w][i];
       v[i] = V(s);
     }
     half ^= 1;
   }
 }
 
+__device__ __forceinline__ float fma_of(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ double fma_of(double a, double b, double c) { return __builtin_fma(a, b, c); }
+__device__ __forceinline__ float sigmoid_times(float s, float z) { return s / (1.f + expf(-z)); }
+__device__ __forceinline__ double sigmoid_times(double s, float z) { return s / (1. + exp(-double(z))); }
+__device__ __forceinline__ float inverse_root(float x) { return 1.f / sqrtf(x); }
+// The hardware's 2^-24 and two steps of Newton's: 2^-50.
+__device__ __forceinline__ double inverse_root(double x) {
+  double r = __builtin_amdgcn_rsq(x);
+  r = r * __builtin_fma(-0.5 * x * r, r, 1.5);
+  return r * __builtin_fma(-0.5 * x * r, r, 1.5);
+}
+
 // What enters the residual: nothing (h = r), scale b, or b with its norm or gate.
 enum { BLOCK_NONE = 0, BLOCK_SUM = 1, BLOCK_NORM = 2 };
 
-// Threads of a workgroup whose rows take WAVES waves: one row a workgroup, or four of one wave each.
-constexpr int norm_threads(int waves) { return waves == 1 ? 256 : 64 * waves; }
+// Rows and threads of a workgroup whose rows take that many waves: four waves at least.
+constexpr int norm_rows(int waves) { return waves < 4 ? 4 / waves : 1; }
+constexpr int norm_threads(int waves) { return 64 * waves * norm_rows(waves); }
 
-template <class IO, class R, int BLOCK, int WAVES, int NV>
+template <class IO, class R>
+constexpr int piece_of() { return sizeof(IO) + sizeof(R) == 8 ? 4 : 8; }
+
+template <class IO, class R, int BLOCK, int WAVES, int EIGHTS>
 __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs a) {
-  constexpr int ROWS = WAVES == 1 ? 4 : 1;
-  __shared__ double red[2][WAVES][3];
+  constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(WAVES);
+  __shared__ double red[2][4 / WAVES + 1][WAVES][3];
   int half = 0;
-  const int tid = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int D = a.D;
-  float w[NV][8], wp[NV][8];
+  const int tid = threadIdx.x % (64 * WAVES), row = threadIdx.x / (64 * WAVES), D = a.D;
+  float w[NV][P], wp[NV][P];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = 8 * (tid + 64 * WAVES * k);
+    const int c = P * (tid + 64 * WAVES * k);
     if (a.w != nullptr) get_weight(a.w, a.w_f32, c, D, w[k]);
     if (BLOCK == BLOCK_NORM && a.w_post != nullptr) get_weight(a.w_post, a.w_f32, c, D, wp[k]);
   }
-  for (int64_t t = int64_t(blockIdx.x) * ROWS + (WAVES == 1 ? threadIdx.x >> 6 : 0); t < a.T;
-       t += int64_t(gridDim.x) * ROWS) {
-    const IO* b = static_cast<const IO*>(a.b) + t * a.ld_b;
-    const R* r = static_cast<const R*>(a.r) + t * a.ld_r;
-    float x[NV][8], bv[NV][8];
+  for (int64_t first = int64_t(blockIdx.x) * ROWS; first < a.T; first += int64_t(gridDim.x) * ROWS) {
+    const int64_t t = first + row;
+    const bool there = t < a.T;  // a row behind the last one goes along with it
+    const R* r = static_cast<const R*>(a.r) + (there ? t : first) * a.ld_r;
+    const IO* b = static_cast<const IO*>(a.b) + (there ? t : first) * a.ld_b;
+    float x[NV][P], bv[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (tid + 64 * WAVES * k);
+      const int c = P * (tid + 64 * WAVES * k);
       get(r, c, D, x[k]);
       if (BLOCK != BLOCK_NONE) get(b, c, D, bv[k]);
     }
@@ -162,130 +234,150 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs 
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = __builtin_fmaf(a.scale, bv[k][i], x[k][i]);
+        for (int i = 0; i < P; ++i) x[k][i] = __builtin_fmaf(a.scale, bv[k][i], x[k][i]);
     } else if constexpr (BLOCK == BLOCK_NORM) {
-      double by = double(a.scale);
-      if (a.gate != nullptr) by /= 1. + exp(-double(a.gate[t]));
+      using V = std::conditional_t<sizeof(R) == 2, double, float>;  // see above
+      V by = V(a.scale);
+      if (a.gate != nullptr) by = sigmoid_times(by, a.gate[there ? t : 0]);
       if (a.w_post != nullptr) {
-        double sum[1] = {0.};
+        V sum[1] = {V(0)};
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[0] = __builtin_fma(double(bv[k][i]), double(bv[k][i]), sum[0]);
-        row_sums<WAVES>(sum, red, half);
-        by /= sqrt(sum[0] / D + double(a.eps));
+          for (int i = 0; i < P; ++i) sum[0] = fma_of(V(bv[k][i]), V(bv[k][i]), sum[0]);
+        row_sums<WAVES>(sum, red, row, half);
+        by *= inverse_root(sum[0] / V(D) + V(a.eps));
       }
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          double u = double(bv[k][i]);
-          if (a.w_post != nullptr) u *= double(wp[k][i]);  // exact
-          x[k][i] = float(__builtin_fma(by, u, double(x[k][i])));
+        for (int i = 0; i < P; ++i) {
+          V u = V(bv[k][i]);
+          if (a.w_post != nullptr) u *= V(wp[k][i]);  // exact in 64 bits
+          x[k][i] = float(fma_of(by, u, V(x[k][i])));
         }
     }
     float sum[1] = {0.f};
     R* h = static_cast<R*>(a.h) + t * a.ld_h;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (tid + 64 * WAVES * k);
-      if (a.h != nullptr) put(h, c, D, x[k]);
+      const int c = P * (tid + 64 * WAVES * k);
+      if (a.h != nullptr && there) put(h, c, D, x[k]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < P; ++i) {
         x[k][i] = kept(h, x[k][i]);
         sum[0] = __builtin_fmaf(x[k][i], x[k][i], sum[0]);
       }
     }
     if (a.w == nullptr) continue;
-    row_sums<WAVES>(sum, red, half);
+    row_sums<WAVES>(sum, red, row, half);
     const float q = 1.f / sqrtf(sum[0] / float(D) + a.eps);
     IO* y = static_cast<IO*>(a.y) + t * a.ld_y;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      float o[8];
+      float o[P];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = x[k][i] * q * w[k][i];
-      put(y, 8 * (tid + 64 * WAVES * k), D, o);
+      for (int i = 0; i < P; ++i) o[i] = x[k][i] * q * w[k][i];
+      if (there) put(y, P * (tid + 64 * WAVES * k), D, o);
     }
   }
 }
 
-// One row a workgroup at a time.
-template <class IO, class R, int BLOCK, int WAVES, int NV>
-__global__ void __launch_bounds__(64 * WAVES) norm_bwd_kernel(NormArgs a) {
-  __shared__ double red[2][WAVES][3];
+template <class IO, class R, int BLOCK, int WAVES, int EIGHTS>
+__global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs a) {
+  constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(WAVES);
+  __shared__ double red[2][4 / WAVES + 1][WAVES][3];
   int half = 0;
-  const int tid = threadIdx.x, D = a.D;
+  const int tid = threadIdx.x % (64 * WAVES), row = threadIdx.x / (64 * WAVES), D = a.D;
   const bool pre = a.w != nullptr, post = BLOCK == BLOCK_NORM && a.w_post != nullptr;
-  float w[NV][8], wp[NV][8];
-  double acc[NV][8], acc_post[NV][8];
+  float w[NV][P], wp[NV][P];
+  double acc[NV][P], acc_post[NV][P];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = 8 * (tid + 64 * WAVES * k);
+    const int c = P * (tid + 64 * WAVES * k);
     if (pre) get_weight(a.w, a.w_f32, c, D, w[k]);
     if (post) get_weight(a.w_post, a.w_f32, c, D, wp[k]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < P; ++i) {
       acc[k][i] = acc_post[k][i] = 0.;
       if (!post) wp[k][i] = 1.f;
     }
   }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const IO* b = static_cast<const IO*>(a.b) + t * a.ld_b;
-    const IO* dy = static_cast<const IO*>(a.dy) + t * a.ld_y;
-    const R* h = static_cast<const R*>(a.h) + t * a.ld_h;
-    const R* dh = static_cast<const R*>(a.dh) + t * a.ld_h;
-    float g[NV][8], x[NV][8], e[NV][8], bv[NV][8];
+  // a row ahead; a row behind the last one is a row of zeros
+  struct Row {
+    Piece<IO, P> b[NV], dy[NV];
+    Piece<R, P> h[NV], dh[NV];
+  } next;
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = P * (tid + 64 * WAVES * k);
+      next.b[k].clear(); next.dy[k].clear(); next.h[k].clear(); next.dh[k].clear();
+      if (t >= a.T) continue;
+      if (a.dh != nullptr) next.dh[k].get(static_cast<const R*>(a.dh) + t * a.ld_h, c, D);
+      if (pre && a.dy != nullptr) {
+        next.h[k].get(static_cast<const R*>(a.h) + t * a.ld_h, c, D);
+        next.dy[k].get(static_cast<const IO*>(a.dy) + t * a.ld_y, c, D);
+      }
+      if (BLOCK == BLOCK_NORM) next.b[k].get(static_cast<const IO*>(a.b) + t * a.ld_b, c, D);
+    }
+  };
+  const int64_t step = int64_t(gridDim.x) * ROWS;
+  fetch(int64_t(blockIdx.x) * ROWS + row);
+  for (int64_t first = int64_t(blockIdx.x) * ROWS; first < a.T; first += step) {
+    const int64_t t = first + row;
+    const bool there = t < a.T;
+    float g[NV][P], x[NV][P], e[NV][P], bv[NV][P];
     float sum[3] = {0.f, 0.f, 0.f};  // h^2, e h, b^2
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = 8 * (tid + 64 * WAVES * k);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[k][i] = x[k][i] = e[k][i] = 0.f;
-      if (a.dh != nullptr) get(dh, c, D, g[k]);
-      if (pre && a.dy != nullptr) {
-        get(h, c, D, x[k]);
-        get(dy, c, D, e[k]);
-      }
-      if (BLOCK == BLOCK_NORM) get(b, c, D, bv[k]);
+      next.dh[k].values(g[k]);
+      next.h[k].values(x[k]);
+      next.dy[k].values(e[k]);
+      if (BLOCK == BLOCK_NORM) next.b[k].values(bv[k]);
     }
+    if (first + step < a.T) fetch(t + step);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < P; ++i) {
         if (pre) {
           sum[0] = __builtin_fmaf(x[k][i], x[k][i], sum[0]);
           sum[1] = __builtin_fmaf(e[k][i] * w[k][i], x[k][i], sum[1]);
         }
         if (post) sum[2] = __builtin_fmaf(bv[k][i], bv[k][i], sum[2]);
       }
-    row_sums<WAVES>(sum, red, half);
-    if (pre && a.dy != nullptr) {
+    row_sums<WAVES>(sum, red, row, half);
+    if (pre && a.dy != nullptr && there) {
       const float q = 1.f / sqrtf(sum[0] / float(D) + a.eps);
       const float m = sum[1] / float(D) * q * q;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < P; ++i) {
           acc[k][i] += double(e[k][i] * (x[k][i] * q));
           g[k][i] = __builtin_fmaf(q, __builtin_fmaf(-x[k][i], m, e[k][i] * w[k][i]), g[k][i]);
         }
     }
     R* dr = static_cast<R*>(a.dr) + t * a.ld_r;
     IO* db = static_cast<IO*>(a.db) + t * a.ld_b;
+    if (there) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) put(dr, 8 * (tid + 64 * WAVES * k), D, g[k]);
+      for (int k = 0; k < NV; ++k) put(dr, P * (tid + 64 * WAVES * k), D, g[k]);
+    }
     if constexpr (BLOCK == BLOCK_SUM) {
+      if (there) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
+        for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[k][i] *= a.scale;
-        put(db, 8 * (tid + 64 * WAVES * k), D, g[k]);
+          for (int i = 0; i < P; ++i) g[k][i] *= a.scale;
+          put(db, P * (tid + 64 * WAVES * k), D, g[k]);
+        }
       }
     } else if constexpr (BLOCK == BLOCK_NORM) {
       float by = a.scale, rest = 0.f;
       if (a.gate != nullptr) {
-        const float z = a.gate[t];
+        const float z = a.gate[there ? t : 0];
         by = a.scale / (1.f + expf(-z));
         rest = 1.f / (1.f + expf(z));
       }
@@ -293,82 +385,99 @@ __global__ void __launch_bounds__(64 * WAVES) norm_bwd_kernel(NormArgs a) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot[0] = __builtin_fmaf(g[k][i] * wp[k][i], bv[k][i], dot[0]);
-      row_sums<WAVES>(dot, red, half);
-      const float p = post ? 1.f / sqrtf(sum[2] / float(D) + a.eps) : 1.f;
-      if (a.gate != nullptr && tid == 0) a.dgate[t] = by * rest * (dot[0] * p);
-      const float m = post ? dot[0] / float(D) * p * p : 0.f;
+        for (int i = 0; i < P; ++i) dot[0] = __builtin_fmaf(g[k][i] * wp[k][i], bv[k][i], dot[0]);
+      row_sums<WAVES>(dot, red, row, half);
+      if (there) {
+        const float p = post ? 1.f / sqrtf(sum[2] / float(D) + a.eps) : 1.f;
+        if (a.gate != nullptr && tid == 0) a.dgate[t] = by * rest * (dot[0] * p);
+        const float m = post ? dot[0] / float(D) * p * p : 0.f;
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        float o[8];
+        for (int k = 0; k < NV; ++k) {
+          float o[P];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (post) acc_post[k][i] += double(by * g[k][i] * (bv[k][i] * p));
-          o[i] = by * p * __builtin_fmaf(-bv[k][i], m, g[k][i] * wp[k][i]);
+          for (int i = 0; i < P; ++i) {
+            if (post) acc_post[k][i] += double(by * g[k][i] * (bv[k][i] * p));
+            o[i] = by * p * __builtin_fmaf(-bv[k][i], m, g[k][i] * wp[k][i]);
+          }
+          put(db, P * (tid + 64 * WAVES * k), D, o);
         }
-        put(db, 8 * (tid + 64 * WAVES * k), D, o);
       }
     }
   }
+  // the workgroup's rows, then its row of the scratch
+  auto store = [&](const double (&v)[NV][P], float* part) __attribute__((always_inline)) {
+    if constexpr (ROWS > 1) {
+      __shared__ double s[ROWS - 1][NV][P][64 * WAVES];
+      __syncthreads();
+      if (row > 0) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int c = 8 * (tid + 64 * WAVES * k);
-    float f[8];
-    if (pre) {
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = float(acc[k][i]);
-      put(a.part + size_t(blockIdx.x) * D, c, D, f);
+          for (int i = 0; i < P; ++i) s[row - 1][k][i][tid] = v[k][i];
+      }
+      __syncthreads();
+      if (row > 0) return;
+      float f[P];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          double sum = v[k][i];
+#pragma unroll
+          for (int r = 0; r < ROWS - 1; ++r) sum += s[r][k][i][tid];
+          f[i] = float(sum);
+        }
+        put(part + size_t(blockIdx.x) * D, P * (tid + 64 * WAVES * k), D, f);
+      }
+    } else {
+      float f[P];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = float(v[k][i]);
+        put(part + size_t(blockIdx.x) * D, P * (tid + 64 * WAVES * k), D, f);
+      }
     }
-    if (post) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = float(acc_post[k][i]);
-      put(a.part_post + size_t(blockIdx.x) * D, c, D, f);
-    }
-  }
+  };
+  if (pre) store(acc, a.part);
+  if (post) store(acc_post, a.part_post);
 }
 
-// The rows of the scratch, 64 columns a workgroup and 16 rows side by side.
+// The rows of the scratch, sixteen columns a workgroup: 64 rows side by side, four a wave.
 __global__ void __launch_bounds__(1024) norm_finish_kernel(const float* __restrict__ part, const float* __restrict__ part_post,
                                                            int rows, int D, float* __restrict__ dw,
                                                            float* __restrict__ dw_post) {
-  __shared__ double s[16][64];
-  const int l = threadIdx.x & 63, r = threadIdx.x >> 6, c = blockIdx.x * 64 + l;
+  __shared__ double s[16][16];
+  const int l = threadIdx.x & 15, c = blockIdx.x * 16 + l;
   const bool second = blockIdx.y == 1 || dw == nullptr;
   const float* in = second ? part_post : part;
   double v = 0.;
   if (c < D) {
 #pragma unroll 8
-    for (int k = r; k < rows; k += 16) v += double(in[size_t(k) * D + c]);
+    for (int k = threadIdx.x >> 4; k < rows; k += 64) v += double(in[size_t(k) * D + c]);
   }
-  s[r][l] = v;
+  v += __shfl_xor(v, 16, 64);
+  v += __shfl_xor(v, 32, 64);
+  if ((threadIdx.x & 63) < 16) s[threadIdx.x >> 6][l] = v;
   __syncthreads();
-  if (r != 0 || c >= D) return;
+  if (threadIdx.x >= 16 || c >= D) return;
 #pragma unroll
   for (int k = 1; k < 16; ++k) v += s[k][l];
   (second ? dw_post : dw)[c] = float(v);
 }
 
-// f(waves a row, pieces a lane) for a forward and for a backward row.
+// f(waves a row, eights of values a lane) for a row of D.
 template <class F>
-int with_row_fwd(int D, F&& f) {
-  using std::integral_constant;
-  if (D <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (D <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (D <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  if (D <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (D <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-}
-template <class F>
-int with_row_bwd(int D, F&& f) {
+int with_row(int D, F&& f) {
   using std::integral_constant;
   if (D <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
   if (D <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
   if (D <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
   if (D <= 4096) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (D <= 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (D <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
   return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
 }
+int rows_a_workgroup(int D) { return D <= 512 ? 4 : D <= 1024 ? 2 : 1; }
 // f(IO, R) by example.
 template <class F>
 int with_types(const moe_norm_desc& d, F&& f) {
@@ -420,7 +529,11 @@ int check_buffers(const Buffer* in, int n_in, const Buffer* out, int n_out, cons
   return MOE_OK;
 }
 
-int norm_partials(const moe_norm_desc& d) { return d.T < kNormPartials ? (d.T > 0 ? d.T : 1) : kNormPartials; }
+// Workgroups of a backward, so rows of the scratch: as many as there is room for (8 to 12 waves a CU).
+int norm_partials(const moe_norm_desc& d) {
+  const long long most = d.D <= 2048 ? 768 : 256, want = ceil_div(d.T, rows_a_workgroup(d.D));
+  return int(std::max(1ll, std::min(most, want)));
+}
 
 }  // namespace
 }  // namespace moe
@@ -448,12 +561,12 @@ int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const flo
   hipStream_t s = static_cast<hipStream_t>(stream);
   prof_begin("norm_fwd", s);
   with_types(*d, [&](auto io, auto res) {
-    return with_row_fwd(d->D, [&](auto waves, auto nv) {
+    return with_row(d->D, [&](auto waves, auto nv) {
       constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
       using IO = decltype(io);
       using R = decltype(res);
-      const long long want = ceil_div(d->T, W == 1 ? 4 : 1);
-      const unsigned grid = unsigned(want < 4096 ? want : 4096);
+      // a workgroup for each row or rows: 1024 that step through 16384 rows of 4096 take 383 us forward and backward, so 366
+      const unsigned grid = unsigned(std::min(ceil_div(d->T, norm_rows(W)), (1LL << 32) / norm_threads(W) - 1));
       if (b == nullptr) norm_fwd_kernel<IO, R, BLOCK_NONE, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
       else if (gate != nullptr || w_post != nullptr) norm_fwd_kernel<IO, R, BLOCK_NORM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
       else norm_fwd_kernel<IO, R, BLOCK_SUM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
@@ -506,13 +619,13 @@ int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const flo
   if (d->T > 0) {
     prof_begin("norm_bwd", s);
     with_types(*d, [&](auto io, auto res) {
-      return with_row_bwd(d->D, [&](auto waves, auto nv) {
+      return with_row(d->D, [&](auto waves, auto nv) {
         constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
         using IO = decltype(io);
         using R = decltype(res);
-        if (db == nullptr) norm_bwd_kernel<IO, R, BLOCK_NONE, W, NV><<<grid, 64 * W, 0, s>>>(a);
-        else if (block) norm_bwd_kernel<IO, R, BLOCK_NORM, W, NV><<<grid, 64 * W, 0, s>>>(a);
-        else norm_bwd_kernel<IO, R, BLOCK_SUM, W, NV><<<grid, 64 * W, 0, s>>>(a);
+        if (db == nullptr) norm_bwd_kernel<IO, R, BLOCK_NONE, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
+        else if (block) norm_bwd_kernel<IO, R, BLOCK_NORM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
+        else norm_bwd_kernel<IO, R, BLOCK_SUM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
         return 0;
       });
     });
@@ -521,7 +634,7 @@ int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const flo
   }
   if (dw == nullptr && dw_post == nullptr) return MOE_OK;
   prof_begin("norm_finish", s);
-  const dim3 blocks(unsigned(ceil_div(d->D, 64)), dw != nullptr && dw_post != nullptr ? 2 : 1);
+  const dim3 blocks(unsigned(ceil_div(d->D, 16)), dw != nullptr && dw_post != nullptr ? 2 : 1);
   norm_finish_kernel<<<blocks, 1024, 0, s>>>(a.part, a.part_post, d->T > 0 ? int(grid) : 0, d->D, dw, dw_post);
   prof_end(s);
   return launched();

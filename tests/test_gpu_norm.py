@@ -1,8 +1,9 @@
 """The residual sum with the norms on both of its sides on the GPU (through the C ABI) against the float64 oracle.
 
 Tolerances, u = 2^-24, half = 2^-8 for bf16 and u for fp32:
-* h: without gate and w_post one fused multiply-add, with them 64 bits: rounded to fp32 (u), then to its type
-  (half), 2^-45 of its terms' sizes for the 64-bit sums' sake;
+* h: without gate and w_post one fused multiply-add, with them 64 bits for a bf16 residual: rounded to fp32 (u), then to
+  its type (half), 2^-45 of its terms' sizes for the 64-bit sums' sake; with them and an fp32 residual in fp32: 1 / rms(b)
+  15 u as below, scale sigmoid(gate) 8 u, three products and the sum 4 u: 32 u of the sizes;
 * y, from the h that the call stored: a sum of squares adds at most 16 values a lane and 6 lane steps in fp32 (22 u,
   positive terms; waves are joined in 64 bits), mean, eps, root and reciprocal 4 u, so q = 1 / rms is off by 15 u
   and y = h q w by 17 u: 24 u, and half;
@@ -79,7 +80,8 @@ def _check(T, D, io=B, res=B, wt=F, block=True, post=False, gated=False, pre=Tru
     f = no.forward(_np(b), r0, _np(gate), _np(w_post), _np(w), np.float64(np.float32(eps)), np.float64(np.float32(scale)))
     if block:
         size = np.abs(r0) + np.abs(f["h"] - r0)
-        assert np.all(np.abs(_np(h) - f["h"]) <= (HALF[res] + U) * np.abs(f["h"]) * 1.01 + 2.0 ** -45 * size + TINY)
+        terms = 32 * U if res == F and (post or gated) else 2.0 ** -45
+        assert np.all(np.abs(_np(h) - f["h"]) <= (HALF[res] + U) * np.abs(f["h"]) * 1.01 + terms * size + TINY)
     kept = _np(h) if block else r0
     if pre:
         ref = no.forward(None, kept, None, None, _np(w), np.float64(np.float32(eps)), 0.0)["y"]
