@@ -290,13 +290,15 @@ struct Choice {
 // Errors, u = 2^-24: of a sigmoid's e^-z 3 u (its exponent is formed in two parts), 1 + e u, the reciprocal 2 u; of a
 // softmax's score 2 u + 0.6 u of the row's largest for the exp, 11 u for the sum by halves over VPL values and
 // the lanes, 3 u for the reciprocal and the product; 1 u each for the sum with the bias and the product with the unit's
-// reciprocal: below 20 u of M, the largest score or choice.  A unit of 2^-22 M is 4 u, so that keys
-// are off by 5 units and half a one for their rounding, the fp32 rounding of c a quarter: a difference of 13 units is
-// one of c's.  With units of 2^-20 M (16 u) one of 5 is.  The sums of two of a group twice that and an fp32 rounding.
+// reciprocal: below 8 u and 20 u of M, the largest score or choice.  A unit of 2^-22 M is 4 u, so that keys
+// are off by 2 or 5 units and half a one for their rounding, the fp32 rounding of c a quarter: a difference of 6 or 13
+// units is one of c's.  With units of 2^-20 M (16 u) one of 3 or 5 is.  The sums of two of a group twice that and two for an fp32
+// rounding.
 template <bool RAGGED, class Z, int LPT, int VPL>
 __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>& sh, const Z* row, Choice& out,
                                              float& m, float& inv) {
-  constexpr int PB = LPT == 16 ? 8 : 10, GAP = LPT == 16 ? 13 : 5, N = VPL < 8 ? VPL : 8;
+  constexpr int PB = LPT == 16 ? 8 : 10, N = VPL < 8 ? VPL : 8;
+  const int gap = LPT == 16 ? (a.softmax ? 13 : 6) : (a.softmax ? 5 : 3);
   constexpr uint32_t PLACES = (1u << PB) - 1;
   constexpr float TOP = LPT == 16 ? 4194304.f : 1048576.f;  // units of M
   constexpr float MAGIC = LPT == 16 ? 12582912.f : 13631488.f;  // 1.5 * 2^23 (+ TOP): an integer's bits are the low ones
@@ -381,13 +383,13 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
     const bool in = ahead < a.top_groups;
     const uint32_t worst = token_min<LPT>(in ? score : 0xffffffffu), next = token_max<LPT>(in ? 0u : score);
     if (two) {
-      hard |= worst < next + (2 * GAP + 2);  // also where equal ones are all in, which then are too many: worst >= next
+      hard |= worst < next + (2 * gap + 2);  // also where equal ones are all in, which then are too many: worst >= next
       const uint64_t lanes = LPT == 64 ? ~0ull : 0xffffull << (threadIdx.x & 48);
       hard |= __popcll(__ballot(in) & lanes) != a.top_groups * a.lanes;
-    } else if (__ballot((worst >> PB) < (next >> PB) + GAP) != 0) {
+    } else if (__ballot((worst >> PB) < (next >> PB) + gap) != 0) {
       // equal logits without a bias have equal choices: near the border all have to be
       const int to_border = int(score >> PB) - int(worst >> PB);
-      const bool at_border = sh.mine && to_border < GAP && to_border > -GAP;
+      const bool at_border = sh.mine && to_border < gap && to_border > -gap;
       hard |= at_border && !(a.bias == nullptr && element(row + place_of(k0)) == element(row + place_of(worst)));
     }
 #pragma unroll
@@ -423,7 +425,7 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
       behind = loser;
       if (a.bias == nullptr) x_behind = element(row + place_of(loser));
     }
-    return sh.l < n && behind != 0 && (won >> PB) < (behind >> PB) + GAP && !(a.bias == nullptr && out.x == x_behind);
+    return sh.l < n && behind != 0 && (won >> PB) < (behind >> PB) + gap && !(a.bias == nullptr && out.x == x_behind);
   };
   const bool close = near(a.K);
   hard |= full && key[0] == 0;
