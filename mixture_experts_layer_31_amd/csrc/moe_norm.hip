@@ -2,9 +2,9 @@
 // (moe_norm_fwd, moe_norm_bwd in moe.h).
 //
 // Both are bound by memory: four arrays of rows forward (b, r in, h, y out), six
-// backward (b, h, dy, dh in, db, dr out).  A row stays in the registers of its WAVES waves, eight
-// or four neighbouring values a lane and piece: it is read once, its sums are joined over the
-// lanes and, past one wave, through LDS, and what depends on them is computed from the
+// backward (b, h, dy, dh in, db, dr out).  A row stays in the registers of its TPR threads (16 of them for up to 128
+// values, 512 for 4096), eight or four neighbouring values a thread and piece: it is read once, its sums are joined over
+// the lanes and, past one wave, through LDS, and what depends on them is computed from the
 // registers.  The weights of a lane's columns stay in registers over the rows that a workgroup takes,
 // and so do its parts of dw and dw_post, which go to the scratch as one row a workgroup; a second launch
 // adds those rows in their order.
@@ -24,6 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kNormMaxD = 16384;
+constexpr int kFold = 16;  // rows
 
 struct NormArgs {
   const void *b, *r, *w_post, *w;
@@ -159,13 +160,37 @@ __device__ __forceinline__ V wave_sum(V v) {
   return last_lane(v);
 }
 
-// Sums over a row's waves; `row` is the workgroup's row that this wave belongs to.  A join writes one half of `red`
-// and reads it behind one barrier, the next join of the workgroup uses the other half.
-template <int WAVES, int N, class V>
-__device__ __forceinline__ void row_sums(V (&v)[N], double (*red)[4 / WAVES + 1][WAVES][3], int row, int& half) {
+// Sum over an aligned group of 16 or 32 lanes, in each of them.
+template <int LANES, class V>
+__device__ __forceinline__ V group_sum(V v) {
+  v += moved<0xB1, 0xF>(v);
+  v += moved<0x4E, 0xF>(v);
+  v += moved<0x141, 0xF>(v);
+  v += moved<0x140, 0xF>(v);
+  if constexpr (LANES == 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+
+// Rows of a workgroup whose rows take TPR threads: 256 threads at least.
+constexpr int norm_rows(int tpr) { return tpr < 256 ? 256 / tpr : 1; }
+constexpr int norm_threads(int tpr) { return tpr * norm_rows(tpr); }
+constexpr int norm_waves(int tpr) { return tpr > 64 ? tpr / 64 : 1; }
+
+// Sums over a row's threads; `row` is the workgroup's row that this thread belongs to.  A join of several waves writes one
+// half of `red` and reads it behind one barrier, the next join of the workgroup uses the other half.
+template <int TPR>
+using Joins = double[2][norm_rows(TPR)][norm_waves(TPR)][3];
+template <int TPR, int N, class V>
+__device__ __forceinline__ void row_sums(V (&v)[N], Joins<TPR>& red, int row, int& half) {
+  if constexpr (TPR < 64) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (WAVES > 1) {
+    for (int i = 0; i < N; ++i) v[i] = group_sum<TPR>(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  }
+  if constexpr (TPR > 64) {
+    constexpr int WAVES = TPR / 64;
     const int wv = (threadIdx.x >> 6) % WAVES;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
@@ -198,23 +223,19 @@ __device__ __forceinline__ double inverse_root(double x) {
 // What enters the residual: nothing (h = r), scale b, or b with its norm or gate.
 enum { BLOCK_NONE = 0, BLOCK_SUM = 1, BLOCK_NORM = 2 };
 
-// Rows and threads of a workgroup whose rows take that many waves: four waves at least.
-constexpr int norm_rows(int waves) { return waves < 4 ? 4 / waves : 1; }
-constexpr int norm_threads(int waves) { return 64 * waves * norm_rows(waves); }
-
 template <class IO, class R>
 constexpr int piece_of() { return sizeof(IO) + sizeof(R) == 8 ? 4 : 8; }
 
-template <class IO, class R, int BLOCK, int WAVES, int EIGHTS>
-__global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs a) {
-  constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(WAVES);
-  __shared__ double red[2][4 / WAVES + 1][WAVES][3];
+template <class IO, class R, int BLOCK, int TPR, int EIGHTS>
+__global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a) {
+  constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(TPR);
+  __shared__ Joins<TPR> red;
   int half = 0;
-  const int tid = threadIdx.x % (64 * WAVES), row = threadIdx.x / (64 * WAVES), D = a.D;
+  const int tid = threadIdx.x % TPR, row = threadIdx.x / TPR, D = a.D;
   float w[NV][P], wp[NV][P];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = P * (tid + 64 * WAVES * k);
+    const int c = P * (tid + TPR * k);
     if (a.w != nullptr) get_weight(a.w, a.w_f32, c, D, w[k]);
     if (BLOCK == BLOCK_NORM && a.w_post != nullptr) get_weight(a.w_post, a.w_f32, c, D, wp[k]);
   }
@@ -226,7 +247,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs 
     float x[NV][P], bv[NV][P];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = P * (tid + 64 * WAVES * k);
+      const int c = P * (tid + TPR * k);
       get(r, c, D, x[k]);
       if (BLOCK != BLOCK_NONE) get(b, c, D, bv[k]);
     }
@@ -245,7 +266,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs 
         for (int k = 0; k < NV; ++k)
 #pragma unroll
           for (int i = 0; i < P; ++i) sum[0] = fma_of(V(bv[k][i]), V(bv[k][i]), sum[0]);
-        row_sums<WAVES>(sum, red, row, half);
+        row_sums<TPR>(sum, red, row, half);
         by *= inverse_root(sum[0] / V(D) + V(a.eps));
       }
 #pragma unroll
@@ -261,7 +282,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs 
     R* h = static_cast<R*>(a.h) + t * a.ld_h;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = P * (tid + 64 * WAVES * k);
+      const int c = P * (tid + TPR * k);
       if (a.h != nullptr && there) put(h, c, D, x[k]);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
@@ -270,7 +291,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs 
       }
     }
     if (a.w == nullptr) continue;
-    row_sums<WAVES>(sum, red, row, half);
+    row_sums<TPR>(sum, red, row, half);
     const float q = 1.f / sqrtf(sum[0] / float(D) + a.eps);
     IO* y = static_cast<IO*>(a.y) + t * a.ld_y;
 #pragma unroll
@@ -278,28 +299,44 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_fwd_kernel(NormArgs 
       float o[P];
 #pragma unroll
       for (int i = 0; i < P; ++i) o[i] = x[k][i] * q * w[k][i];
-      if (there) put(y, P * (tid + 64 * WAVES * k), D, o);
+      if (there) put(y, P * (tid + TPR * k), D, o);
     }
   }
 }
 
-template <class IO, class R, int BLOCK, int WAVES, int EIGHTS>
-__global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs a) {
-  constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(WAVES);
-  __shared__ double red[2][4 / WAVES + 1][WAVES][3];
+template <class IO, class R, int BLOCK, int TPR, int EIGHTS>
+__global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a) {
+  constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(TPR);
+  __shared__ Joins<TPR> red;
   int half = 0;
-  const int tid = threadIdx.x % (64 * WAVES), row = threadIdx.x / (64 * WAVES), D = a.D;
+  const int tid = threadIdx.x % TPR, row = threadIdx.x / TPR, D = a.D;
   const bool pre = a.w != nullptr, post = BLOCK == BLOCK_NORM && a.w_post != nullptr;
   float w[NV][P], wp[NV][P];
-  double acc[NV][P], acc_post[NV][P];
+  // parts of dw and dw_post: 64 bits, or (two eights a thread, where those do not fit the registers) fp32 over kFold rows,
+  // folded into 64 bits in LDS
+  constexpr bool FOLD = EIGHTS == 2 && TPR == 512;
+  using Acc = std::conditional_t<FOLD, float, double>;
+  Acc acc[NV][P], acc_post[NV][P];
+  __shared__ double kept_sums[FOLD ? 2 : 1][FOLD ? NV : 1][FOLD ? P : 1][FOLD ? TPR : 1];
+  auto fold = [&](Acc (&v)[NV][P], int which) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        kept_sums[which][k][i][tid] += double(v[k][i]);
+        v[k][i] = 0;
+      }
+  };
+  int since = 0;  // rows since the last fold
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = P * (tid + 64 * WAVES * k);
+    const int c = P * (tid + TPR * k);
     if (pre) get_weight(a.w, a.w_f32, c, D, w[k]);
     if (post) get_weight(a.w_post, a.w_f32, c, D, wp[k]);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      acc[k][i] = acc_post[k][i] = 0.;
+      acc[k][i] = acc_post[k][i] = 0;
+      if constexpr (FOLD) kept_sums[0][k][i][tid] = kept_sums[1][k][i][tid] = 0.;
       if (!post) wp[k][i] = 1.f;
     }
   }
@@ -311,7 +348,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
   auto fetch = [&](int64_t t) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = P * (tid + 64 * WAVES * k);
+      const int c = P * (tid + TPR * k);
       next.b[k].clear(); next.dy[k].clear(); next.h[k].clear(); next.dh[k].clear();
       if (t >= a.T) continue;
       if (a.dh != nullptr) next.dh[k].get(static_cast<const R*>(a.dh) + t * a.ld_h, c, D);
@@ -347,7 +384,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
         }
         if (post) sum[2] = __builtin_fmaf(bv[k][i], bv[k][i], sum[2]);
       }
-    row_sums<WAVES>(sum, red, row, half);
+    row_sums<TPR>(sum, red, row, half);
     if (pre && a.dy != nullptr && there) {
       const float q = 1.f / sqrtf(sum[0] / float(D) + a.eps);
       const float m = sum[1] / float(D) * q * q;
@@ -355,7 +392,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          acc[k][i] += double(e[k][i] * (x[k][i] * q));
+          acc[k][i] += Acc(e[k][i] * (x[k][i] * q));
           g[k][i] = __builtin_fmaf(q, __builtin_fmaf(-x[k][i], m, e[k][i] * w[k][i]), g[k][i]);
         }
     }
@@ -363,7 +400,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
     IO* db = static_cast<IO*>(a.db) + t * a.ld_b;
     if (there) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) put(dr, P * (tid + 64 * WAVES * k), D, g[k]);
+      for (int k = 0; k < NV; ++k) put(dr, P * (tid + TPR * k), D, g[k]);
     }
     if constexpr (BLOCK == BLOCK_SUM) {
       if (there) {
@@ -371,7 +408,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
         for (int k = 0; k < NV; ++k) {
 #pragma unroll
           for (int i = 0; i < P; ++i) g[k][i] *= a.scale;
-          put(db, P * (tid + 64 * WAVES * k), D, g[k]);
+          put(db, P * (tid + TPR * k), D, g[k]);
         }
       }
     } else if constexpr (BLOCK == BLOCK_NORM) {
@@ -386,7 +423,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < P; ++i) dot[0] = __builtin_fmaf(g[k][i] * wp[k][i], bv[k][i], dot[0]);
-      row_sums<WAVES>(dot, red, row, half);
+      row_sums<TPR>(dot, red, row, half);
       if (there) {
         const float p = post ? 1.f / sqrtf(sum[2] / float(D) + a.eps) : 1.f;
         if (a.gate != nullptr && tid == 0) a.dgate[t] = by * rest * (dot[0] * p);
@@ -396,18 +433,34 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
           float o[P];
 #pragma unroll
           for (int i = 0; i < P; ++i) {
-            if (post) acc_post[k][i] += double(by * g[k][i] * (bv[k][i] * p));
+            if (post) acc_post[k][i] += Acc(by * g[k][i] * (bv[k][i] * p));
             o[i] = by * p * __builtin_fmaf(-bv[k][i], m, g[k][i] * wp[k][i]);
           }
-          put(db, P * (tid + 64 * WAVES * k), D, o);
+          put(db, P * (tid + TPR * k), D, o);
         }
+      }
+    }
+    if constexpr (FOLD) {
+      if (++since == kFold) {
+        if (pre) fold(acc, 0);
+        if (post) fold(acc_post, 1);
+        since = 0;
       }
     }
   }
   // the workgroup's rows, then its row of the scratch
-  auto store = [&](const double (&v)[NV][P], float* part) __attribute__((always_inline)) {
-    if constexpr (ROWS > 1) {
-      __shared__ double s[ROWS - 1][NV][P][64 * WAVES];
+  auto store = [&](Acc (&v)[NV][P], int which, float* part) __attribute__((always_inline)) {
+    if constexpr (FOLD) {
+      fold(v, which);
+      float f[P];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) f[i] = float(kept_sums[which][k][i][tid]);
+        put(part + size_t(blockIdx.x) * D, P * (tid + TPR * k), D, f);
+      }
+    } else if constexpr (ROWS > 1) {
+      __shared__ double s[ROWS - 1][NV][P][TPR];
       __syncthreads();
       if (row > 0) {
 #pragma unroll
@@ -427,7 +480,7 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
           for (int r = 0; r < ROWS - 1; ++r) sum += s[r][k][i][tid];
           f[i] = float(sum);
         }
-        put(part + size_t(blockIdx.x) * D, P * (tid + 64 * WAVES * k), D, f);
+        put(part + size_t(blockIdx.x) * D, P * (tid + TPR * k), D, f);
       }
     } else {
       float f[P];
@@ -435,12 +488,12 @@ __global__ void __launch_bounds__(norm_threads(WAVES)) norm_bwd_kernel(NormArgs 
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int i = 0; i < P; ++i) f[i] = float(v[k][i]);
-        put(part + size_t(blockIdx.x) * D, P * (tid + 64 * WAVES * k), D, f);
+        put(part + size_t(blockIdx.x) * D, P * (tid + TPR * k), D, f);
       }
     }
   };
-  if (pre) store(acc, a.part);
-  if (post) store(acc_post, a.part_post);
+  if (pre) store(acc, 0, a.part);
+  if (post) store(acc_post, 1, a.part_post);
 }
 
 // The rows of the scratch, sixteen columns a workgroup: 64 rows side by side, four a wave.
@@ -466,18 +519,20 @@ __global__ void __launch_bounds__(1024) norm_finish_kernel(const float* __restri
   (second ? dw_post : dw)[c] = float(v);
 }
 
-// f(waves a row, eights of values a lane) for a row of D.
+// f(threads a row, eights of values a thread) for a row of D.
 template <class F>
 int with_row(int D, F&& f) {
   using std::integral_constant;
-  if (D <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-  if (D <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
-  if (D <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-  if (D <= 4096) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (D <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  if (D <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (D <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (D <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (D <= 1024) return f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  if (D <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (D <= 4096) return f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
+  if (D <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
 }
-int rows_a_workgroup(int D) { return D <= 512 ? 4 : D <= 1024 ? 2 : 1; }
+int rows_a_workgroup(int D) { return D <= 128 ? 16 : D <= 256 ? 8 : D <= 512 ? 4 : D <= 1024 ? 2 : 1; }
 // f(IO, R) by example.
 template <class F>
 int with_types(const moe_norm_desc& d, F&& f) {
@@ -561,8 +616,8 @@ int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const flo
   hipStream_t s = static_cast<hipStream_t>(stream);
   prof_begin("norm_fwd", s);
   with_types(*d, [&](auto io, auto res) {
-    return with_row(d->D, [&](auto waves, auto nv) {
-      constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
+    return with_row(d->D, [&](auto threads, auto nv) {
+      constexpr int W = decltype(threads)::value, NV = decltype(nv)::value;
       using IO = decltype(io);
       using R = decltype(res);
       // a workgroup for each row or rows: 1024 that step through 16384 rows of 4096 take 383 us forward and backward, so 366
@@ -619,8 +674,8 @@ int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const flo
   if (d->T > 0) {
     prof_begin("norm_bwd", s);
     with_types(*d, [&](auto io, auto res) {
-      return with_row(d->D, [&](auto waves, auto nv) {
-        constexpr int W = decltype(waves)::value, NV = decltype(nv)::value;
+      return with_row(d->D, [&](auto threads, auto nv) {
+        constexpr int W = decltype(threads)::value, NV = decltype(nv)::value;
         using IO = decltype(io);
         using R = decltype(res);
         if (db == nullptr) norm_bwd_kernel<IO, R, BLOCK_NONE, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
