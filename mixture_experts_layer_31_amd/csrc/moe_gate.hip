@@ -293,12 +293,15 @@ struct Choice {
 // reciprocal: below 8 u and 20 u of M, the largest score or choice.  A unit of 2^-22 M is 4 u, so that keys
 // are off by 2 or 5 units and half a one for their rounding, the fp32 rounding of c a quarter: a difference of 6 or 13
 // units is one of c's.  With units of 2^-20 M (16 u) one of 3 or 5 is.  The sums of two of a group twice that and two for an fp32
-// rounding.
+// rounding.  Of logits in units of 2^-22 of the largest or 1 a difference of 4 (2^-20: 3) is one of 2.5 (1.5) units, more
+// than 2^-21 relative in their scores, so that those differ in fp32 as long as they are normal numbers.
 template <bool RAGGED, class Z, int LPT, int VPL>
 __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>& sh, const Z* row, Choice& out,
                                              float& m, float& inv) {
   constexpr int PB = LPT == 16 ? 8 : 10, N = VPL < 8 ? VPL : 8;
-  const int gap = LPT == 16 ? (a.softmax ? 13 : 6) : (a.softmax ? 5 : 3);
+  // Softmax scores without a bias rise with the logits, one by one or by the best of a group: no score is computed.
+  const bool by_logit = a.softmax && a.bias == nullptr && (a.top_groups == a.groups || a.best == 1 || a.each == 1);
+  const int gap = by_logit ? (LPT == 16 ? 4 : 3) : LPT == 16 ? (a.softmax ? 13 : 6) : (a.softmax ? 5 : 3);
   constexpr uint32_t PLACES = (1u << PB) - 1;
   constexpr float TOP = LPT == 16 ? 4194304.f : 1048576.f;  // units of M
   constexpr float MAGIC = LPT == 16 ? 12582912.f : 13631488.f;  // 1.5 * 2^23 (+ TOP): an integer's bits are the low ones
@@ -318,12 +321,17 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
 #pragma unroll
     for (int i = 0; i < VPL; ++i) m = fmaxf(m, z[i]);
     m = fmaxf(token_max<LPT>(m), -FLT_MAX);
+    if (!by_logit || !a.renorm) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)  // with a NaN or +inf the sum is a NaN, with only -inf it is 0
-      c[i] = __builtin_amdgcn_exp2f((z[i] - m) * 1.44269504f);
-    inv = __builtin_amdgcn_rcpf(token_sum<LPT>(half_sum<VPL>(c)));
+      for (int i = 0; i < VPL; ++i) c[i] = __builtin_amdgcn_exp2f((z[i] - m) * 1.44269504f);
+      inv = __builtin_amdgcn_rcpf(token_sum<LPT>(half_sum<VPL>(c)));
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) c[i] *= inv;
+      for (int i = 0; i < VPL; ++i) c[i] *= inv;
+    }
+    if (by_logit) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = !RAGGED || is(i) ? z[i] : 0.f;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -334,9 +342,9 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
       c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_fmaf(e, lo * 0.693147181f, e));
     }
   }
-  float M = 0.f;
+  float M = by_logit ? 1.f : 0.f;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) M = fmaxf(M, c[i]);
+  for (int i = 0; i < VPL; ++i) M = fmaxf(M, fabsf(c[i]));
   if (a.bias != nullptr) {
     load_logits<RAGGED>(a, sh, a.bias, z);
 #pragma unroll
@@ -392,6 +400,7 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
       const bool at_border = sh.mine && to_border < gap && to_border > -gap;
       hard |= at_border && !(a.bias == nullptr && element(row + place_of(k0)) == element(row + place_of(worst)));
     }
+    if (by_logit) hard |= float((token_max<LPT>(score) >> PB) - (worst >> PB)) > 60.f * unit;  // e^-60: see below
 #pragma unroll
     for (int i = 0; i < N; ++i) key[i] = in ? key[i] : 0u;
     full &= in;
@@ -429,6 +438,7 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
   };
   const bool close = near(a.K);
   hard |= full && key[0] == 0;
+  hard |= by_logit && sh.l < a.K && m - out.x > 60.f;  // scores that may be below the normal numbers, equal ones then
   if (__ballot(hard) != 0 || (__ballot(close) != 0 && a.softmax)) return false;
   if (__ballot(close) == 0) return true;
   // Sigmoid scores: K and three more candidates, if the next one is clear of them, by 64-bit keys.
@@ -449,12 +459,13 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
 
 // The choice by 64-bit keys, one maximum over the lane's values a slot.
 template <bool RAGGED, class Z, int LPT, int VPL>
-__device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LPT>& sh, const Z* row, Choice& out) {
+__device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LPT>& sh, const Z* row, Choice& out, float& m,
+                                               float& inv_sum) {
   float z[VPL];
   load_logits<RAGGED>(a, sh, row, z);
   double key[VPL];
   if (a.softmax) {
-    float m = -INFINITY;
+    m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) m = fmaxf(m, z[i]);
     m = token_max<LPT>(m);
@@ -466,6 +477,7 @@ __device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LP
     }
     sum = token_sum<LPT>(sum);
     const double inv = sum == 0. ? 0. : 1. / sum;
+    inv_sum = sum == 0. ? INFINITY : float(inv);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] *= inv;
   } else {
@@ -531,7 +543,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int3
   const Z* row = static_cast<const Z*>(a.z) + (t < a.T ? t : a.T - 1) * a.ld;
   Choice ch;
   float m = 0.f, inv = 1.f;
-  if (!choose_fixed<RAGGED, Z, LPT, VPL>(a, sh, row, ch, m, inv)) choose_exactly<RAGGED, Z, LPT, VPL>(a, sh, row, ch);
+  if (!choose_fixed<RAGGED, Z, LPT, VPL>(a, sh, row, ch, m, inv)) choose_exactly<RAGGED, Z, LPT, VPL>(a, sh, row, ch, m, inv);
   const bool chosen = ch.slot < a.K;
   double s = 0.;
   if (chosen) s = a.softmax ? (ch.x == -INFINITY ? 0. : exp64(double(ch.x) - double(m))) : sigmoid64(ch.x);

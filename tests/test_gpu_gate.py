@@ -211,6 +211,17 @@ def test_extreme_logits():
     _check(np.float32(z * 1e36), None, 8, name="huge")
 
 
+def test_peaked_softmax():
+    """Scores without a bias, chosen by the logits: far apart, below fp32's normal numbers, and equal again as 0."""
+    for spread in (0.01, 1.0, 6.0, 25.0, 120.0):
+        for t in (F, B):
+            z, _ = _logits(11, 300, 96, spread=spread)
+            for renorm in (True, False):
+                _check(z, None, 8, "softmax", renorm=renorm, t=t, name=f"spread {spread}")
+                _check(z, None, 8, "softmax", 8, 3, 1, renorm=renorm, t=t, name=f"spread {spread} in groups")
+                _check(z, None, 8, "softmax", 8, 3, 2, renorm=renorm, t=t, name=f"spread {spread} in groups by two")
+
+
 def test_ids_twice_and_out_of_range():
     z, bias = _logits(6, 40, 48)
     rng = np.random.default_rng(6)
