@@ -388,7 +388,8 @@ enum moe_scale { MOE_SCALE_TILE = 0, MOE_SCALE_BLOCK = 1 };
  *   topk_idx: the K largest c in descending order, ties to the lower expert;
  *   topk_w[t,k] = scale s_k, or with MOE_GATE_RENORM scale s_k / sum_k' s_k' (0 where
  *   that sum is 0), of the scores without the bias.
- * A +inf or NaN logit gives its scores as the formulas do (ids stay distinct and in range). */
+ * A +inf or NaN logit gives its scores as the formulas do (ids stay distinct and in range).  Scores and the sum of
+ * the chosen ones are 64 bits wide; the sum of a softmax that is not renormalised is fp32. */
 enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
 #define MOE_GATE_RENORM 0x1     /* weights of a token sum to scale */
 #define MOE_GATE_ACCUMULATE 0x2 /* moe_gate_bwd adds to dlogits (in_type MOE_TYPE_F32 only) */
@@ -408,8 +409,8 @@ typedef struct moe_gate_desc {
  * <= top_groups (E / groups), and the values above (else MOE_EINVAL); E <= 1024, K <= 64,
  * groups <= 64, T < 2^26 and row strides below 2^40 (else MOE_EUNSUPPORTED).  logits: device [T, E] of in_type, aligned to
  * its element; bias: device float32 [E] or NULL (0); topk_idx: device int32 [T, K]
- * and topk_w: device float32 [T, K], written (the layout moe_fwd reads); 4-byte
- * aligned (MOE_EALIGN).  T = 0 is MOE_OK and touches nothing.  Asynchronous on
+ * and topk_w: device float32 [T, K], written (the layout moe_fwd reads), apart from each other and
+ * every input (MOE_EINVAL); 4-byte aligned (MOE_EALIGN).  T = 0 is MOE_OK and touches nothing.  Asynchronous on
  * `stream`; allocates nothing. */
 int moe_gate_fwd(const moe_gate_desc* d, const void* logits, const float* bias,
                  int32_t* topk_idx, float* topk_w, void* stream);
@@ -550,9 +551,9 @@ int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const flo
  * dr: device [T, D] of res_type, may be dh (with ld_r = ld_h); db: [T, D] of io_type (NULL with b NULL);
  * dgate: float32 [T], NULL exactly where gate is; dw, dw_post: float32 [D], NULL exactly
  * where w, w_post are.  With w NULL dy is NULL.  b is read only with gate or w_post (else it may be NULL where
- * db is not); h only with w.  Row sums are fp32; sums over rows are 64 bits wide over a workgroup's rows and over the
- * workgroups, rounded to fp32 between the two and at the end, in an order that
- * depends on the sizes alone.  scratch: device, 16-byte aligned, of
+ * db is not); h only with w.  Row sums are fp32; sums over rows are 64 bits wide over a workgroup's rows (for D
+ * from 4097 to 8192 over fp32 sums of sixteen of them) and over the workgroups, rounded to fp32 between the two and at
+ * the end, in an order that depends on the sizes alone.  scratch: device, 16-byte aligned, of
  * moe_norm_scratch_bytes(d) (MOE_ESCRATCH), used only during the call.  With T = 0 dw and
  * dw_post are written 0.  Other requirements as moe_norm_fwd. */
 size_t moe_norm_scratch_bytes(const moe_norm_desc* d);

@@ -477,7 +477,8 @@ __device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LP
     }
     sum = token_sum<LPT>(sum);
     const double inv = sum == 0. ? 0. : 1. / sum;
-    inv_sum = sum == 0. ? INFINITY : float(inv);
+    // of weights that are not renormalised choose_fixed's stays: a token's do not depend on its neighbours in the wave
+    if (a.renorm || !(inv_sum > 0.f && inv_sum < INFINITY)) inv_sum = sum == 0. ? INFINITY : float(inv);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] *= inv;
   } else {
@@ -748,6 +749,11 @@ int moe_gate_fwd(const moe_gate_desc* d, const void* logits, const float* bias, 
   if (!aligned_to(logits, type_bytes(d->in_type)) || !aligned_to(bias, 4) || !aligned_to(topk_idx, 4) ||
       !aligned_to(topk_w, 4))
     return MOE_EALIGN;
+  const size_t in = span(d->T, d->E, d->ld_logits, type_bytes(d->in_type)), out = size_t(d->T) * d->K * 4,
+               row = size_t(d->E) * 4;
+  if (overlap(topk_idx, out, topk_w, out) || overlap(topk_idx, out, logits, in) || overlap(topk_w, out, logits, in) ||
+      overlap(topk_idx, out, bias, row) || overlap(topk_w, out, bias, row))
+    return MOE_EINVAL;
   GateArgs a = gate_args(*d, logits, bias);
   int gp = 1;
   while (gp < a.groups) gp *= 2;

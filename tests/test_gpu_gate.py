@@ -222,6 +222,32 @@ def test_peaked_softmax():
                 _check(z, None, 8, "softmax", 8, 3, 2, renorm=renorm, t=t, name=f"spread {spread} in groups by two")
 
 
+@pytest.mark.parametrize("E,G,top,K", [(96, 8, 3, 8), (256, 1, 1, 8), (130, 1, 1, 5), (512, 8, 4, 8), (40, 4, 2, 20)])
+def test_a_token_alone_and_among_others(E, G, top, K):
+    """A token's ids and weights are the same bits whatever stands beside it: rows that are chosen again in 64 bits
+    (masked, equal, past the numbers) among others that are not."""
+    z, bias = _logits(12, 60, E)
+    z[::7, ::3] = -np.inf
+    z[5::14] = 0.25
+    z[2, 1], z[11, 2], z[23, :] = np.inf, np.nan, -np.inf
+    zt = torch.from_numpy(z).cuda()
+    bt = torch.from_numpy(np.float32(bias)).cuda()
+    for score in SCORE:
+        for flags in (0, moe.MOE_GATE_RENORM):
+            for b in (None, bt):
+                outs = []
+                for rows in [range(0, 60), *[range(t, t + 1) for t in range(60)]]:
+                    n = len(rows)
+                    d = moe.make_gate_desc(n, E, K, SCORE[score], G, top, 2, moe.MOE_TYPE_F32, flags, 2.5)
+                    it = torch.full((n, K), -7, dtype=torch.int32, device="cuda")
+                    w = torch.full((n, K), 7.0, device="cuda")
+                    assert moe.moe_gate_fwd(d, zt[rows.start:rows.stop], b, it, w) == moe.MOE_OK
+                    outs.append((it, w))
+                alone = [torch.cat(v) for v in zip(*outs[1:])]
+                for got, want in zip(alone, outs[0]):
+                    assert torch.equal(got.view(torch.int32), want.view(torch.int32)), (score, flags, b is None)
+
+
 def test_ids_twice_and_out_of_range():
     z, bias = _logits(6, 40, 48)
     rng = np.random.default_rng(6)

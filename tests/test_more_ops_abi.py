@@ -61,6 +61,10 @@ def test_gate_buffers():
     assert _gate_bwd(d, dz=_at(0) + 64 * 128 * 4 - 4) == EINVAL
     assert _gate_bwd(d, dz=_at(1) - 64 * 128 * 4 + 4) == EINVAL
     assert _gate_bwd(d, dz=_at(2) + 64 * 8 * 4 - 4) == EINVAL
+    for k, at in dict(idx=_at(0) + 64 * 128 * 4 - 4, w=_at(1) + 64 * 8 * 4 - 4).items():  # logits, the ids
+        assert _gate_fwd(d, **{k: at}) == EINVAL
+    assert _gate_fwd(d, w=_at(0) - 64 * 8 * 4 + 4) == EINVAL
+    assert _gate_fwd(d, bias=_at(1) - 128 * 4 + 4) == EINVAL and _gate_fwd(d, bias=_at(2) + 64 * 8 * 4 - 4) == EINVAL
     empty = moe.make_gate_desc(0, 128, 8)
     assert _gate_fwd(empty, z=None, idx=None, w=None) == OK
     assert _gate_bwd(empty, z=None, idx=None, dw=None, dz=None) == OK
@@ -122,7 +126,7 @@ def test_norm_buffers():
 
 def test_norm_backward_buffers():
     d = moe.make_norm_desc(4, 64)
-    assert moe.moe_norm_scratch_bytes(d) >= 2 * 4 * 64 * 4
+    assert moe.moe_norm_scratch_bytes(d) >= 2 * 64 * 4  # a row each of both weights'
     for k in ("h", "w", "db", "dr", "dw", "scratch"):
         assert _norm_bwd(d, **{k: None}) == EINVAL, k
     assert _norm_bwd(d, gate=_at(9)) == EINVAL and _norm_bwd(d, dgate=_at(9)) == EINVAL
