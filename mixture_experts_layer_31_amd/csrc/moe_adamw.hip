@@ -53,26 +53,6 @@ struct AdamStep {
 };
 static_assert(sizeof(AdamList) + sizeof(AdamStep) <= 3584, "kernel arguments hold the list");
 
-// 1 - e^x for x <= 0: e^x by its series on half an octave, in 64 bits, for the difference from 1.
-__device__ __forceinline__ float left_over(double x) {
-  x = x > -700. ? x : -700.;
-  const double n = __builtin_rint(x * 1.4426950408889634074);  // log2(e)
-  const double r = __builtin_fma(n, -0.69314718055994530942, x);
-  double y = 1. / 39916800.;
-  y = __builtin_fma(y, r, 1. / 3628800.);
-  y = __builtin_fma(y, r, 1. / 362880.);
-  y = __builtin_fma(y, r, 1. / 40320.);
-  y = __builtin_fma(y, r, 1. / 5040.);
-  y = __builtin_fma(y, r, 1. / 720.);
-  y = __builtin_fma(y, r, 1. / 120.);
-  y = __builtin_fma(y, r, 1. / 24.);
-  y = __builtin_fma(y, r, 1. / 6.);
-  y = __builtin_fma(y, r, 0.5);
-  y = __builtin_fma(y, r, 1.);
-  y = __builtin_fma(y, r, 1.);
-  return float(1. - __builtin_ldexp(y, int(n)));
-}
-
 // The step's numbers, the same in every thread.
 struct Coef {
   float c, b1, b2, a1, a2;    // clipping factor, betas and 1 - betas
@@ -93,8 +73,8 @@ __device__ __forceinline__ Coef coefficients(const AdamStep& s) {
   k.b1 = s.b1; k.b2 = s.b2;
   k.a1 = s.a1; k.a2 = s.a2;
   k.lr = lr;
-  k.rate = lr / left_over(double(t) * s.log_b1);
-  k.root = 1.f / sqrtf(left_over(double(t) * s.log_b2));
+  k.rate = lr / float(1. - exp64(double(t) * s.log_b1));
+  k.root = 1.f / sqrtf(float(1. - exp64(double(t) * s.log_b2)));
   k.eps = s.eps;
   return k;
 }

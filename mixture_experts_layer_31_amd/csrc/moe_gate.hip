@@ -139,43 +139,6 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// A constant of 64 bits in scalar registers where it is used: kept over a loop in vector registers, those of
-// exp64 take half of them.
-__device__ __forceinline__ double scalar(double c) {
-  asm volatile("" : "+s"(c));
-  return c;
-}
-// e^x in 64 bits (2^-45 relative): its series on half an octave.  0 below -745, infinite above 709.
-__device__ __forceinline__ double exp64(double x) {
-  const double c = x < -745. ? -745. : x > 745. ? 745. : x;  // a NaN stays
-  const double n = __builtin_rint(c * scalar(1.4426950408889634074));
-  double r = __builtin_fma(n, scalar(-0.693147180559945286), c);
-  r = __builtin_fma(n, scalar(-2.3190468138462996e-17), r);
-  double y = scalar(1. / 39916800.);
-  y = __builtin_fma(y, r, scalar(1. / 3628800.));
-  y = __builtin_fma(y, r, scalar(1. / 362880.));
-  y = __builtin_fma(y, r, scalar(1. / 40320.));
-  y = __builtin_fma(y, r, scalar(1. / 5040.));
-  y = __builtin_fma(y, r, scalar(1. / 720.));
-  y = __builtin_fma(y, r, scalar(1. / 120.));
-  y = __builtin_fma(y, r, scalar(1. / 24.));
-  y = __builtin_fma(y, r, scalar(1. / 6.));
-  y = __builtin_fma(y, r, 0.5);
-  y = __builtin_fma(y, r, 1.);
-  y = __builtin_fma(y, r, 1.);
-  return __builtin_ldexp(y, int(n));
-}
-// 1 / y for y of normal size (2^-50 relative).
-__device__ __forceinline__ double inverse64(double y) {
-  double r = __builtin_amdgcn_rcp(y);
-  r = __builtin_fma(__builtin_fma(-y, r, 1.), r, r);
-  return __builtin_fma(__builtin_fma(-y, r, 1.), r, r);
-}
-__device__ __forceinline__ double sigmoid64(float z) {
-  const double e = exp64(-double(z));
-  return e < 1e300 ? inverse64(1. + e) : e != e ? e : 0.;
-}
-
 // Descending, by Batcher's odd-even merging network.
 template <int N>
 __device__ __forceinline__ void sort8(uint32_t (&k)[N], int from) {

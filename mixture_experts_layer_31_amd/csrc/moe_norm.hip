@@ -36,6 +36,7 @@ struct NormArgs {
   int64_t ld_b, ld_r, ld_h, ld_y;
   int T, D;
   float eps, scale;
+  double inv_d;  // 1 / D
   bool w_f32;
 };
 
@@ -210,9 +211,15 @@ __device__ __forceinline__ void row_sums(V (&v)[N], Joins<TPR>& red, int row, in
 
 __device__ __forceinline__ float fma_of(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
 __device__ __forceinline__ double fma_of(double a, double b, double c) { return __builtin_fma(a, b, c); }
-__device__ __forceinline__ float sigmoid_times(float s, float z) { return s / (1.f + expf(-z)); }
-__device__ __forceinline__ double sigmoid_times(double s, float z) { return s / (1. + exp(-double(z))); }
-__device__ __forceinline__ float inverse_root(float x) { return 1.f / sqrtf(x); }
+__device__ __forceinline__ float sigmoid_times(float s, float z) { return s * __builtin_amdgcn_rcpf(1.f + expf(-z)); }
+__device__ __forceinline__ double sigmoid_times(double s, float z) { return s * sigmoid64(z); }
+// The hardware's, within an ulp (a correctly rounded root and quotient take 25 instructions a row, of some 200); it takes
+// numbers below the normal ones for 0.
+__device__ __forceinline__ float inverse_root(float x) {
+  const bool tiny = x < 0x1p-100f;
+  const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p100f : x);
+  return tiny ? r * 0x1p50f : r;
+}
 // The hardware's 2^-24 and two steps of Newton's: 2^-50.
 __device__ __forceinline__ double inverse_root(double x) {
   double r = __builtin_amdgcn_rsq(x);
@@ -232,6 +239,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a)
   __shared__ Joins<TPR> red;
   int half = 0;
   const int tid = threadIdx.x % TPR, row = threadIdx.x / TPR, D = a.D;
+  const float inv_d = float(a.inv_d);
   float w[NV][P], wp[NV][P];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -267,14 +275,19 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a)
 #pragma unroll
           for (int i = 0; i < P; ++i) sum[0] = fma_of(V(bv[k][i]), V(bv[k][i]), sum[0]);
         row_sums<TPR>(sum, red, row, half);
-        by *= inverse_root(sum[0] / V(D) + V(a.eps));
+        by *= inverse_root(fma_of(sum[0], V(a.inv_d), V(a.eps)));
       }
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < P; ++i) {
+          // converted here again: 64-bit copies of b and w_post kept over the join cost a third of the waves
+          asm("" : "+v"(bv[k][i]));
           V u = V(bv[k][i]);
-          if (a.w_post != nullptr) u *= V(wp[k][i]);  // exact in 64 bits
+          if (a.w_post != nullptr) {
+            asm("" : "+v"(wp[k][i]));
+            u *= V(wp[k][i]);  // exact in 64 bits
+          }
           x[k][i] = float(fma_of(by, u, V(x[k][i])));
         }
     }
@@ -292,7 +305,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a)
     }
     if (a.w == nullptr) continue;
     row_sums<TPR>(sum, red, row, half);
-    const float q = 1.f / sqrtf(sum[0] / float(D) + a.eps);
+    const float q = inverse_root(__builtin_fmaf(sum[0], inv_d, a.eps));
     IO* y = static_cast<IO*>(a.y) + t * a.ld_y;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -310,6 +323,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
   __shared__ Joins<TPR> red;
   int half = 0;
   const int tid = threadIdx.x % TPR, row = threadIdx.x / TPR, D = a.D;
+  const float inv_d = float(a.inv_d);
   const bool pre = a.w != nullptr, post = BLOCK == BLOCK_NORM && a.w_post != nullptr;
   float w[NV][P], wp[NV][P];
   // parts of dw and dw_post: 64 bits, or (two eights a thread, where those do not fit the registers) fp32 over kFold rows,
@@ -360,12 +374,14 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
     }
   };
   const int64_t step = int64_t(gridDim.x) * ROWS;
-  fetch(int64_t(blockIdx.x) * ROWS + row);
+  constexpr bool AHEAD = TPR < 1024;
+  if (AHEAD) fetch(int64_t(blockIdx.x) * ROWS + row);
   for (int64_t first = int64_t(blockIdx.x) * ROWS; first < a.T; first += step) {
     const int64_t t = first + row;
     const bool there = t < a.T;
     float g[NV][P], x[NV][P], e[NV][P], bv[NV][P];
     float sum[3] = {0.f, 0.f, 0.f};  // h^2, e h, b^2
+    if (!AHEAD) fetch(t);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       next.dh[k].values(g[k]);
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
       next.dy[k].values(e[k]);
       if (BLOCK == BLOCK_NORM) next.b[k].values(bv[k]);
     }
-    if (first + step < a.T) fetch(t + step);
+    if (AHEAD && first + step < a.T) fetch(t + step);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -386,8 +402,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
       }
     row_sums<TPR>(sum, red, row, half);
     if (pre && a.dy != nullptr && there) {
-      const float q = 1.f / sqrtf(sum[0] / float(D) + a.eps);
-      const float m = sum[1] / float(D) * q * q;
+      const float q = inverse_root(__builtin_fmaf(sum[0], inv_d, a.eps));
+      const float m = sum[1] * inv_d * q * q;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -415,8 +431,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
       float by = a.scale, rest = 0.f;
       if (a.gate != nullptr) {
         const float z = a.gate[there ? t : 0];
-        by = a.scale / (1.f + expf(-z));
-        rest = 1.f / (1.f + expf(z));
+        by = sigmoid_times(a.scale, z);
+        rest = sigmoid_times(1.f, -z);
       }
       float dot[1] = {0.f};
 #pragma unroll
@@ -425,9 +441,9 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
         for (int i = 0; i < P; ++i) dot[0] = __builtin_fmaf(g[k][i] * wp[k][i], bv[k][i], dot[0]);
       row_sums<TPR>(dot, red, row, half);
       if (there) {
-        const float p = post ? 1.f / sqrtf(sum[2] / float(D) + a.eps) : 1.f;
+        const float p = post ? inverse_root(__builtin_fmaf(sum[2], inv_d, a.eps)) : 1.f;
         if (a.gate != nullptr && tid == 0) a.dgate[t] = by * rest * (dot[0] * p);
-        const float m = post ? dot[0] / float(D) * p * p : 0.f;
+        const float m = post ? dot[0] * inv_d * p * p : 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           float o[P];
@@ -612,6 +628,7 @@ int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const flo
   a.b = b; a.r = r; a.w_post = w_post; a.w = w; a.gate = gate; a.h = h; a.y = y;
   a.ld_b = d->ld_b; a.ld_r = d->ld_r; a.ld_h = d->ld_h; a.ld_y = d->ld_y;
   a.T = d->T; a.D = d->D; a.eps = d->eps; a.scale = d->scale;
+  a.inv_d = 1. / d->D;
   a.w_f32 = d->w_type == MOE_TYPE_F32;
   hipStream_t s = static_cast<hipStream_t>(stream);
   prof_begin("norm_fwd", s);
@@ -668,6 +685,7 @@ int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const flo
   a.part_post = reinterpret_cast<float*>(static_cast<char*>(scratch) + need / 2);
   a.ld_b = d->ld_b; a.ld_r = d->ld_r; a.ld_h = d->ld_h; a.ld_y = d->ld_y;
   a.T = d->T; a.D = d->D; a.eps = d->eps; a.scale = d->scale;
+  a.inv_d = 1. / d->D;
   a.w_f32 = d->w_type == MOE_TYPE_F32;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const unsigned grid = unsigned(norm_partials(*d));
