@@ -410,7 +410,8 @@ typedef struct moe_gate_desc {
  * groups <= 64, T < 2^26 and row strides below 2^40 (else MOE_EUNSUPPORTED).  logits: device [T, E] of in_type, aligned to
  * its element; bias: device float32 [E] or NULL (0); topk_idx: device int32 [T, K]
  * and topk_w: device float32 [T, K], written (the layout moe_fwd reads), apart from each other and
- * every input (MOE_EINVAL); 4-byte aligned (MOE_EALIGN).  T = 0 is MOE_OK and touches nothing.  Asynchronous on
+ * every input (MOE_EINVAL; a buffer of rows reaches from its first row's start to its last one's end, what
+ * lies between its rows included); 4-byte aligned (MOE_EALIGN).  T = 0 is MOE_OK and touches nothing.  Asynchronous on
  * `stream`; allocates nothing. */
 int moe_gate_fwd(const moe_gate_desc* d, const void* logits, const float* bias,
                  int32_t* topk_idx, float* topk_w, void* stream);
@@ -534,8 +535,8 @@ typedef struct moe_norm_desc {
 
 /* b, r, h, y: device [T, D]; gate: device float32 [T] or NULL; w, w_post: device [D]
  * (w_post or NULL); all aligned to their element (MOE_EALIGN).  h may be r (with ld_h =
- * ld_r); no other written buffer may overlap another buffer (MOE_EINVAL, as are null pointers but for those
- * above, T < 0, D < 1, bad types and row strides below D).  D <= 16384 and strides below
+ * ld_r); no other written buffer may overlap another buffer, what lies between its rows included (MOE_EINVAL,
+ * as are null pointers but for those above, T < 0, D < 1, bad types and row strides below D).  D <= 16384 and strides below
  * 2^40 (MOE_EUNSUPPORTED).  Padding of rows is left as it was.  T = 0 is MOE_OK and touches nothing.
  * Asynchronous on `stream`; allocates nothing. */
 int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const float* gate,

@@ -494,7 +494,8 @@ def make_adamw_list(params, grads, m, v, masters=None, m_scales=None, v_scales=N
     anew when they move.  The call refuses it with another GPU current than the tensors'."""
     import torch
     types = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
-    params, count = list(params), len(params)
+    params = list(params)
+    count = len(params)
     e4m3 = m_scales is not None
     lists = [list(x) if x is not None else [None] * count for x in (masters, grads, m, v, m_scales, v_scales)]
     decay = [weight_decay] * count if isinstance(weight_decay, (int, float)) else list(weight_decay)
@@ -504,7 +505,7 @@ def make_adamw_list(params, grads, m, v, masters=None, m_scales=None, v_scales=N
     rows = []
     for p, w, g, a, b, sa, sb, wd in zip(params, *lists, decay):
         n = p.numel()
-        if p.dtype not in types or g.dtype not in types or g.numel() != n:
+        if p.dtype not in types or g is None or g.dtype not in types or g.numel() != n:
             raise ValueError("parameters and gradients are float32 or bfloat16, of one length")
         if w is not None and (p.dtype != torch.bfloat16 or w.dtype != torch.float32 or w.numel() != n):
             raise ValueError("a master is float32, beside a bfloat16 parameter of its length")

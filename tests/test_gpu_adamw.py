@@ -356,3 +356,24 @@ def test_offsets_past_2_31_elements():
     assert bool((m[:-1000] == 0x7E).all()) and bool((m[-1000:] == 0xFE).all()) and bool((v == 0x7E).all())
     assert torch.allclose(ms, torch.full_like(ms, 0.1 * 0.25 / 448), rtol=1e-6)
     assert torch.allclose(vs, torch.full_like(vs, 0.05 ** 0.5 * 0.25 / 448), rtol=1e-6)
+
+
+def test_list_of_a_modules_parameters():
+    """Lists come as they stand in a training loop: the parameters as an iterator, a missing gradient refused."""
+    torch.manual_seed(3)
+    net = torch.nn.Sequential(torch.nn.Linear(19, 33), torch.nn.Linear(33, 5, bias=False)).cuda()
+    states = [[torch.zeros_like(p) for p in net.parameters()] for _ in range(2)]
+    with pytest.raises(ValueError):
+        moe.make_adamw_list(net.parameters(), (p.grad for p in net.parameters()), *states)
+    net(torch.randn(7, 19, device="cuda")).square().sum().backward()
+    ref = [p.detach().cpu().double().numpy() for p in net.parameters()]
+    grads = [p.grad.cpu().double().numpy() for p in net.parameters()]
+    lst = moe.make_adamw_list(net.parameters(), (p.grad for p in net.parameters()), *states, weight_decay=0.1)
+    assert len(lst) == 3
+    lr, t, _ = _scalars(1e-2, 1, 1.0)
+    assert moe.moe_adamw(moe.make_adamw_desc(), lst, lr, t) == moe.MOE_OK
+    torch.cuda.synchronize()
+    for p, old, g in zip(net.parameters(), ref, grads):
+        # the first step: m and sqrt(v) are g and |g| after their corrections; 32 u of each term's size
+        want = old * (1 - 1e-2 * 0.1) - 1e-2 * g / (np.abs(g) + 1e-8)
+        assert np.all(np.abs(p.detach().cpu().double().numpy() - want) <= 32 * 2.0 ** -24 * (np.abs(old) + 1e-2))
