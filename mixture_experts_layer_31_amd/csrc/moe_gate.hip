@@ -581,11 +581,11 @@ __global__ void __launch_bounds__(kGateThreads) gate_bwd_kernel(GateArgs a, cons
     float m = 0.f;
     if (a.softmax) {
       m = token_max<LPT>(id >= 0 ? x : -INFINITY);
-      s = id >= 0 && x != -INFINITY ? exp(double(x) - double(m)) : 0.;
+      s = id >= 0 && x != -INFINITY ? exp64(double(x) - double(m)) : 0.;
     } else if (id >= 0) {
       s = sigmoid64(x);
     }
-    const double rest = a.softmax ? 1. : 1. / (1. + exp(double(x)));  // 1 - s
+    const double rest = a.softmax ? 1. : sigmoid64(-x);  // 1 - s
     if (a.renorm) {
       const double sum = token_sum<LPT>(s);
       s = sum == 0. ? 0. : s / sum;
