@@ -54,12 +54,26 @@ __device__ __forceinline__ float kept(const uint16_t*, float f) {
 // P values c .. c + P - 1 of a row of D (zeros behind its end) as they are stored, and their store.  Of fp32 rows P is
 // 4: pieces of 8 are two loads of 16 bytes that each touch half of every line (1363 x 1001 forward and backward 23.5 us,
 // so 22.7); beside bf16 rows, whose loads would have 8 bytes, it is 8 (16384 x 4096: 364 us, with 4 386).
-template <class T, int P>
+//
+// MOVED, for rows of bf16 alone that do not fill their threads: a load that would pass the row's end starts where it ends
+// there, with no branch, and `mend` shifts what it got.  With a branch a row's last piece, loaded element by element, waits
+// for each of them (16784 x 1999 forward and backward: 233 us, so 146; 13421 x 2500 315, so 181; 524288 x 64, whose lanes
+// behind the end only skip their loads, 208, so 149).  Where all pieces are whole the shifts cost registers (16384 x 4096
+// with both norms 262 us, with them 276), and fp32 rows, whose elements need not be put together, lose more than
+// they gain (1363 x 1001 with both norms: 22 us, so 24).
+template <class T, int P, bool MOVED>
 struct Piece {
   static constexpr int W = P * int(sizeof(T)) / 4;
+  static constexpr int N = 16 / int(sizeof(T));  // elements a load, with MOVED
   uint32_t w[W];
   __device__ __forceinline__ void get(const T* row, int c, int D) {
-    if (c + P <= D) {
+    if (MOVED && D >= N) {
+#pragma unroll
+      for (int u = 0; u < P / N; ++u) {
+        const uint4 v = load16(row + min(c + u * N, D - N));
+        w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
+      }
+    } else if (c + P <= D) {
       if constexpr (W == 2) {
         const uint2 v = fetch8<false>(row + c);
         w[0] = v.x; w[1] = v.y;
@@ -80,6 +94,25 @@ struct Piece {
         }
     }
   }
+  __device__ __forceinline__ void mend(int c, int D) {
+    if constexpr (MOVED) {
+      if (D < N || __ballot(c + P > D) == 0) return;
+#pragma unroll
+      for (int u = 0; u < P / N; ++u) {
+        const int past = min(max(c + u * N - (D - N), 0), N), words = past * int(sizeof(T)) / 4;
+        uint32_t v[5] = {w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3], 0};
+#pragma unroll
+        for (int by = 4; by >= 1; by /= 2) {
+          const bool go = (words & by) != 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = go ? (k + by < 4 ? v[k + by] : 0u) : v[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[4 * u + k] = sizeof(T) == 2 ? __builtin_amdgcn_alignbit(v[k + 1], v[k], (past & 1) * 16) : v[k];
+      }
+    }
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int k = 0; k < W; ++k) w[k] = 0;
@@ -97,10 +130,11 @@ struct Piece {
     }
   }
 };
-template <class T, int P>
+template <bool MOVED, class T, int P>
 __device__ __forceinline__ void get(const T* row, int c, int D, float (&f)[P]) {
-  Piece<T, P> e;
+  Piece<T, P, MOVED> e;
   e.get(row, c, D);
+  e.mend(c, D);
   e.values(f);
 }
 template <class T, int P>
@@ -126,10 +160,10 @@ __device__ __forceinline__ void put(T* row, int c, int D, const float (&f)[P]) {
       if (c + i < D) put_one(row + c + i, f[i]);
   }
 }
-template <int P>
+template <bool MOVED, int P>
 __device__ __forceinline__ void get_weight(const void* w, bool f32, int c, int D, float (&f)[P]) {
-  if (f32) get(static_cast<const float*>(w), c, D, f);
-  else get(static_cast<const uint16_t*>(w), c, D, f);
+  if (f32) get<MOVED>(static_cast<const float*>(w), c, D, f);
+  else get<MOVED>(static_cast<const uint16_t*>(w), c, D, f);
 }
 
 // Sum over the wave by lane moves of the vector ALU (a shuffle through the LDS crossbar costs ten times as long, and
@@ -236,7 +270,7 @@ enum { BLOCK_NONE = 0, BLOCK_SUM = 1, BLOCK_NORM = 2 };
 template <class IO, class R>
 constexpr int piece_of() { return sizeof(IO) + sizeof(R) == 8 ? 4 : 8; }
 
-template <class IO, class R, int BLOCK, int TPR, int EIGHTS>
+template <class IO, class R, int BLOCK, int TPR, int EIGHTS, bool MOVED>
 __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a) {
   constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(TPR);
   __shared__ Joins<TPR> red;
@@ -247,8 +281,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = P * (tid + TPR * k);
-    if (a.w != nullptr) get_weight(a.w, a.w_f32, c, D, w[k]);
-    if (BLOCK == BLOCK_NORM && a.w_post != nullptr) get_weight(a.w_post, a.w_f32, c, D, wp[k]);
+    if (a.w != nullptr) get_weight<MOVED>(a.w, a.w_f32, c, D, w[k]);
+    if (BLOCK == BLOCK_NORM && a.w_post != nullptr) get_weight<MOVED>(a.w_post, a.w_f32, c, D, wp[k]);
   }
   for (int64_t first = int64_t(blockIdx.x) * ROWS; first < a.T; first += int64_t(gridDim.x) * ROWS) {
     const int64_t t = first + row;
@@ -256,11 +290,23 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a)
     const R* r = static_cast<const R*>(a.r) + (there ? t : first) * a.ld_r;
     const IO* b = static_cast<const IO*>(a.b) + (there ? t : first) * a.ld_b;
     float x[NV][P], bv[NV][P];
+    Piece<R, P, MOVED> rp[NV];
+    Piece<IO, P, MOVED> bp[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = P * (tid + TPR * k);
-      get(r, c, D, x[k]);
-      if (BLOCK != BLOCK_NONE) get(b, c, D, bv[k]);
+      rp[k].get(r, c, D);
+      if (BLOCK != BLOCK_NONE) bp[k].get(b, c, D);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = P * (tid + TPR * k);
+      rp[k].mend(c, D);
+      rp[k].values(x[k]);
+      if (BLOCK != BLOCK_NONE) {
+        bp[k].mend(c, D);
+        bp[k].values(bv[k]);
+      }
     }
     if constexpr (BLOCK == BLOCK_SUM) {
 #pragma unroll
@@ -320,7 +366,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_fwd_kernel(NormArgs a)
   }
 }
 
-template <class IO, class R, int BLOCK, int TPR, int EIGHTS>
+template <class IO, class R, int BLOCK, int TPR, int EIGHTS, bool MOVED>
 __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a) {
   constexpr int P = piece_of<IO, R>(), NV = EIGHTS * 8 / P, ROWS = norm_rows(TPR);
   __shared__ Joins<TPR> red;
@@ -348,8 +394,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = P * (tid + TPR * k);
-    if (pre) get_weight(a.w, a.w_f32, c, D, w[k]);
-    if (post) get_weight(a.w_post, a.w_f32, c, D, wp[k]);
+    if (pre) get_weight<MOVED>(a.w, a.w_f32, c, D, w[k]);
+    if (post) get_weight<MOVED>(a.w_post, a.w_f32, c, D, wp[k]);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       acc[k][i] = acc_post[k][i] = 0;
@@ -359,8 +405,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
   }
   // a row ahead; a row behind the last one is a row of zeros
   struct Row {
-    Piece<IO, P> b[NV], dy[NV];
-    Piece<R, P> h[NV], dh[NV];
+    Piece<IO, P, MOVED> b[NV], dy[NV];
+    Piece<R, P, MOVED> h[NV], dh[NV];
   } next;
   auto fetch = [&](int64_t t) __attribute__((always_inline)) {
 #pragma unroll
@@ -387,10 +433,17 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_bwd_kernel(NormArgs a)
     if (!AHEAD) fetch(t);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      const int c = P * (tid + TPR * k);
+      next.dh[k].mend(c, D);
       next.dh[k].values(g[k]);
+      next.h[k].mend(c, D);
       next.h[k].values(x[k]);
+      next.dy[k].mend(c, D);
       next.dy[k].values(e[k]);
-      if (BLOCK == BLOCK_NORM) next.b[k].values(bv[k]);
+      if (BLOCK == BLOCK_NORM) {
+        next.b[k].mend(c, D);
+        next.b[k].values(bv[k]);
+      }
     }
     if (AHEAD && first + step < a.T) fetch(t + step);
 #pragma unroll
@@ -553,12 +606,17 @@ int with_row(int D, F&& f) {
   return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
 }
 int rows_a_workgroup(int D) { return D <= 128 ? 16 : D <= 256 ? 8 : D <= 512 ? 4 : D <= 1024 ? 2 : 1; }
-// f(IO, R) by example.
+// f(IO, R, MOVED) by example.
 template <class F>
 int with_types(const moe_norm_desc& d, F&& f) {
+  const std::true_type yes;
+  const std::false_type no;
   const bool io = d.io_type == MOE_TYPE_F32, res = d.res_type == MOE_TYPE_F32;
-  if (io) return res ? f(float(), float()) : f(float(), uint16_t());
-  return res ? f(uint16_t(), float()) : f(uint16_t(), uint16_t());
+  if (io) return res ? f(float(), float(), no) : f(float(), uint16_t(), no);
+  if (res) return f(uint16_t(), float(), no);
+  // rows that fill their threads' pieces (with_row's powers of two), or past those at least whole pieces
+  const bool whole = d.D <= 4096 ? d.D >= 128 && (d.D & (d.D - 1)) == 0 : d.D % 8 == 0;
+  return whole ? f(uint16_t(), uint16_t(), no) : f(uint16_t(), uint16_t(), yes);
 }
 
 bool float_type(int32_t t) { return t == MOE_TYPE_F32 || t == MOE_TYPE_BF16; }
@@ -637,16 +695,17 @@ int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const flo
   a.w_f32 = d->w_type == MOE_TYPE_F32;
   hipStream_t s = static_cast<hipStream_t>(stream);
   prof_begin("norm_fwd", s);
-  with_types(*d, [&](auto io, auto res) {
+  with_types(*d, [&](auto io, auto res, auto moved) {
     return with_row(d->D, [&](auto threads, auto nv) {
       constexpr int W = decltype(threads)::value, NV = decltype(nv)::value;
       using IO = decltype(io);
       using R = decltype(res);
+      constexpr bool M = decltype(moved)::value;
       // a workgroup for each row or rows: 1024 that step through 16384 rows of 4096 take 383 us forward and backward, so 366
       const unsigned grid = unsigned(std::min(ceil_div(d->T, norm_rows(W)), (1LL << 32) / norm_threads(W) - 1));
-      if (b == nullptr) norm_fwd_kernel<IO, R, BLOCK_NONE, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
-      else if (gate != nullptr || w_post != nullptr) norm_fwd_kernel<IO, R, BLOCK_NORM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
-      else norm_fwd_kernel<IO, R, BLOCK_SUM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
+      if (b == nullptr) norm_fwd_kernel<IO, R, BLOCK_NONE, W, NV, M><<<grid, norm_threads(W), 0, s>>>(a);
+      else if (gate != nullptr || w_post != nullptr) norm_fwd_kernel<IO, R, BLOCK_NORM, W, NV, M><<<grid, norm_threads(W), 0, s>>>(a);
+      else norm_fwd_kernel<IO, R, BLOCK_SUM, W, NV, M><<<grid, norm_threads(W), 0, s>>>(a);
       return 0;
     });
   });
@@ -696,14 +755,15 @@ int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const flo
   const unsigned grid = unsigned(norm_partials(*d));
   if (d->T > 0) {
     prof_begin("norm_bwd", s);
-    with_types(*d, [&](auto io, auto res) {
+    with_types(*d, [&](auto io, auto res, auto moved) {
       return with_row(d->D, [&](auto threads, auto nv) {
         constexpr int W = decltype(threads)::value, NV = decltype(nv)::value;
         using IO = decltype(io);
         using R = decltype(res);
-        if (db == nullptr) norm_bwd_kernel<IO, R, BLOCK_NONE, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
-        else if (block) norm_bwd_kernel<IO, R, BLOCK_NORM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
-        else norm_bwd_kernel<IO, R, BLOCK_SUM, W, NV><<<grid, norm_threads(W), 0, s>>>(a);
+        constexpr bool M = decltype(moved)::value;
+        if (db == nullptr) norm_bwd_kernel<IO, R, BLOCK_NONE, W, NV, M><<<grid, norm_threads(W), 0, s>>>(a);
+        else if (block) norm_bwd_kernel<IO, R, BLOCK_NORM, W, NV, M><<<grid, norm_threads(W), 0, s>>>(a);
+        else norm_bwd_kernel<IO, R, BLOCK_SUM, W, NV, M><<<grid, norm_threads(W), 0, s>>>(a);
         return 0;
       });
     });
