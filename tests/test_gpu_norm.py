@@ -116,6 +116,13 @@ def _check(T, D, io=B, res=B, wt=F, block=True, post=False, gated=False, pre=Tru
         _clean(buf, T, D, pad, o)
 
 
+@pytest.mark.parametrize("D", [4, 5, 6, 8, 12, 15, 17, 31, 120, 130, 250, 300, 1300, 2500, 3500, 4097, 6500, 8191, 9001])
+def test_rows_that_do_not_fill_their_threads(D):
+    """Rows of bf16 whose last loads are moved back to their end, with weights of both types, padding and odd addresses."""
+    _check(7, D, wt=B, post=True, gated=True, pad=3, off=1)
+    _check(9, D, wt=F, pad=1, off=5)
+
+
 @pytest.mark.parametrize("D", [1, 2, 3, 7, 8, 9, 63, 64, 65, 100, 511, 512, 513, 1000, 1024, 1025, 2048, 2049, 4096, 4099, 5000, 8192,
                                8193, 16384])
 def test_widths(D):
