@@ -632,8 +632,9 @@ typedef struct moe_adamw_desc {
  * (beta1 m) + ((1 - beta1) g), v = (beta2 v) + ((1 - beta2) (g g)).  p is computed from those in fp32 and
  * rounded once to its type.
  * With state_type MOE_TYPE_E4M3 the states are kept as codes of runs of 128 elements
- * from the tensor's first, with moe_block_quant's scales and codes (scale = amax / 448, 1
- * where that is 0; code = e4m3 of the fp32 quotient; a value is code * scale rounded to fp32): m, and
+ * from the tensor's first, with moe_block_quant's scales and codes (scale = amax / 448 in fp32, 1 where that
+ * quotient is 0, also of an amax that is not (2^-149 times 224 at most; the codes are then zeros); code = e4m3 of the fp32
+ * quotient, saturating at 448; a value is code * scale rounded to fp32): m, and
  * sqrt(v), whose code is at least 1 (2^-9) where
  * v > 0, so that no update divides by eps alone where a gradient has been seen; p
  * is computed from m and v as they are before that.  All zeros is the state before the first step

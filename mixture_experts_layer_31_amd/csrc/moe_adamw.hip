@@ -205,23 +205,29 @@ __device__ __forceinline__ uint2 codes_of(const float (&x)[8], float s, float d,
                              pack_e4m3x4(x[4] * hi, x[5] * hi, x[6] * hi, x[7] * hi));
   if (((c.x ^ h.x) | (c.y ^ h.y)) != 0 || !(s >= 0x1p-120f)) {  // below, the reciprocal may be infinite
     float y[8];
+    // a scale of a few of the smallest numbers is rounded by up to half, and the quotient is then past 448, where the
+    // conversion would give NaN
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = exact(i);
+    for (int i = 0; i < 8; ++i)
+      y[i] = __builtin_elementwise_minimum(__builtin_elementwise_maximum(exact(i), -448.f), 448.f);  // a NaN stays
     c = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
   }
   return c;
 }
-// A run's eight values in each of its sixteen lanes; returns the scale.
+// A run's eight values in each of its sixteen lanes; returns the scale.  Of a run that has shrunk to half of 448 of the
+// smallest numbers the quotient is 0, and x / 0 would be NaN for its zeros and for all of it in the next step: its scale is 1,
+// whose codes are zeros.
 __device__ __forceinline__ float code8(const float (&x)[8], uint2& codes) {
   float am = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
   am = max16(am);
-  const float s = am == 0.f ? 1.f : am / 448.f;
+  const float of = am / 448.f, s = of == 0.f ? 1.f : of;
   codes = codes_of(x, s, 0x1p-21f, [&](int i) { return x[i] / s; });
   return s;
 }
-// The same of the square roots of v, r their approximations within an ulp; what is positive has a positive code.
+// The same of the square roots of v, r their approximations within an ulp (2^-75 at least, so that only 0 has a scale of 0);
+// what is positive has a positive code.
 __device__ __forceinline__ float code8_root(const float (&v)[8], const float (&r)[8], uint2& codes) {
   float am = 0.f;
 #pragma unroll

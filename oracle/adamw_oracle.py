@@ -30,13 +30,16 @@ def moments32(g, m, v, beta1, beta2, norm=None, max_norm=0.0):
 
 
 def encode(x, least=False):
-    """(codes uint8, scales fp32) of x, fp32 values, in runs of 128; least: what is positive has a code of 1 at least."""
+    """(codes uint8, scales fp32) of x, fp32 values, in runs of 128; least: what is positive has a code of 1 at least.  A scale
+    amax / 448 that rounds to 0 is 1, and the codes are zeros; a NaN, which amax passes over, is 0x7F."""
     x = np.asarray(x, np.float32)
     n = x.size
     t = np.pad(x, (0, -n % 128)).reshape(-1, 128)
-    amax = np.abs(t).max(axis=1)
-    s = np.where(amax == 0, np.float32(1), amax / np.float32(448)).astype(np.float32)
-    codes = q8.e4m3_encode((t / s[:, None]).astype(np.float32))
+    s = (np.fmax.reduce(np.abs(t), axis=1, initial=0) / np.float32(448)).astype(np.float32)
+    s = np.where(s == 0, np.float32(1), s)
+    with np.errstate(invalid="ignore"):
+        q = (t / s[:, None]).astype(np.float32)
+    codes = np.where(np.isnan(q), 0x7F, q8.e4m3_encode(q))
     if least:
         codes = np.where((t > 0) & (codes == 0), 1, codes)
     return codes.astype(np.uint8).reshape(-1)[:n], s
