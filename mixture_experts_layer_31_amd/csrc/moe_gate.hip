@@ -275,7 +275,7 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
   constexpr float TOP = LPT == 16 ? 4194304.f : 1048576.f;  // units of M
   constexpr float MAGIC = LPT == 16 ? 12582912.f : 13631488.f;  // 1.5 * 2^23 (+ TOP): an integer's bits are the low ones
   auto is = [&](int i) { return sh.mine && sh.place(a, i) < a.each; };
-  // -inf, NaN and +inf are left to the 64-bit keys
+  // -inf, NaN and +inf, of the bias too, are left to the 64-bit keys
   float z[VPL], c[VPL];
   load_logits<RAGGED>(a, sh, row, z);
 #pragma unroll
@@ -319,9 +319,10 @@ __device__ __forceinline__ bool choose_fixed(const GateArgs& a, const Share<LPT>
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       c[i] += RAGGED && !is(i) ? 0.f : z[i];
-      M = fmaxf(M, fabsf(c[i]));
+      M = __builtin_elementwise_maximum(M, fabsf(c[i]));  // NaN where one of them is: the bias may hold one
     }
   }
+  hard |= !(M < 0x1p100f);  // this lane's: a NaN may not pass the maximum over the token
   M = token_max<LPT>(M);
   hard |= !(M >= 0x1p-60f && M < 0x1p100f);
   const float unit = __builtin_amdgcn_rcpf(M) * (TOP - 2048.f);
