@@ -386,8 +386,10 @@ enum moe_scale { MOE_SCALE_TILE = 0, MOE_SCALE_BLOCK = 1 };
  *   sum of its group_best largest c (of its one, where it has one), and only the experts of the top_groups
  *   best groups (ties to the lower group) can be chosen;
  *   topk_idx: the K largest c in descending order, ties to the lower expert;
- *   topk_w[t,k] = scale s_k, or with MOE_GATE_RENORM scale s_k / sum_k' s_k' (0 where
- *   that sum is 0), of the scores without the bias.
+ *   topk_w[t,k] = scale s_k, or with MOE_GATE_RENORM scale s_k / sum_k' s_k', of the scores
+ *   without the bias.  Those quotients hold however small the scores are (a softmax's far below
+ *   its row's largest too); they are 0 where all of the chosen logits are -inf, or of sigmoid scores that are
+ *   0 in 64 bits (logits below -745).
  * A +inf or NaN logit gives its scores as the formulas do (ids stay distinct and in range).  Scores and the sum of
  * the chosen ones are 64 bits wide; the sum of a softmax that is not renormalised is fp32. */
 enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };

@@ -109,9 +109,10 @@ __device__ __forceinline__ double scalar(double c) {
   asm volatile("" : "+s"(c));
   return c;
 }
-// e^x in 64 bits (2^-45 relative): its series on half an octave.  0 below -745, infinite above 709.
+// e^x in 64 bits (2^-45 relative): its Taylor series on half an octave, which ln 2 in two parts leaves.  0 below -745.2, infinite
+// above 709.
 __device__ __forceinline__ double exp64(double x) {
-  const double c = x < -745. ? -745. : x > 745. ? 745. : x;  // a NaN stays
+  const double c = x < -746. ? -746. : x > 746. ? 746. : x;  // a NaN stays
   const double n = __builtin_rint(c * scalar(1.4426950408889634074));
   double r = __builtin_fma(n, scalar(-0.693147180559945286), c);
   r = __builtin_fma(n, scalar(-2.3190468138462996e-17), r);
@@ -136,8 +137,9 @@ __device__ __forceinline__ double inverse64(double y) {
   return __builtin_fma(__builtin_fma(-y, r, 1.), r, r);
 }
 __device__ __forceinline__ double sigmoid64(float z) {
-  const double e = exp64(-double(z));
-  return e < 1e300 ? inverse64(1. + e) : e != e ? e : 0.;
+  const bool far = z < -600.f;  // there 1 / (1 + e^-z) is e^z, and e^-z may be infinite
+  const double e = exp64(far ? double(z) : -double(z));
+  return far ? e : inverse64(1. + e);
 }
 
 }  // namespace moe

@@ -504,6 +504,21 @@ __device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LP
   out.slot = sh.l;
 }
 
+// The sum of a token's chosen scores s, of logits x (slot: whether this lane has one).  Where it comes to the end of 64-bit
+// numbers (a bias can choose experts whose logits lie 700 below the row's largest) the quotients s / sum would be 0 / 0 or
+// their sum's reciprocal infinite: there they are those of exp(x - max) over the chosen, whose sum is 1 or more.  So far
+// down a sigmoid is exp x; scores of it that are 0 stay 0.
+template <int LPT>
+__device__ __forceinline__ double slot_sum(bool softmax, bool slot, float x, double& s) {
+  double sum = token_sum<LPT>(s);
+  if (sum < 1e-280 && (softmax || sum > 0.)) {  // the same in all lanes of a token
+    const float m = token_max<LPT>(slot ? x : -INFINITY);
+    s = slot && x != -INFINITY ? exp64(double(x) - double(m)) : 0.;
+    sum = token_sum<LPT>(s);
+  }
+  return sum;
+}
+
 template <class Z, int LPT, int VPL, bool RAGGED>
 __global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int32_t* __restrict__ topk_idx,
                                                                 float* __restrict__ topk_w) {
@@ -520,8 +535,8 @@ __global__ void __launch_bounds__(kGateThreads) gate_fwd_kernel(GateArgs a, int3
   if (chosen) s = a.softmax ? (ch.x == -INFINITY ? 0. : exp64(double(ch.x) - double(m))) : sigmoid64(ch.x);
   if (a.softmax && (!a.renorm || !(inv < INFINITY))) s *= inv == INFINITY ? 0. : double(inv);  // a row of only -inf, a NaN
   if (a.renorm) {
-    const double sum = token_sum<LPT>(s);
-    s = sum == 0. ? 0. : s * (sum > 1e-300 ? inverse64(sum) : 1. / sum);
+    const double sum = slot_sum<LPT>(a.softmax, chosen, ch.x, s);
+    s = sum == 0. ? 0. : s * inverse64(sum);
   }
   if (chosen && t < a.T) {
     topk_idx[t * a.K + ch.slot] = ch.at;
@@ -588,7 +603,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_bwd_kernel(GateArgs a, cons
     }
     const double rest = a.softmax ? 1. : sigmoid64(-x);  // 1 - s
     if (a.renorm) {
-      const double sum = token_sum<LPT>(s);
+      const double sum = slot_sum<LPT>(a.softmax, id >= 0, x, s);
       s = sum == 0. ? 0. : s / sum;
       const double mean = token_sum<LPT>(id >= 0 ? s * double(up) : 0.);
       part = id >= 0 ? float(s * rest * (double(up) - mean)) : 0.f;
