@@ -257,11 +257,12 @@ __device__ __forceinline__ float inverse_root(float x) {
   const float r = __builtin_amdgcn_rsqf(tiny ? x * 0x1p100f : x);
   return tiny ? r * 0x1p50f : r;
 }
-// The hardware's 2^-24 and two steps of Newton's: 2^-50.
+// The hardware's 2^-24 and two steps of Newton's: 2^-50.  Of an infinity it is 0, which the steps would make NaN of (0 inf).
 __device__ __forceinline__ double inverse_root(double x) {
-  double r = __builtin_amdgcn_rsq(x);
+  const double r0 = __builtin_amdgcn_rsq(x);
+  double r = r0 * __builtin_fma(-0.5 * x * r0, r0, 1.5);
   r = r * __builtin_fma(-0.5 * x * r, r, 1.5);
-  return r * __builtin_fma(-0.5 * x * r, r, 1.5);
+  return x < INFINITY ? r : r0;
 }
 
 // What enters the residual: nothing (h = r), scale b, or b with its norm or gate.
