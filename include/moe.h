@@ -537,7 +537,8 @@ typedef struct moe_norm_desc {
 
 /* b, r, h, y: device [T, D]; gate: device float32 [T] or NULL; w, w_post: device [D]
  * (w_post or NULL); all aligned to their element (MOE_EALIGN).  h may be r (with ld_h =
- * ld_r); no other written buffer may overlap another buffer, what lies between its rows included (MOE_EINVAL,
+ * ld_r; b, the gate and the weights lie elsewhere then too); no other written buffer may overlap
+ * another buffer, what lies between its rows included (MOE_EINVAL,
  * as are null pointers but for those above, T < 0, D < 1, bad types and row strides below D).  D <= 16384 and strides below
  * 2^40 (MOE_EUNSUPPORTED).  Padding of rows is left as it was.  T = 0 is MOE_OK and touches nothing.
  * Asynchronous on `stream`; allocates nothing. */

@@ -647,16 +647,16 @@ Buffer weight_of(const moe_norm_desc& d, const void* p) {
   return {p, size_t(d.D) * es, es};
 }
 
-// Alignment of all, and written ones apart from all others but for the pair (same, as).
-int check_buffers(const Buffer* in, int n_in, const Buffer* out, int n_out, const void* same, const void* as) {
+// Alignment of all, and written ones apart from all others but for out[mine] over in[theirs], the same
+// rows (-1: none).
+int check_buffers(const Buffer* in, int n_in, const Buffer* out, int n_out, int mine, int theirs) {
   for (int i = 0; i < n_in; ++i)
     if (!aligned_to(in[i].p, in[i].align)) return MOE_EALIGN;
   for (int i = 0; i < n_out; ++i)
     if (!aligned_to(out[i].p, out[i].align)) return MOE_EALIGN;
   for (int i = 0; i < n_out; ++i) {
     for (int k = 0; k < n_in; ++k)
-      if (overlap(out[i].p, out[i].n, in[k].p, in[k].n) && !(out[i].p == same && in[k].p == as && same == as))
-        return MOE_EINVAL;
+      if (overlap(out[i].p, out[i].n, in[k].p, in[k].n) && !(i == mine && k == theirs)) return MOE_EINVAL;
     for (int k = 0; k < i; ++k)
       if (overlap(out[i].p, out[i].n, out[k].p, out[k].n)) return MOE_EINVAL;
   }
@@ -687,7 +687,7 @@ int moe_norm_fwd(const moe_norm_desc* d, const void* b, const void* r, const flo
                        {gate, size_t(d->T) * 4, 4}, weight_of(*d, w_post), weight_of(*d, w)};
   const Buffer out[] = {rows_of(*d, h, d->ld_h, d->res_type), rows_of(*d, y, d->ld_y, d->io_type)};
   const bool in_place = h == r && d->ld_h == d->ld_r;
-  if (const int rc = check_buffers(in, 5, out, 2, in_place ? h : nullptr, in_place ? r : nullptr)) return rc;
+  if (const int rc = check_buffers(in, 5, out, 2, in_place ? 0 : -1, 1)) return rc;
   NormArgs a{};
   a.b = b; a.r = r; a.w_post = w_post; a.w = w; a.gate = gate; a.h = h; a.y = y;
   a.ld_b = d->ld_b; a.ld_r = d->ld_r; a.ld_h = d->ld_h; a.ld_y = d->ld_y;
@@ -741,7 +741,7 @@ int moe_norm_bwd(const moe_norm_desc* d, const void* b, const void* h, const flo
                         {dgate, size_t(d->T) * 4, 4}, {dw_post, size_t(d->D) * 4, 4}, {dw, size_t(d->D) * 4, 4},
                         {scratch, need, 16}};
   const bool in_place = dr == dh && d->ld_r == d->ld_h;
-  if (const int rc = check_buffers(in, 7, out, 6, in_place ? dr : nullptr, in_place ? dh : nullptr)) return rc;
+  if (const int rc = check_buffers(in, 7, out, 6, in_place ? 1 : -1, 6)) return rc;
   if (scratch_bytes < need) return MOE_ESCRATCH;
   NormArgs a{};
   a.b = b; a.w_post = w_post; a.w = w; a.gate = gate; a.h = const_cast<void*>(h);
