@@ -409,7 +409,7 @@ typedef struct moe_gate_desc {
 
 /* Requires T >= 0, T*K < 2^31, groups >= 1 with E % groups == 0, 1 <= top_groups <= groups, 1 <= K
  * <= top_groups (E / groups), and the values above (else MOE_EINVAL); E <= 1024, K <= 64,
- * groups <= 64, T < 2^26 and row strides below 2^40 (else MOE_EUNSUPPORTED).  logits: device [T, E] of in_type, aligned to
+ * groups <= 64, T <= 2^26 - 4 and row strides below 2^40 (else MOE_EUNSUPPORTED).  logits: device [T, E] of in_type, aligned to
  * its element; bias: device float32 [E] or NULL (0); topk_idx: device int32 [T, K]
  * and topk_w: device float32 [T, K], written (the layout moe_fwd reads), apart from each other and
  * every input (MOE_EINVAL; a buffer of rows reaches from its first row's start to its last one's end, what

@@ -687,7 +687,7 @@ int check_gate(const moe_gate_desc* d) {
   if ((d->flags & ~(MOE_GATE_RENORM | MOE_GATE_ACCUMULATE)) != 0 || !std::isfinite(d->scale)) return MOE_EINVAL;
   if ((d->flags & MOE_GATE_ACCUMULATE) && d->in_type != MOE_TYPE_F32) return MOE_EINVAL;
   if (d->ld_logits < d->E || d->ld_dlogits < d->E) return MOE_EINVAL;
-  if (d->E > kGateMaxExperts || d->T >= (1 << 26) ||  // 64 lanes a token, below 2^32 threads
+  if (d->E > kGateMaxExperts || !launchable(ceil_div(d->T, kGateThreads / 64), kGateThreads) ||  // 64 lanes a token
       d->K > kGateMaxSlots || d->groups > kGateMaxGroups ||
       d->ld_logits >= (1LL << 40) || d->ld_dlogits >= (1LL << 40))
     return MOE_EUNSUPPORTED;

@@ -1,4 +1,4 @@
-"""Host-side limits of the block norms (moe_norm_*).  No call here reaches a kernel launch."""
+"""Host-side limits of the gate and the block norms (moe_gate_*, moe_norm_*).  No call here reaches a kernel launch."""
 from __future__ import annotations
 
 import ctypes
@@ -32,3 +32,14 @@ def test_norm_in_place_is_the_residual_alone():
             assert _norm_bwd(d, dr=_at(4), **{k: _at(4)}) == moe.MOE_EINVAL, (kw, k)
         assert _norm_bwd(d, dr=_at(4), wp=_at(4), dwp=_at(9)) == moe.MOE_EINVAL
         assert _norm_bwd(d, dr=_at(4), gate=_at(4), dgate=_at(9)) == moe.MOE_EINVAL
+
+
+def test_gate_tokens():
+    """2^24 workgroups of 256 threads are more than a launch counts: 2^26 - 4 tokens of 64 lanes are the most."""
+    for T in ((1 << 26) - 3, (1 << 26) - 1, 1 << 26):
+        for E, K in ((512, 8), (8, 2)):
+            d = moe.make_gate_desc(T, E, K)
+            assert moe.lib().moe_gate_fwd(ctypes.byref(d), _at(0), None, _at(1 << 20), _at(2 << 20), None) == moe.MOE_EUNSUPPORTED
+            assert moe.lib().moe_gate_bwd(ctypes.byref(d), _at(0), _at(1 << 20), _at(2 << 20), _at(3 << 20), None) == moe.MOE_EUNSUPPORTED
+    d = moe.make_gate_desc((1 << 26) - 4, 8, 2)  # refused for its alignment, not for its size
+    assert moe.lib().moe_gate_fwd(ctypes.byref(d), _at(0) + 2, None, _at(1 << 20), _at(2 << 20), None) == moe.MOE_EALIGN
