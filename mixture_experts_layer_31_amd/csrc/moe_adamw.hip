@@ -312,9 +312,15 @@ __device__ __forceinline__ void step_chunk(const AdamList& L, int i, uint32_t c,
 #pragma unroll
       for (int j = 0; j < N; ++j) r[j] = v[j] < 0x1p-126f ? sqrtf(v[j]) : r[j];
     }
+    float by[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      p[j] = __builtin_fmaf(p[j], shrink, -k.rate * (m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], k.root, k.eps))));
+    for (int j = 0; j < N; ++j) by[j] = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], k.root, k.eps));
+    if (k.eps < 0x1p-126f) {  // where v is 0 so is the denominator to the reciprocal, which would make 0 / eps NaN
+#pragma unroll
+      for (int j = 0; j < N; ++j) by[j] = m[j] / __builtin_fmaf(r[j], k.root, k.eps);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] = __builtin_fmaf(p[j], shrink, -k.rate * by[j]);
     if (!own) Piece<float, N>::template put<STREAM>(master + e, n, p);
     Piece<P, N>::template put<STREAM>(param + e, n, p);
     if constexpr (E4M3) {

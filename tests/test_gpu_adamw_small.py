@@ -1,4 +1,4 @@
-"""AdamW on the GPU where moments and scales leave fp32's normal numbers.
+"""AdamW on the GPU where moments, scales and eps leave fp32's normal numbers.
 
 States: the oracle's codes and scales, bit for bit (tests/test_gpu_adamw.py, whose bounds hold here too).
 """
@@ -74,3 +74,16 @@ def test_a_thousand_steps_without_a_gradient(master):
                 assert np.array_equal(got.cpu().numpy(), want), t
             assert torch.isfinite(p.p).all() and (not master or torch.isfinite(p.master).all())
     assert np.abs(m32).max() < 1e-40
+
+
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("eps", [1e-39, 1e-42, ULP])
+def test_an_eps_below_the_normal_numbers(eps, codes):
+    """A parameter that has never seen a gradient moves by its decay alone: 0 / eps is 0."""
+    g = torch.Generator().manual_seed(2)
+    ps = [ta.Param(g, n, t, F, False, codes, 1, 0.1, fresh=True, gstd=1e-2) for n, t in ((700, F), (300, B))]
+    for p in ps:
+        p.g[::3] = 0
+    for t in (1, 2):
+        ta._run(ps, t=t, eps=eps, name=f"eps={eps}")
+    assert all(torch.isfinite(p.p).all() for p in ps)
