@@ -509,9 +509,9 @@ def make_adamw_list(params, grads, m, v, masters=None, m_scales=None, v_scales=N
             raise ValueError("parameters and gradients are float32 or bfloat16, of one length")
         if w is not None and (p.dtype != torch.bfloat16 or w.dtype != torch.float32 or w.numel() != n):
             raise ValueError("a master is float32, beside a bfloat16 parameter of its length")
-        if any(x.numel() < n or x.dtype not in (codes if e4m3 else (torch.float32,)) for x in (a, b)):
+        if any(x is None or x.numel() < n or x.dtype not in (codes if e4m3 else (torch.float32,)) for x in (a, b)):
             raise ValueError("states have an element for each of the parameter's, float32 or codes")
-        if e4m3 and any(x.dtype != torch.float32 or x.numel() < (n + 127) // 128 for x in (sa, sb)):
+        if e4m3 and any(x is None or x.dtype != torch.float32 or x.numel() < (n + 127) // 128 for x in (sa, sb)):
             raise ValueError("codes have a float32 scale for each 128")
         own = [x for x in (p, w, g, a, b, sa, sb) if x is not None]
         if not all(x.is_cuda and x.device == params[0].device and x.is_contiguous() for x in own):

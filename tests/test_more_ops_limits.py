@@ -1,7 +1,10 @@
-"""Host-side limits of the gate and the block norms (moe_gate_*, moe_norm_*).  No call here reaches a kernel launch."""
+"""Host-side limits of the gate, the block norms and AdamW (moe_gate_*, moe_norm_*, moe_adamw).  No call here reaches a kernel launch."""
 from __future__ import annotations
 
 import ctypes
+
+import pytest
+import torch
 
 import mixture_experts_layer_31_amd as moe
 
@@ -43,3 +46,13 @@ def test_gate_tokens():
             assert moe.lib().moe_gate_bwd(ctypes.byref(d), _at(0), _at(1 << 20), _at(2 << 20), _at(3 << 20), None) == moe.MOE_EUNSUPPORTED
     d = moe.make_gate_desc((1 << 26) - 4, 8, 2)  # refused for its alignment, not for its size
     assert moe.lib().moe_gate_fwd(ctypes.byref(d), _at(0) + 2, None, _at(1 << 20), _at(2 << 20), None) == moe.MOE_EALIGN
+
+
+def test_adamw_list_without_states():
+    """A state or a scale that is missing is refused as a gradient is."""
+    x = torch.zeros(200)
+    u8 = torch.zeros(200, dtype=torch.uint8)
+    for args in (dict(m=[None], v=[x]), dict(m=[x], v=[None]), dict(m=[u8], v=[u8], m_scales=[None], v_scales=[x]),
+                 dict(m=[u8], v=[u8], m_scales=[x], v_scales=[None])):
+        with pytest.raises(ValueError):
+            moe.make_adamw_list([x], [x], **args)
