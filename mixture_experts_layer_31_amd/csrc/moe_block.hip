@@ -59,6 +59,26 @@ struct Quant {
   __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
     return pack_e4m3x4(quotient(a), quotient(b), quotient(c), quotient(d));
   }
+  // Values of type T whose quotients may pass 448, where the conversion would give NaN, as those that saturate: a scale of a
+  // few of the smallest numbers is rounded by up to half.  Above 2^9 of them quotients are 448.5 at most, and bf16's
+  // smallest number has a scale of 146.
+  template <class T, int N>
+  __device__ __forceinline__ void saturate(float (&x)[N]) const {
+    if (sizeof(T) == 4 && __ballot(scale < 0x1p-140f) != 0) {
+      const float top = scale < 0x1p-140f ? 448.f * scale : INFINITY;
+#pragma unroll
+      for (int i = 0; i < N; ++i)  // a NaN stays
+        x[i] = __builtin_elementwise_minimum(__builtin_elementwise_maximum(x[i], -top), top);
+    }
+  }
+  template <class T>
+  __device__ __forceinline__ uint2 codes8(const float (&v)[8]) const {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+    saturate<T>(x);
+    return make_uint2(codes(x[0], x[1], x[2], x[3]), codes(x[4], x[5], x[6], x[7]));
+  }
 };
 
 struct QuantArgs {
@@ -160,8 +180,7 @@ __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
     for (int it = 0; it < 8; ++it) {
       const int64_t r = r0 + it * 16 + rw;
       const Quant qz(BLOCK ? amax : max16(amax8(v[it])));
-      const uint2 w = make_uint2(qz.codes(v[it][0], v[it][1], v[it][2], v[it][3]),
-                                 qz.codes(v[it][4], v[it][5], v[it][6], v[it][7]));
+      const uint2 w = qz.codes8<T>(v[it]);
       if (p.q != nullptr && r < p.rows && c0 + 8 * l16 < cols16) {
         *reinterpret_cast<uint2*>(p.q + r * p.ldq + c0 + 8 * l16) = w;
         if (!BLOCK && l16 == 0) p.sc[int64_t(ct) * p.rows + r] = qz.scale;
@@ -229,6 +248,7 @@ __global__ void __launch_bounds__(256) block_quant_kernel(QuantArgs p) {
   amax = fmaxf(amax, __shfl_xor(amax, 32, 64));
   const Quant qz(amax);
   if (h == 0 && c0 + q < p.cols) p.sct[int64_t(rt) * p.cols + c0 + q] = qz.scale;
+  qz.saturate<T>(u);
   uint4 w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -281,7 +301,7 @@ __global__ void __launch_bounds__(256) block_quant_rows_kernel(QuantArgs p) {
       as_floats<T>(raw[it][i].v, v + i * N);
     }
     const Quant qz(max16(amax8(v)));
-    const uint2 w = make_uint2(qz.codes(v[0], v[1], v[2], v[3]), qz.codes(v[4], v[5], v[6], v[7]));
+    const uint2 w = qz.codes8<T>(v);
     if (r < p.rows && c < cols16) {
       *reinterpret_cast<uint2*>(p.q + r * p.ldq + c) = w;
       if (l16 == 0) p.sc[int64_t(ct) * p.rows + r] = qz.scale;
@@ -1147,7 +1167,7 @@ __global__ void __launch_bounds__(64 * kDirectWaves) block_direct_kernel(DirectA
           as_floats<T>(raw[h][i].v, f + i * N);
         }
         const Quant qz(max16(amax8(f)));
-        const uint2 w = make_uint2(qz.codes(f[0], f[1], f[2], f[3]), qz.codes(f[4], f[5], f[6], f[7]));
+        const uint2 w = qz.codes8<T>(f);
         if (r < rows) {
           *reinterpret_cast<uint2*>(smem + r * LDA + kt * 128 + 8 * l16) = w;
           if (l16 == 0) scales[kt * 16 + r] = qz.scale;

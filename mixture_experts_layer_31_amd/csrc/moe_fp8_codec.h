@@ -17,7 +17,8 @@ __device__ __forceinline__ int e8m0_exponent(float amax) {
 }
 
 // Four OCP e4m3 codes (byte k = code of value k) by the hardware conversion:
-// nearest value, ties to even mantissa, magnitudes >= 448 saturate to 448
+// nearest value, ties to even mantissa; magnitudes to 464, the border above 448,
+// give 448 and larger ones NaN, so that who can have those saturates first
 // (checked against a software encoder of that rule with an in-bounds probe
 // over every code, every rounding midpoint and its neighbours, and 4e5 random
 // values).
