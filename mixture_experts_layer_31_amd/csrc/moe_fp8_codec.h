@@ -36,6 +36,8 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 // is in the subnormal e4m3 range (below 2^-6).  Only then is the division
 // done, behind a wave-uniform branch that is skipped unless some lane needs
 // it (a per-element select would make every element pay for the division).
+// Where sc is so small that rc is infinite (bf16 values below 2^-119) a factor of
+// 1 in its place leaves every product but 0 below 2^-6, so that all are divided.
 __device__ __forceinline__ bool near_e4m3_midpoint(float y) {
   const float a = fabsf(y);
   const int d = int(__float_as_uint(a) & 0xFFFFFu) - 0x80000;
@@ -44,6 +46,7 @@ __device__ __forceinline__ bool near_e4m3_midpoint(float y) {
 
 template <int N>
 __device__ __forceinline__ void block_quotients(const float* x, float sc, float rc, float (&y)[N]) {
+  if (!(rc < INFINITY)) rc = 1.f;
   bool any = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
