@@ -2,8 +2,9 @@
 // run of 128 (moe_adamw in moe.h).
 //
 // Bound by memory: a bf16 parameter with its master, fp32 states and a bf16 gradient
-// move 28 bytes an element, a bf16 parameter with e4m3 states 10.  75.5 M elements of the first kind 356 us (5.9 TB/s),
-// 604 M of the second 1007 (6.1); 200 000 with fp32 states 6 us (a launch).
+// move 28 bytes an element, a bf16 parameter with e4m3 states 10.  75.5 M elements of the first kind 357 us (5.9 TB/s),
+// 604 M of the second 1020 (6.0; 990 to 1050 a call, and 1030 to 1150 in the first twenty after a pause); 200 000 with fp32
+// states 6 us (a launch).
 //
 // The list travels in the kernel arguments (kMaxAdam entries a launch), so nothing is
 // copied to the device and a captured graph holds its own list.  A tensor is cut into chunks

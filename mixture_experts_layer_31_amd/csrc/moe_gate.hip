@@ -5,14 +5,17 @@
 // The choice goes by c = fl32(s + bias) of scores in 64 bits, so that the rounding to fp32 decides which
 // of two neighbours comes first and not the error of an fp32 exp.  64-bit scores of every logit cost more than
 // the memory does (65536 tokens of 256 experts in groups: 63 us, where the logits take 11), so a wave first chooses by
-// fp32 scores in fixed point (32 us) and then looks whether any two choices that matter lie within their error bound of
+// fp32 scores in fixed point (31 us) and then looks whether any two choices that matter lie within their error bound of
 // each other: the K chosen ones and the next, and the groups at the border.  Only then (a row in a few hundred, rows
 // with equal scores, masked groups, scores past the numbers) it chooses again by 64-bit ones.
 //
-// Forward is bound by the vector ALU: some 700 instructions for four tokens of 256 experts, of which the scores are a
-// third, the sort and the K + 1 maxima another; 88% of its cycles issue one.  At 16384 x 128 it takes 6.7 us, at one
-// token 3.0 (a launch).  Backward moves a row of zeros for K gathered logits and is bound by memory: 15.5 us for 65536 x 256
-// fp32 (67 MB written, the gathers touch half of the logits' lines), 5.1 for 16384 x 128.
+// Forward is bound by the vector ALU: 768 instructions for four tokens of 256 experts in groups, of which the scores are a
+// third, the sort and the K + 1 maxima another.  Counted at 65536 tokens (31 us) they take 52000 of the 54000 cycles in which a
+// SIMD's waves run, some 25 us; the rest is the launch's start and end (2^20 tokens take 362 us, 22.6 for each 65536).  At
+// 16384 x 128 it takes 6.5 us, at one token 2.7 (a launch).  Where every third expert is masked by -inf, in the bias or the
+// logits, all rows are chosen again: 79 and 76 us for 65536 x 256.  Backward moves a
+// row of zeros for K gathered logits and is bound by memory: 15.4 us for 65536 x 256 fp32 (67 MB written, the gathers touch
+// half of the logits' lines), 4.9 for 16384 x 128.
 //
 // LPT lanes share a token (the rules and both sides measured are at the entry points), each with VPL of its experts in runs of four; with groups, each
 // group has LPT / GP of the lanes (GP the power of two from the number of groups).
@@ -447,7 +450,8 @@ __device__ __forceinline__ void choose_exactly(const GateArgs& a, const Share<LP
     }
     sum = token_sum<LPT>(sum);
     const double inv = sum == 0. ? 0. : 1. / sum;
-    // of weights that are not renormalised choose_fixed's stays: a token's do not depend on its neighbours in the wave
+    // of weights that are not renormalised choose_fixed's stays: a token's do not depend on its neighbours in the wave.  That
+    // sum is fp32, of the hardware's exp: one of 64-bit exps of every logit is what the first choice is there to spare.
     if (a.renorm || !(inv_sum > 0.f && inv_sum < INFINITY)) inv_sum = sum == 0. ? INFINITY : float(inv);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] *= inv;

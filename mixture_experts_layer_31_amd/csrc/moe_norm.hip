@@ -3,19 +3,20 @@
 //
 // Both are bound by memory: four arrays of rows forward (b, r in, h, y out), six
 // backward (b, h, dy, dh in, db, dr out; without gate and w_post no b).  16384 x 2048 bf16: 48 us forward (5.6 TB/s),
-// 58 backward (5.8) and 5 for the second launch; 16384 x 4096 with an fp32 residual, gate and both norms 146 (5.5) and
-// 233 (5.2); a row by itself 2.3.  A row stays in the registers of its TPR threads (16 of them for up to 128
+// 56 backward (6.0) and 5 for the second launch; 16384 x 4096 with an fp32 residual, gate and both norms 140 (5.8) and
+// 218 (5.5); a row by itself 2.3.  A row stays in the registers of its TPR threads (16 of them for up to 128
 // values, 512 for 4096), eight or four neighbouring values a thread and piece: it is read once, its sums are joined over
 // the lanes and, past one wave, through LDS, and what depends on them is computed from the
 // registers.  The weights of a lane's columns stay in registers over the rows that a workgroup takes,
 // and so do its parts of dw and dw_post, which go to the scratch as one row a workgroup; a second launch
 // adds those rows in their order.  Rows past 8192 columns take 1024 threads, of 128 registers each, and spill with
-// w_post (4096 x 16384: 238 us forward and backward, with w_post 735); there no row is loaded ahead (with one 326 and 1153).
+// w_post (4096 x 16384: 235 us forward and backward, with w_post 733); there no row is loaded ahead (with one 326 and 1153).
 //
 // Sums.  With e = w dy, q = 1 / rms(h): dh' = q (e - h q^2 mean(e h)), so sum h^2, sum e h and sum b^2 are
 // joined together; only sum g w_post b, of the finished gradient g, needs a second join.
 // h with a gate or w_post is computed in 64 bits where it is kept in bf16: there a value next to a border goes one
-// way or the other, and an fp32 sum of squares would decide that for one value in 2^15.
+// way or the other, and an fp32 sum of squares would decide that for one value in 2^15.  An fp32 residual is computed in
+// fp32: its own rounding is of the size of the sum's, and 64-bit values of a row need twice the registers.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
